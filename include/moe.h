@@ -327,6 +327,106 @@ MOE_API moe_status_t moe_layer_forward_fp8(const moe_config_t* cfg, const void* 
                                            void* h_shared_out, int32_t* perm_out, void* ws, size_t ws_bytes,
                                            moe_stream_t stream);
 
+/* moe_layer_forward_fp8 for tokens that come with their E4M3 codes, as moe_add_rmsnorm
+ * writes them: x_codes [T, d] uint8 (16-byte aligned) and x_scales [T] fp32 are the rows
+ * that the routed and shared experts multiply (moved to segment order as they are, no
+ * second quantization), x [T, d] bf16 is what the router reads. With the codes and
+ * scales that moe_quantize_e4m3 makes of x the outputs equal moe_layer_forward_fp8's.
+ * Everything else as there. */
+MOE_API moe_status_t moe_layer_forward_fp8_codes(const moe_config_t* cfg, const void* x, const uint8_t* x_codes,
+                                                 const float* x_scales, const void* w_router, const float* bias,
+                                                 const moe_fp8_experts_t* wq, void* out, float* logits_out,
+                                                 int32_t* topk_idx_out, float* topk_w_out, int32_t* counts_out,
+                                                 moe_lis_t* lis_out, void* h_out, void* h_shared_out,
+                                                 int32_t* perm_out, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Residual addition, root-mean-square norm and 8-bit output, the entry of a block that
+ * ends in the layer, in one pass over `rows` rows of d elements (no counterpart in the
+ * reviewed pages: the layer's input is their starting point):
+ *   r = x + residual (residual may be NULL: r = x);
+ *   y = r / sqrt(mean(r^2) + eps) * weight;
+ *   sum_out (nullable) = r, y (nullable) = y, both rounded to `dtype`;
+ *   codes, scales (nullable, both or neither) = E4M3 codes [rows, d] and fp32 scales
+ *   [rows] of y in moe_quantize_e4m3's format, taken from the fp32 y (not from its
+ *   rounding to bf16). r and y are fp32 in between.
+ * x, residual, sum_out, y [rows, d] and weight [d] are `dtype` (moe_dtype_t), contiguous
+ * and 16-byte aligned; scales 4-byte aligned. sum_out and y may be x or residual
+ * themselves (not each other, and no partial overlap). At least one of y and codes is
+ * given. eps >= 0 and finite; a row of zeros with eps = 0 gives NaN, as the formula does.
+ * rows >= 0 (0: nothing is launched); d a multiple of 8 (of 16 with codes) up to 32768
+ * (MOE_ERR_UNSUPPORTED otherwise). No workspace. Asynchronous on `stream`. */
+MOE_API moe_status_t moe_add_rmsnorm(int64_t rows, int32_t d, int32_t dtype, float eps, const void* x,
+                                     const void* residual, const void* weight, void* sum_out, void* y,
+                                     uint8_t* codes, float* scales, moe_stream_t stream);
+
+/* 4-bit expert weights by plain rounding. (The reviewed pages' formats below 8 bits need
+ * calibrated or learned parts; this one needs the weights alone.) A row of K weights is cut into groups of `group` = 32, 64 or 128
+ * columns (the last may be shorter). A group's scale is max |v| / 7 rounded to 5
+ * significant bits, nearest, ties to even (1 where that is below 2^-126); a code is
+ * v / scale rounded to the nearest whole number, ties to even (-7 .. 7; -8 is valid on
+ * input); the weight that a code stands for is code * scale, which for these scales is
+ * exactly a bf16 number.
+ *   codes  [n, rows, cols / 2] uint8: a row is a sequence of little-endian 32-bit words
+ *          of 8 columns; column 2i of a word is held as code + 8 in bits 4i .. 4i+3 and
+ *          column 2i + 1 in bits 16+4i .. 19+4i (i = 0 .. 3);
+ *   scales [n, ceil(cols / group), rows] bf16.
+ *
+ * moe_quantize_w4: src [n, rows, cols] bf16 -> codes and scales. moe_dequantize_w4: dst
+ * [n, rows, cols] bf16 = code * scale (rounded to bf16 where a scale of another origin
+ * has more than 5 significant bits). All pointers on the device and 16-byte aligned;
+ * rows a multiple of 8 and at most 2^21 - 32, cols a multiple of 32, n at most 65535
+ * (MOE_ERR_UNSUPPORTED otherwise); n = 0 or rows = 0 launches nothing. Infinities and
+ * NaN have no representation: a group that holds one gets unspecified codes.
+ * Asynchronous on `stream`. */
+MOE_API moe_status_t moe_quantize_w4(int64_t n, int64_t rows, int64_t cols, int32_t group, const void* src,
+                                     uint8_t* codes, void* scales, moe_stream_t stream);
+MOE_API moe_status_t moe_dequantize_w4(int64_t n, int64_t rows, int64_t cols, int32_t group, const uint8_t* codes,
+                                       const void* scales, void* dst, moe_stream_t stream);
+
+/* 4-bit expert weights of a layer, each matrix in moe_quantize_w4's format with one
+ * common group. Device pointers, 16-byte aligned; scales bf16.
+ *   gate, up  [m, f, d / 2] codes, scales [m, ceil(d / group), f]  (up: SwiGLU only)
+ *   down      [m, d, f / 2] codes, scales [m, ceil(f / group), d]
+ *   sh_gate, sh_up [n_shared, f_shared, d / 2], scales [n_shared, ceil(d / group), f_shared]
+ *   sh_down   [n_shared, d, f_shared / 2], scales [n_shared, ceil(f_shared / group), d]
+ * (sh_*: only with n_shared > 0; unused entries may be NULL). */
+typedef struct {
+  int32_t group;
+  const uint8_t* gate;
+  const void* gate_scale;
+  const uint8_t* up;
+  const void* up_scale;
+  const uint8_t* down;
+  const void* down_scale;
+  const uint8_t* sh_gate;
+  const void* sh_gate_scale;
+  const uint8_t* sh_up;
+  const void* sh_up_scale;
+  const uint8_t* sh_down;
+  const void* sh_down_scale;
+} moe_w4_experts_t;
+
+/* Workspace of moe_grouped_ffn_w4 and moe_layer_forward_w4 (host out-parameter). bf16
+ * layers with d, f and f_shared multiples of 32 only (MOE_ERR_UNSUPPORTED otherwise). */
+MOE_API moe_status_t moe_w4_workspace_size(const moe_config_t* cfg, size_t* bytes);
+
+/* moe_grouped_ffn with 4-bit experts: same segments, task weights and fp32 y_perm; only
+ * the routed matrices of wq are read. Activations stay bf16 (the hidden activation h is
+ * rounded to bf16 between the two products), sums are fp32. */
+MOE_API moe_status_t moe_grouped_ffn_w4(const moe_config_t* cfg, const void* x_perm, const int32_t* offsets,
+                                        const moe_w4_experts_t* wq, const float* task_w, const int32_t* perm,
+                                        float* y_perm, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* moe_layer_forward with 4-bit experts, routed and shared. The router is the bf16
+ * layer's (same logits, top-k and gate weights, same histogram, LIS and permutation).
+ * Optional outputs as in moe_layer_forward. ws: moe_w4_workspace_size() bytes, 256-byte
+ * aligned. Stage events (moe_set_stage_events) as in moe_layer_forward. */
+MOE_API moe_status_t moe_layer_forward_w4(const moe_config_t* cfg, const void* x, const void* w_router,
+                                          const float* bias, const moe_w4_experts_t* wq, void* out,
+                                          float* logits_out, int32_t* topk_idx_out, float* topk_w_out,
+                                          int32_t* counts_out, moe_lis_t* lis_out, void* ws, size_t ws_bytes,
+                                          moe_stream_t stream);
+
 /* Cartesian Product Router (OmniMoE Sec. 2.2, Eq. 8; App. A): lr = log_softmax(x
  * w_row^T), lc = log_softmax(x w_col^T) (fp32); expert (i, j) with flat id
  * i Nc + j scores S = fl32(lr_i + lc_j); idx_out [T, K] = the exact top-K of all

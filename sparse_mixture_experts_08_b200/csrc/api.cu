@@ -8,6 +8,7 @@
 #include <initializer_list>
 
 #include "atomic.cuh"
+#include "w4.cuh"
 
 namespace moe {
 
@@ -267,6 +268,11 @@ struct Fp8Io {
   float* sx_sh;    // [T]
   uint8_t* hq_sh;  // [n_shared T, f_shared]
   float* sh_sh;    // [n_shared T]
+  // codes and scales of x that came with the call (nullable: x is quantized here), and
+  // where each task's row goes
+  const uint8_t* x_codes;   // [T, d]
+  const float* x_scales;    // [T]
+  const int32_t* inv_perm;  // [T k]
 };
 
 static int kblocks8(int K) { return (K + 127) / 128; }
@@ -293,6 +299,7 @@ struct FfnIo {
   void* h_sh;             // [n_shared T, f_shared]
   float* y_sh;            // [n_shared T, d]
   const Fp8Io* q8;        // 8-bit experts (nullable)
+  const moe_w4_experts_t* w4;  // 4-bit experts (nullable)
 };
 
 static void fill_common(GemmParams& p, int* status) {
@@ -300,13 +307,70 @@ static void fill_common(GemmParams& p, int* status) {
   p.wait_limit_ns = g_wait_limit_ns;
 }
 
+// The two products with 4-bit expert weights (routed and shared classes in one launch
+// each); the down projection is not split over K.
+static moe_status_t run_ffn_w4(const moe_config_t& c, const FfnIo& io, int* status, cudaStream_t s,
+                               bool stage_marks) {
+  const moe_w4_experts_t& w = *io.w4;
+  const bool swiglu = c.act == MOE_SWIGLU;
+  using bf = __nv_bfloat16;
+  W4Params p;
+  std::memset(&p, 0, sizeof(p));
+  p.group = w.group;
+  p.status = status;
+  p.wait_limit_ns = g_wait_limit_ns;
+  for (int down = 0; down < 2; ++down) {
+    int n = 0;
+    if (io.n_routed > 0) {
+      W4Class& g = p.cls[n++];
+      g.n_groups = io.n_routed;
+      g.R = down ? c.d : c.f;
+      g.K = down ? c.f : c.d;
+      g.seg_off = io.offsets;
+      g.max_row = (int)io.routed_rows;
+      g.b = (const bf*)(down ? io.h : io.x_perm);
+      g.b_rows = io.routed_rows;
+      g.out = down ? (void*)io.y : io.h;
+      g.a0 = down ? W4Matrix{w.down, (const bf*)w.down_scale} : W4Matrix{w.gate, (const bf*)w.gate_scale};
+      g.a1 = W4Matrix{w.up, (const bf*)w.up_scale};
+      g.row_w = io.row_w;
+      g.task_w = io.task_w;
+      g.perm = io.perm;
+    }
+    if (io.n_shared > 0) {
+      W4Class& g = p.cls[n++];
+      std::memset(&g, 0, sizeof(g));
+      g.n_groups = io.n_shared;
+      g.R = down ? c.d : c.f_shared;
+      g.K = down ? c.f_shared : c.d;
+      g.const_rows = c.T;
+      g.b_group_stride = down ? c.T : 0;
+      g.out_group_stride = c.T;
+      g.b = (const bf*)(down ? io.h_sh : io.x);
+      g.b_rows = down ? (long long)io.n_shared * c.T : c.T;
+      g.out = down ? (void*)io.y_sh : io.h_sh;
+      g.a0 = down ? W4Matrix{w.sh_down, (const bf*)w.sh_down_scale} : W4Matrix{w.sh_gate, (const bf*)w.sh_gate_scale};
+      g.a1 = W4Matrix{w.sh_up, (const bf*)w.sh_up_scale};
+    }
+    p.n_classes = n;
+    const int epi = down ? EPI_DOWN : swiglu ? EPI_SWIGLU : EPI_RELU;
+    MOE_CUDA(launch_w4_gemm(epi, p, c.T, (double)c.T * c.k / c.m, s));
+    if (!down && stage_marks) MOE_TRY(mark_stage(5, s));
+  }
+  return MOE_OK;
+}
+
 static moe_status_t run_ffn(const moe_config_t& c, const Plan& pl, const FfnIo& io, int ksplit, int kbps, int* status,
                             cudaStream_t s, bool stage_marks = false) {
+  if (io.w4) return run_ffn_w4(c, io, status, s, stage_marks);
   const bool swiglu = c.act == MOE_SWIGLU;
   const bool tc = c.dtype == MOE_BF16;
   const Fp8Io* q8 = io.q8;
   auto kbl = [&](int K) { return q8 ? kblocks8(K) : kblocks(K); };
-  if (q8) {  // E4M3 rows of the up projection's inputs
+  if (q8 && q8->x_codes) {  // codes that came with x: moved to segment order (two codes as one 16-bit element)
+    MOE_CUDA(launch_permute_rows(MOE_BF16, (int)io.routed_rows, c.k, c.d / 2, q8->x_codes, q8->inv_perm, q8->xq, s));
+    MOE_CUDA(launch_permute_scales((int)io.routed_rows, c.k, q8->x_scales, q8->inv_perm, q8->sx, s));
+  } else if (q8) {  // E4M3 rows of the up projection's inputs
     MOE_CUDA(launch_quantize_e4m3(io.routed_rows, c.d, io.x_perm, c.d, q8->xq, c.d, q8->sx, s));
     if (io.n_shared > 0) MOE_CUDA(launch_quantize_e4m3(c.T, c.d, io.x, c.d, q8->xq_sh, c.d, q8->sx_sh, s));
   }
@@ -371,10 +435,10 @@ static moe_status_t run_ffn(const moe_config_t& c, const Plan& pl, const FfnIo& 
     if (q8) {
       mu.a0[ncls].ptr = q8->w->sh_gate;
       mu.a1[ncls].ptr = swiglu ? q8->w->sh_up : q8->w->sh_gate;
-      mu.b[ncls].ptr = q8->xq_sh;
+      mu.b[ncls].ptr = q8->x_codes ? q8->x_codes : q8->xq_sh;
       g.a0_scale = q8->w->sh_gate_scale;
       g.a1_scale = swiglu ? q8->w->sh_up_scale : nullptr;
-      g.b_scale = q8->sx_sh;
+      g.b_scale = q8->x_codes ? q8->x_scales : q8->sx_sh;
     }
     ++ncls;
   }
@@ -650,14 +714,17 @@ static Fp8Layout make_fp8_layout(const moe_config_t& c, size_t base) {
 }
 
 // Route -> histogram/LIS -> permute -> expert FFN -> combine; the expert weights
-// are bf16 (w_gate ...) or, with wq, E4M3 codes and scales.
+// are bf16 (w_gate ...) or, with wq, E4M3 codes and scales (x_codes and x_scales: of x
+// too) or, with w4, 4-bit codes and group scales.
 static moe_status_t layer_forward_impl(const moe_config_t& c, const void* x, const void* w_router, const float* bias,
                                        const void* w_gate, const void* w_up, const void* w_down, const void* ws_gate,
                                        const void* ws_up, const void* ws_down, const moe_fp8_experts_t* wq, void* out,
                                        float* logits_out, int32_t* topk_idx_out, float* topk_w_out,
                                        int32_t* counts_out, moe_lis_t* lis_out, void* h_out, void* h_shared_out,
                                        int32_t* perm_out, int32_t* offsets_out, int32_t* inv_perm_out,
-                                       void* x_perm_out, void* ws, cudaStream_t s) {
+                                       void* x_perm_out, void* ws, cudaStream_t s,
+                                       const moe_w4_experts_t* w4 = nullptr, const uint8_t* x_codes = nullptr,
+                                       const float* x_scales = nullptr) {
   const Plan pl = make_plan(c);
   const Layout L = make_layout(c, pl);
   int* status = at<int>(ws, L.status);
@@ -690,11 +757,13 @@ static moe_status_t layer_forward_impl(const moe_config_t& c, const void* x, con
     MOE_CUDA(launch_route_index(1, c.T, c.k, c.m, idx, counts, offsets, lis, start, status, s));
     MOE_CUDA(launch_rank(c.T, c.k, c.m, idx, offsets, start, w, perm, inv_perm, w_perm, status, s));
     MOE_TRY(mark_stage(3, s));
-    MOE_CUDA(launch_permute_rows(c.dtype, (int)Tk, c.k, c.d, x, inv_perm, at<void>(ws, L.x_perm), s));
+    if (!x_codes)  // (given codes are moved instead, in run_ffn)
+      MOE_CUDA(launch_permute_rows(c.dtype, (int)Tk, c.k, c.d, x, inv_perm, at<void>(ws, L.x_perm), s));
   }
   MOE_TRY(mark_stage(4, s));
   FfnIo io;
   std::memset(&io, 0, sizeof(io));
+  io.w4 = w4;
   io.n_routed = c.m;
   io.offsets = offsets;
   io.x_perm = at<void>(ws, L.x_perm);
@@ -716,13 +785,14 @@ static moe_status_t layer_forward_impl(const moe_config_t& c, const void* x, con
   io.y_sh = at<float>(ws, L.y_sh);
   // K split of the down projection: the plan's, re-cut into 128-element k-blocks
   // for 8-bit operands (never more splits than the plan sized y for)
-  int ksplit = pl.ksplit, kbps = pl.kbps;
+  int ksplit = w4 ? 1 : pl.ksplit, kbps = pl.kbps;
   Fp8Io q8;
   if (wq) {
     const Fp8Layout F = make_fp8_layout(c, L.total);
     q8 = {wq,
           at<uint8_t>(ws, F.xq), at<float>(ws, F.sx), at<uint8_t>(ws, F.hq), at<float>(ws, F.sh),
-          at<uint8_t>(ws, F.xq_sh), at<float>(ws, F.sx_sh), at<uint8_t>(ws, F.hq_sh), at<float>(ws, F.sh_sh)};
+          at<uint8_t>(ws, F.xq_sh), at<float>(ws, F.sx_sh), at<uint8_t>(ws, F.hq_sh), at<float>(ws, F.sh_sh),
+          x_codes, x_scales, inv_perm};
     io.q8 = &q8;
     const int kb = kblocks8(c.f);
     const int ks = std::min(pl.ksplit, kb);
@@ -732,7 +802,7 @@ static moe_status_t layer_forward_impl(const moe_config_t& c, const void* x, con
   // Top-1 routing without shared experts: each token has exactly one weighted
   // expert output, so the down projection's epilogue scatters it straight into
   // `out` and the combine kernel (and the fp32 y_perm round trip) disappears.
-  const bool fuse_combine = c.k == 1 && c.n_shared == 0 && ksplit == 1 && c.dtype == MOE_BF16;
+  const bool fuse_combine = c.k == 1 && c.n_shared == 0 && ksplit == 1 && c.dtype == MOE_BF16 && !w4;
   io.out_k1 = fuse_combine ? out : nullptr;
   MOE_TRY(run_ffn(c, pl, io, ksplit, kbps, status, s, true));
   MOE_TRY(mark_stage(6, s));
@@ -804,11 +874,12 @@ moe_status_t moe_quantize_e4m3(int64_t rows, int64_t cols, const void* src, uint
   return cuda_status(launch_quantize_e4m3(rows, (int)cols, src, cols, codes, cols, scales, (cudaStream_t)stream));
 }
 
-moe_status_t moe_layer_forward_fp8(const moe_config_t* cfg, const void* x, const void* w_router, const float* bias,
-                                   const moe_fp8_experts_t* wq, void* out, float* logits_out, int32_t* topk_idx_out,
-                                   float* topk_w_out, int32_t* counts_out, moe_lis_t* lis_out, void* h_out,
-                                   void* h_shared_out, int32_t* perm_out, void* ws, size_t ws_bytes,
-                                   moe_stream_t stream) {
+static moe_status_t layer_forward_fp8(const moe_config_t* cfg, const void* x, const uint8_t* x_codes,
+                                      const float* x_scales, const void* w_router, const float* bias,
+                                      const moe_fp8_experts_t* wq, void* out, float* logits_out,
+                                      int32_t* topk_idx_out, float* topk_w_out, int32_t* counts_out,
+                                      moe_lis_t* lis_out, void* h_out, void* h_shared_out, int32_t* perm_out,
+                                      void* ws, size_t ws_bytes, moe_stream_t stream) {
   MOE_TRY(check_fp8_cfg(cfg));
   const moe_config_t& c = *cfg;
   const bool swiglu = c.act == MOE_SWIGLU;
@@ -821,9 +892,9 @@ moe_status_t moe_layer_forward_fp8(const moe_config_t* cfg, const void* x, const
   for (const void* p : std::initializer_list<const void*>{x, w_router, (const void*)bias, out, (const void*)logits_out,
                         (const void*)topk_idx_out, (const void*)topk_w_out, (const void*)counts_out,
                         (const void*)lis_out, wq->gate, wq->up, wq->down, wq->sh_gate, wq->sh_up, wq->sh_down,
-                        h_out, h_shared_out, (const void*)perm_out})
+                        h_out, h_shared_out, (const void*)perm_out, (const void*)x_codes})
     if (p && !aligned16(p)) return MOE_ERR_INVALID_ARG;
-  for (const float* p : {wq->gate_scale, wq->up_scale, wq->down_scale, wq->sh_gate_scale, wq->sh_up_scale,
+  for (const float* p : {x_scales, wq->gate_scale, wq->up_scale, wq->down_scale, wq->sh_gate_scale, wq->sh_up_scale,
                          wq->sh_down_scale})
     if (p && ((uintptr_t)p & 3u)) return MOE_ERR_INVALID_ARG;
   size_t need = 0;
@@ -832,8 +903,154 @@ moe_status_t moe_layer_forward_fp8(const moe_config_t* cfg, const void* x, const
   MOE_TRY(check_device());
   return layer_forward_impl(c, x, w_router, bias, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, wq, out,
                             logits_out, topk_idx_out, topk_w_out, counts_out, lis_out, h_out, h_shared_out, perm_out,
-                            nullptr, nullptr, nullptr, ws, (cudaStream_t)stream);
+                            nullptr, nullptr, nullptr, ws, (cudaStream_t)stream, nullptr, x_codes, x_scales);
 }
+
+moe_status_t moe_layer_forward_fp8(const moe_config_t* cfg, const void* x, const void* w_router, const float* bias,
+                                   const moe_fp8_experts_t* wq, void* out, float* logits_out, int32_t* topk_idx_out,
+                                   float* topk_w_out, int32_t* counts_out, moe_lis_t* lis_out, void* h_out,
+                                   void* h_shared_out, int32_t* perm_out, void* ws, size_t ws_bytes,
+                                   moe_stream_t stream) {
+  return layer_forward_fp8(cfg, x, nullptr, nullptr, w_router, bias, wq, out, logits_out, topk_idx_out, topk_w_out,
+                           counts_out, lis_out, h_out, h_shared_out, perm_out, ws, ws_bytes, stream);
+}
+
+moe_status_t moe_layer_forward_fp8_codes(const moe_config_t* cfg, const void* x, const uint8_t* x_codes,
+                                         const float* x_scales, const void* w_router, const float* bias,
+                                         const moe_fp8_experts_t* wq, void* out, float* logits_out,
+                                         int32_t* topk_idx_out, float* topk_w_out, int32_t* counts_out,
+                                         moe_lis_t* lis_out, void* h_out, void* h_shared_out, int32_t* perm_out,
+                                         void* ws, size_t ws_bytes, moe_stream_t stream) {
+  MOE_TRY(check_fp8_cfg(cfg));
+  if (!x_codes || !x_scales) return MOE_ERR_INVALID_ARG;
+  return layer_forward_fp8(cfg, x, x_codes, x_scales, w_router, bias, wq, out, logits_out, topk_idx_out, topk_w_out,
+                           counts_out, lis_out, h_out, h_shared_out, perm_out, ws, ws_bytes, stream);
+}
+
+// ------------------------------------------------------------------ residual + RMS norm
+moe_status_t moe_add_rmsnorm(int64_t rows, int32_t d, int32_t dtype, float eps, const void* x, const void* residual,
+                             const void* weight, void* sum_out, void* y, uint8_t* codes, float* scales,
+                             moe_stream_t stream) {
+  if (rows < 0 || d < 8 || (dtype != MOE_F32 && dtype != MOE_BF16)) return MOE_ERR_INVALID_ARG;
+  if (!(eps >= 0.f && eps <= 3.0e38f)) return MOE_ERR_INVALID_ARG;
+  if (!codes != !scales || (!y && !codes)) return MOE_ERR_INVALID_ARG;
+  if (d % (codes ? 16 : 8) || d > norm_max_d() || rows > (1LL << 40) / d) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!x || !weight) return MOE_ERR_INVALID_ARG;
+  for (const void* p : std::initializer_list<const void*>{x, residual, weight, sum_out, y, (const void*)codes})
+    if (p && !aligned16(p)) return MOE_ERR_INVALID_ARG;
+  if (((uintptr_t)scales & 3u) || (sum_out && sum_out == y)) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_device());
+  return cuda_status(launch_add_rmsnorm(dtype, rows, d, eps, x, residual, weight, sum_out, y, codes, scales,
+                                        (cudaStream_t)stream));
+}
+
+// ------------------------------------------------------------------ 4-bit experts
+static moe_status_t check_w4_matrix(int64_t n, int64_t rows, int64_t cols, int32_t group) {
+  if (n < 0 || rows < 0 || cols < 8) return MOE_ERR_INVALID_ARG;
+  if (group != 32 && group != 64 && group != 128) return MOE_ERR_UNSUPPORTED;
+  if (n > 65535 || rows % 8 || rows > (1LL << 21) - 32 || cols % 32 || cols > (1LL << 30)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status_t moe_quantize_w4(int64_t n, int64_t rows, int64_t cols, int32_t group, const void* src, uint8_t* codes,
+                             void* scales, moe_stream_t stream) {
+  MOE_TRY(check_w4_matrix(n, rows, cols, group));
+  if (n == 0 || rows == 0) return MOE_OK;
+  for (const void* p : std::initializer_list<const void*>{src, (const void*)codes, scales})
+    if (!p || !aligned16(p)) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_device());
+  return cuda_status(launch_quantize_w4(n, (int)rows, (int)cols, group, src, codes, scales, (cudaStream_t)stream));
+}
+
+moe_status_t moe_dequantize_w4(int64_t n, int64_t rows, int64_t cols, int32_t group, const uint8_t* codes,
+                               const void* scales, void* dst, moe_stream_t stream) {
+  MOE_TRY(check_w4_matrix(n, rows, cols, group));
+  if (n == 0 || rows == 0) return MOE_OK;
+  for (const void* p : std::initializer_list<const void*>{(const void*)codes, scales, dst})
+    if (!p || !aligned16(p)) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_device());
+  return cuda_status(launch_dequantize_w4(n, (int)rows, (int)cols, group, codes, scales, dst, (cudaStream_t)stream));
+}
+
+static moe_status_t check_w4_cfg(const moe_config_t* cfg) {
+  MOE_TRY(check_cfg(cfg));
+  const moe_config_t& c = *cfg;
+  if (c.dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (c.d % 32 || c.f % 32 || (c.n_shared && c.f_shared % 32)) return MOE_ERR_UNSUPPORTED;  // 16-byte code rows
+  return MOE_OK;
+}
+
+// The matrices that a call reads, each with its scales.
+static moe_status_t check_w4_experts(const moe_config_t& c, const moe_w4_experts_t* wq, bool shared) {
+  if (!wq) return MOE_ERR_INVALID_ARG;
+  if (wq->group != 32 && wq->group != 64 && wq->group != 128) return MOE_ERR_UNSUPPORTED;
+  const bool swiglu = c.act == MOE_SWIGLU;
+  if (!wq->gate || !wq->gate_scale || !wq->down || !wq->down_scale) return MOE_ERR_INVALID_ARG;
+  if (swiglu && (!wq->up || !wq->up_scale)) return MOE_ERR_INVALID_ARG;
+  if (shared && c.n_shared > 0 &&
+      (!wq->sh_gate || !wq->sh_gate_scale || !wq->sh_down || !wq->sh_down_scale ||
+       (swiglu && (!wq->sh_up || !wq->sh_up_scale))))
+    return MOE_ERR_INVALID_ARG;
+  for (const void* p : std::initializer_list<const void*>{
+           wq->gate, wq->gate_scale, wq->up, wq->up_scale, wq->down, wq->down_scale, wq->sh_gate, wq->sh_gate_scale,
+           wq->sh_up, wq->sh_up_scale, wq->sh_down, wq->sh_down_scale})
+    if (p && !aligned16(p)) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+moe_status_t moe_w4_workspace_size(const moe_config_t* cfg, size_t* bytes) {
+  MOE_TRY(check_w4_cfg(cfg));
+  return moe_workspace_size(cfg, bytes);
+}
+
+moe_status_t moe_grouped_ffn_w4(const moe_config_t* cfg, const void* x_perm, const int32_t* offsets,
+                                const moe_w4_experts_t* wq, const float* task_w, const int32_t* perm, float* y_perm,
+                                void* ws, size_t ws_bytes, moe_stream_t stream) {
+  MOE_TRY(check_w4_cfg(cfg));
+  const moe_config_t& c = *cfg;
+  MOE_TRY(check_w4_experts(c, wq, false));
+  if (!x_perm || !offsets || !y_perm || (task_w && !perm)) return MOE_ERR_INVALID_ARG;
+  for (const void* p : std::initializer_list<const void*>{x_perm, (const void*)offsets, (const void*)task_w,
+                                                          (const void*)perm, (const void*)y_perm})
+    if (p && !aligned16(p)) return MOE_ERR_INVALID_ARG;
+  const Plan pl = make_plan(c);
+  const Layout L = make_layout(c, pl);
+  MOE_TRY(check_ws(c, ws, ws_bytes, L.h + align256((size_t)c.T * c.k * c.f * pl.es)));
+  MOE_TRY(check_device());
+  FfnIo io;
+  std::memset(&io, 0, sizeof(io));
+  io.w4 = wq;
+  io.n_routed = c.m;
+  io.offsets = offsets;
+  io.x_perm = x_perm;
+  io.routed_rows = (long long)c.T * c.k;
+  io.h = at<void>(ws, L.h);
+  io.y = y_perm;
+  io.task_w = task_w;
+  io.perm = perm;
+  return run_ffn(c, pl, io, 1, kblocks(c.f), at<int>(ws, L.status), (cudaStream_t)stream);
+}
+
+moe_status_t moe_layer_forward_w4(const moe_config_t* cfg, const void* x, const void* w_router, const float* bias,
+                                  const moe_w4_experts_t* wq, void* out, float* logits_out, int32_t* topk_idx_out,
+                                  float* topk_w_out, int32_t* counts_out, moe_lis_t* lis_out, void* ws,
+                                  size_t ws_bytes, moe_stream_t stream) {
+  MOE_TRY(check_w4_cfg(cfg));
+  const moe_config_t& c = *cfg;
+  MOE_TRY(check_w4_experts(c, wq, true));
+  if (!x || !w_router || !out) return MOE_ERR_INVALID_ARG;
+  for (const void* p : std::initializer_list<const void*>{x, w_router, (const void*)bias, out, (const void*)logits_out,
+                        (const void*)topk_idx_out, (const void*)topk_w_out, (const void*)counts_out,
+                        (const void*)lis_out})
+    if (p && !aligned16(p)) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_ws(c, ws, ws_bytes, make_layout(c, make_plan(c)).total));
+  MOE_TRY(check_device());
+  return layer_forward_impl(c, x, w_router, bias, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, out,
+                            logits_out, topk_idx_out, topk_w_out, counts_out, lis_out, nullptr, nullptr, nullptr,
+                            nullptr, nullptr, nullptr, ws, (cudaStream_t)stream, wq);
+}
+
 
 // ------------------------------------------------------------------ atomic experts
 static moe_status_t check_atomic_cfg(const moe_atomic_config_t* c) {

@@ -275,6 +275,15 @@ cudaError_t launch_atomic_experts(int T, int d, int K, int act, const void* x, c
 // elements, multiples of 8; src 16-byte and dst 8-byte aligned).
 cudaError_t launch_quantize_e4m3(long long rows, int cols, const void* src, long long src_ld, uint8_t* dst,
                                  long long dst_ld, float* scale, cudaStream_t s);
+// scales of rows moved to segment order: dst[inv_perm[q]] = src[q / k] for q < Tk
+// (inv_perm[q] < 0: skipped).
+cudaError_t launch_permute_scales(int Tk, int k, const float* src, const int32_t* inv_perm, float* dst,
+                                  cudaStream_t s);
+// Residual addition, RMS norm and 8-bit output (csrc/norm.cu); d <= norm_max_d().
+cudaError_t launch_add_rmsnorm(int dtype, long long rows, int d, float eps, const void* x, const void* residual,
+                               const void* weight, void* sum_out, void* y, uint8_t* codes, float* scales,
+                               cudaStream_t s);
+int norm_max_d();
 // Records the profiling hook's event i (moe_set_stage_events) on `s`, if one is set.
 cudaError_t mark_stage_event(int i, cudaStream_t s);
 

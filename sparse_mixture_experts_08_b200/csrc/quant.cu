@@ -56,7 +56,25 @@ __global__ void __launch_bounds__(QZ_WARPS * 32) quantize_e4m3_rows_kernel(long 
   }
 }
 
+__global__ void __launch_bounds__(256) permute_scales_kernel(int Tk, int k, const float* __restrict__ src,
+                                                             const int32_t* __restrict__ inv_perm,
+                                                             float* __restrict__ dst) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int q = blockIdx.x * 256 + threadIdx.x;
+  if (q >= Tk) return;
+  const int pos = inv_perm[q];
+  if (pos >= 0 && pos < Tk) dst[pos] = src[q / k];
+}
+
 }  // namespace
+
+cudaError_t launch_permute_scales(int Tk, int k, const float* src, const int32_t* inv_perm, float* dst,
+                                  cudaStream_t s) {
+  cudaError_t e = launch_k(permute_scales_kernel, dim3((Tk + 255) / 256), dim3(256), 0, s, Tk, k, src, inv_perm, dst);
+  count_launch();
+  return e;
+}
 
 cudaError_t launch_quantize_e4m3(long long rows, int cols, const void* src, long long src_ld, uint8_t* dst,
                                  long long dst_ld, float* scale, cudaStream_t s) {

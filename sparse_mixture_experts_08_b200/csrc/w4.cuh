@@ -1,0 +1,55 @@
+// 4-bit expert weights: the internal interface of csrc/w4.cu.
+//
+// A matrix [R, K] is held as codes [R, K / 2] bytes and bf16 scales [ceil(K / G), R]
+// (group-major: a tile's rows are contiguous, so a few 16-byte copies fetch them). A row
+// is a sequence of 32-bit words of 8 columns; column 2i of a word sits in bits 4i..4i+3
+// and column 2i+1 in bits 16+4i..19+4i, so (word >> 4i) & 0x000F000F is the bf16 pair of
+// neighbouring columns that the tensor cores take, up to the exponent.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+struct W4Matrix {
+  const uint8_t* codes;         // [n, R, K / 2]
+  const __nv_bfloat16* scales;  // [n, ceil(K / G), R]
+};
+
+// One class of products  out rows = epi(rows . W_g^T): group g multiplies its rows with
+// matrix g.
+struct W4Class {
+  int n_groups;
+  int R;                 // weight rows (output features) of a matrix
+  int K;                 // reduction length, a multiple of 32
+  const int* seg_off;    // device [n_groups + 1]: rows of group g (nullable)
+  int max_row;           // seg_off entries and perm values lie in [0, max_row]
+  int const_rows;        // rows per group when seg_off == nullptr
+  int b_group_stride;    // first input row of group g, and its first output row, when
+  int out_group_stride;  //   seg_off == nullptr
+  const __nv_bfloat16* b;  // input rows [b_rows, K]
+  long long b_rows;
+  W4Matrix a0, a1;       // a1: the up matrix (SwiGLU)
+  void* out;             // bf16 rows (SWIGLU, RELU) or fp32 rows (DOWN), pitch R
+  const float* row_w;    // DOWN: weight of an output row (nullable; preferred over task_w)
+  const float* task_w;   // DOWN: weight task_w[perm[row]] (nullable: 1)
+  const int* perm;
+};
+
+struct W4Params {
+  W4Class cls[2];
+  int n_classes;
+  int group;    // 32, 64 or 128
+  int* status;
+  unsigned long long wait_limit_ns;
+};
+
+// max_rows: an upper bound on a group's rows that the host knows (the batch); avg_rows:
+// the routed segments' mean length.
+cudaError_t launch_w4_gemm(int epi, const W4Params& p, int max_rows, double avg_rows, cudaStream_t s);
+cudaError_t launch_quantize_w4(long long n, int rows, int cols, int group, const void* src, uint8_t* codes,
+                               void* scales, cudaStream_t s);
+cudaError_t launch_dequantize_w4(long long n, int rows, int cols, int group, const uint8_t* codes, const void* scales,
+                                 void* dst, cudaStream_t s);
+
+}  // namespace moe

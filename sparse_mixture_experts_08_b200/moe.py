@@ -33,7 +33,8 @@ EXPORTS = ["moe_workspace_size", "moe_atomic_workspace_size", "moe_route", "moe_
            "moe_debug_set_wait_limit_ns", "moe_debug_set_barrier_extra", "moe_set_stage_events", "moe_launch_count", "moe_route_static",
            "moe_replica_split", "moe_layer_forward_replicated", "moe_floe_pack_down", "moe_floe_calibrate",
            "moe_floe_workspace_size", "moe_layer_forward_floe", "moe_quantize_e4m3", "moe_fp8_workspace_size",
-           "moe_layer_forward_fp8"]
+           "moe_layer_forward_fp8", "moe_layer_forward_fp8_codes", "moe_add_rmsnorm", "moe_quantize_w4",
+           "moe_dequantize_w4", "moe_w4_workspace_size", "moe_grouped_ffn_w4", "moe_layer_forward_w4"]
 
 
 class MoEConfig(ctypes.Structure):
@@ -53,6 +54,13 @@ LIS_BYTES = 16  # moe_lis_t: int32 max_count, int32 argmax_expert, double lis
 class MoEFp8Experts(ctypes.Structure):
     """moe_fp8_experts_t: device pointers to E4M3 codes (uint8) and fp32 row scales."""
     _fields_ = [(name, ctypes.c_void_p) for name in (
+        "gate", "gate_scale", "up", "up_scale", "down", "down_scale", "sh_gate", "sh_gate_scale", "sh_up",
+        "sh_up_scale", "sh_down", "sh_down_scale")]
+
+
+class MoEW4Experts(ctypes.Structure):
+    """moe_w4_experts_t: the group and device pointers to 4-bit codes (uint8) and bf16 group scales."""
+    _fields_ = [("group", ctypes.c_int32)] + [(name, ctypes.c_void_p) for name in (
         "gate", "gate_scale", "up", "up_scale", "down", "down_scale", "sh_gate", "sh_gate_scale", "sh_up",
         "sh_up_scale", "sh_down", "sh_down_scale")]
 
@@ -101,6 +109,13 @@ def lib() -> ctypes.CDLL:
             "moe_quantize_e4m3": [ctypes.c_int64, ctypes.c_int64, P, P, P, P],
             "moe_fp8_workspace_size": [P, P],
             "moe_layer_forward_fp8": [P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, S, P],
+            "moe_layer_forward_fp8_codes": [P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, S, P],
+            "moe_add_rmsnorm": [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_float, P, P, P, P, P, P, P, P],
+            "moe_quantize_w4": [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, P, P, P, P],
+            "moe_dequantize_w4": [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, P, P, P, P],
+            "moe_w4_workspace_size": [P, P],
+            "moe_grouped_ffn_w4": [P, P, P, P, P, P, P, P, S, P],
+            "moe_layer_forward_w4": [P, P, P, P, P, P, P, P, P, P, P, P, S, P],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -122,6 +137,10 @@ def _p(t) -> Optional[int]:
     if isinstance(t, int):
         return t
     return t.data_ptr()
+
+
+def _dtype_code(t) -> int:
+    return {torch.float32: F32, torch.bfloat16: BF16}.get(t.dtype, -1)  # -1: the library refuses it
 
 
 def _stream(stream) -> Optional[int]:
@@ -277,6 +296,99 @@ def moe_layer_forward_fp8(cfg, x, w_router, bias, wq, out, ws, logits_out=None, 
         ctypes.byref(cfg), _p(x), _p(w_router), _p(bias), ctypes.byref(st), _p(out), _p(logits_out),
         _p(topk_idx_out), _p(topk_w_out), _p(counts_out), _p(lis_out), _p(h_out), _p(h_shared_out), _p(perm_out),
         _p(ws), ws.numel(), _stream(stream)))
+
+
+def moe_layer_forward_fp8_codes(cfg, x, x_codes, x_scales, w_router, bias, wq, out, ws, logits_out=None,
+                                topk_idx_out=None, topk_w_out=None, counts_out=None, lis_out=None, h_out=None,
+                                h_shared_out=None, perm_out=None, stream=None):
+    """moe_layer_forward_fp8 for tokens that come with E4M3 codes [T, d] and scales [T] (moe_add_rmsnorm's)."""
+    st = MoEFp8Experts(**{k: _p(wq.get(k)) for k, _ in MoEFp8Experts._fields_})
+    _check("moe_layer_forward_fp8_codes", lib().moe_layer_forward_fp8_codes(
+        ctypes.byref(cfg), _p(x), _p(x_codes), _p(x_scales), _p(w_router), _p(bias), ctypes.byref(st), _p(out),
+        _p(logits_out), _p(topk_idx_out), _p(topk_w_out), _p(counts_out), _p(lis_out), _p(h_out), _p(h_shared_out),
+        _p(perm_out), _p(ws), ws.numel(), _stream(stream)))
+
+
+def moe_add_rmsnorm(x, residual, weight, eps, y, sum_out=None, codes=None, scales=None, stream=None):
+    """y [rows, d] = RMS norm of x + residual (residual may be None) times weight; sum_out: the sum; codes
+    (uint8, like x) and scales [rows] (fp32): E4M3 codes of y, one scale a row. x is fp32 or bf16, contiguous."""
+    d = int(x.shape[-1])
+    _check("moe_add_rmsnorm", lib().moe_add_rmsnorm(x.numel() // d if d else 0, d, _dtype_code(x), float(eps), _p(x),
+                                                    _p(residual), _p(weight), _p(sum_out), _p(y), _p(codes),
+                                                    _p(scales), _stream(stream)))
+
+
+def _w4_shape(t, cols):
+    """(matrices, rows) of a stack of matrices [..., rows, cols] or one matrix [rows, cols]."""
+    rows = int(t.shape[-2])
+    return (t.numel() // (rows * cols) if rows and cols else 0), rows
+
+
+def moe_quantize_w4(src, group, codes, scales, stream=None):
+    """4-bit codes [n, rows, cols / 2] (uint8) and bf16 scales [n, ceil(cols / group), rows] of bf16 matrices
+    src [n, rows, cols] (or one matrix [rows, cols])."""
+    cols = int(src.shape[-1])
+    n, rows = _w4_shape(src, cols)
+    _check("moe_quantize_w4", lib().moe_quantize_w4(n, rows, cols, int(group), _p(src), _p(codes), _p(scales),
+                                                    _stream(stream)))
+
+
+def moe_dequantize_w4(codes, scales, group, dst, stream=None):
+    """The bf16 matrices dst [n, rows, cols] that codes and scales (as moe_quantize_w4 writes them) stand for."""
+    cols = int(dst.shape[-1])
+    n, rows = _w4_shape(dst, cols)
+    _check("moe_dequantize_w4", lib().moe_dequantize_w4(n, rows, cols, int(group), _p(codes), _p(scales), _p(dst),
+                                                        _stream(stream)))
+
+
+def moe_w4_workspace_size(cfg) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_w4_workspace_size", lib().moe_w4_workspace_size(ctypes.byref(cfg), ctypes.byref(n)))
+    return n.value
+
+
+def _w4_experts(wq) -> MoEW4Experts:
+    st = MoEW4Experts(**{k: _p(wq.get(k)) for k, _ in MoEW4Experts._fields_[1:]})
+    st.group = int(wq["group"])
+    return st
+
+
+def moe_grouped_ffn_w4(cfg, x_perm, offsets, wq, task_w, perm, y_perm, ws, stream=None):
+    """wq: a dict of device tensors as quantize_experts_w4 returns (kept alive by the caller)."""
+    st = _w4_experts(wq)
+    _check("moe_grouped_ffn_w4", lib().moe_grouped_ffn_w4(ctypes.byref(cfg), _p(x_perm), _p(offsets),
+                                                          ctypes.byref(st), _p(task_w), _p(perm), _p(y_perm), _p(ws),
+                                                          ws.numel(), _stream(stream)))
+
+
+def moe_layer_forward_w4(cfg, x, w_router, bias, wq, out, ws, logits_out=None, topk_idx_out=None, topk_w_out=None,
+                         counts_out=None, lis_out=None, stream=None):
+    """wq: a dict of device tensors as quantize_experts_w4 returns (kept alive by the caller)."""
+    st = _w4_experts(wq)
+    _check("moe_layer_forward_w4", lib().moe_layer_forward_w4(
+        ctypes.byref(cfg), _p(x), _p(w_router), _p(bias), ctypes.byref(st), _p(out), _p(logits_out),
+        _p(topk_idx_out), _p(topk_w_out), _p(counts_out), _p(lis_out), _p(ws), ws.numel(), _stream(stream)))
+
+
+def quantize_experts_w4(w_gate, w_up, w_down, ws_gate=None, ws_up=None, ws_down=None, group=128,
+                        stream=None) -> dict:
+    """4-bit codes and group scales of every expert weight (device bf16 tensors in,
+    device tensors out), keyed as moe_w4_experts_t's fields, and the group."""
+    out = {"group": int(group)}
+    for key, w in (("gate", w_gate), ("up", w_up), ("down", w_down), ("sh_gate", ws_gate), ("sh_up", ws_up),
+                   ("sh_down", ws_down)):
+        if w is None:
+            continue
+        n, rows, cols = w.shape
+        codes = torch.empty((n, rows, cols // 2), dtype=torch.uint8, device=w.device)
+        scales = torch.empty((n, -(-cols // group), rows), dtype=torch.bfloat16, device=w.device)
+        moe_quantize_w4(w, group, codes, scales, stream=stream)
+        out[key], out[key + "_scale"] = codes, scales
+    return out
+
+
+def w4_workspace(cfg, device="cuda") -> torch.Tensor:
+    return torch.zeros(max(moe_w4_workspace_size(cfg), 256), dtype=torch.uint8, device=device)
 
 
 def quantize_experts(w_gate, w_up, w_down, ws_gate=None, ws_up=None, ws_down=None, stream=None) -> dict:

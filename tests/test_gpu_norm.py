@@ -1,0 +1,200 @@
+"""Residual + RMS norm with 8-bit output on the GPU against the formulas in 64 bits.
+
+Bounds (relative, per element): the sum is one fp32 addition and one rounding to the
+output type, so it is compared bit-exactly. y: fp32 squares and their sum over d terms
+(any order: at most d 2^-24, half of it after the root), the sum x + residual (2^-24 each,
+in r and, twice, in the mean), root, division and two products (4 x 2^-24), then half a
+step of the output type. Codes: half a step of E4M3 (2^-4 of the value, or half the
+smallest step) on top of the fp32 part.
+"""
+import pytest
+import torch
+
+import sparse_mixture_experts_08_b200 as moe
+from gpu_helpers import require_gpu
+
+pytestmark = pytest.mark.gpu
+
+F64 = torch.float64
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _gpu():
+    require_gpu()
+
+
+def _inputs(rows, d, dtype, residual, seed=0):
+    gen = torch.Generator().manual_seed(rows * 31 + d + seed)
+    x = (torch.randn(rows, d, generator=gen) * torch.exp2(torch.randint(-8, 8, (rows, 1), generator=gen).float()))
+    r = torch.randn(rows, d, generator=gen) * 3 if residual else None
+    w = 1 + 0.3 * torch.randn(d, generator=gen)
+    return x.to(dtype).cuda(), None if r is None else r.to(dtype).cuda(), w.to(dtype).cuda()
+
+
+def norm64(x, residual, w, eps):
+    r = x.to(F64) + (residual.to(F64) if residual is not None else 0)
+    return r / torch.sqrt((r * r).mean(1, keepdim=True) + eps) * w.to(F64)
+
+
+def fp32_part(d):
+    return (0.5 * d + 8) * 2.0 ** -24
+
+
+def check_codes(codes, scales, ref, d):
+    rel = fp32_part(d) + 2.0 ** -22
+    top = ref.abs().amax(1)
+    want = torch.where(top > 0, top / 448, torch.ones_like(top))
+    assert ((scales.to(F64) - want).abs() <= rel * want).all()
+    val = codes.view(torch.float8_e4m3fn).to(F64) * scales.to(F64)[:, None]
+    half = torch.maximum(2.0 ** -4 * ref.abs(), 2.0 ** -10 * want[:, None])
+    assert ((val - ref).abs() <= half * (1 + 2.0 ** -10) + rel * ref.abs()).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,d", [(1, 8), (1, 4096), (3, 16), (5, 248), (16, 4096), (7, 264), (129, 512), (2, 520),
+                                    (33, 1032), (4, 2048), (9, 2056), (5, 4104), (3, 8192), (2, 8200), (2, 16384),
+                                    (3, 16392), (2, 32768), (1025, 64)])
+def test_norm(rows, d, dtype):
+    for residual in (False, True):
+        x, r, w = _inputs(rows, d, dtype, residual)
+        y = torch.full_like(x, float("nan"))
+        total = torch.full_like(x, float("nan")) if residual else None
+        with_codes = d % 16 == 0
+        codes = torch.empty(rows, d, dtype=torch.uint8, device="cuda") if with_codes else None
+        scales = torch.empty(rows, device="cuda") if with_codes else None
+        moe.moe_add_rmsnorm(x, r, w, 1e-5, y, sum_out=total, codes=codes, scales=scales)
+        ref = norm64(x, r, w, 1e-5)
+        if residual:
+            assert torch.equal(total, (x.float() + r.float()).to(dtype))
+        half = torch.finfo(dtype).eps / 2
+        assert ((y.to(F64) - ref).abs() <= (half + fp32_part(d)) * ref.abs() + 1e-38).all()
+        if with_codes:
+            check_codes(codes, scales, ref, d)
+            only, osc = torch.empty_like(codes), torch.empty_like(scales)
+            moe.moe_add_rmsnorm(x, r, w, 1e-5, None, codes=only, scales=osc)
+            assert torch.equal(only, codes) and torch.equal(osc, scales)
+
+
+def test_rows_of_zeros_and_extremes():
+    d = 256
+    x = torch.zeros(6, d, dtype=torch.bfloat16)
+    x[1] = 1e-20
+    x[2, 3] = 1e18
+    x[3] = float("inf")
+    x[4, 9] = float("nan")
+    x = x.cuda()
+    w = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    y, codes, scales = torch.empty_like(x), torch.empty(6, d, dtype=torch.uint8, device="cuda"), torch.empty(6, device="cuda")
+    moe.moe_add_rmsnorm(x, None, w, 1e-6, y, codes=codes, scales=scales)
+    assert (y[0] == 0).all() and (y[5] == 0).all() and scales[0] == 1 and (codes[0] == 0).all()
+    ref = norm64(x[1:3], None, w, 1e-6)
+    assert ((y[1:3].to(F64) - ref).abs() <= (2.0 ** -8 + fp32_part(d)) * ref.abs() + 1e-38).all()
+    assert torch.isnan(y[3]).all() and torch.isnan(y[4]).all()
+    assert torch.isfinite(y[[0, 1, 2, 5]].float()).all()
+
+
+@pytest.mark.parametrize("target", ["x", "residual"])
+def test_in_place(target):
+    x, r, w = _inputs(37, 1040, torch.bfloat16, True)
+    y, total = torch.empty_like(x), torch.empty_like(x)
+    moe.moe_add_rmsnorm(x, r, w, 1e-5, y, sum_out=total)
+    a, b = x.clone(), r.clone()
+    if target == "x":      # the sum over the residual, y over x
+        moe.moe_add_rmsnorm(a, b, w, 1e-5, a, sum_out=b)
+        assert torch.equal(a, y) and torch.equal(b, total)
+    else:                  # the sum over x, y over the residual
+        moe.moe_add_rmsnorm(a, b, w, 1e-5, b, sum_out=a)
+        assert torch.equal(b, y) and torch.equal(a, total)
+
+
+def test_rows_past_32_bit_offsets():
+    rows, d = (1 << 31) // 4096 + 5, 4096
+    x = torch.zeros(rows, d, dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator().manual_seed(1)
+    tail = torch.randn(7, d, generator=gen).to(torch.bfloat16).cuda()
+    x[-7:] = tail
+    w = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    y = torch.empty_like(x)
+    moe.moe_add_rmsnorm(x, None, w, 1e-5, y)
+    want = torch.empty_like(tail)
+    moe.moe_add_rmsnorm(tail, None, w, 1e-5, want)
+    assert torch.equal(y[-7:], want) and (y[:3] == 0).all()
+
+
+def test_captured_and_replayed():
+    x, r, w = _inputs(16, 4096, torch.bfloat16, True)
+    y, total = torch.empty_like(x), torch.empty_like(x)
+    codes, scales = torch.empty(16, 4096, dtype=torch.uint8, device="cuda"), torch.empty(16, device="cuda")
+    moe.moe_add_rmsnorm(x, r, w, 1e-5, y, sum_out=total, codes=codes, scales=scales)
+    want = [t.clone() for t in (y, total, codes, scales)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.moe_add_rmsnorm(x, r, w, 1e-5, y, sum_out=total, codes=codes, scales=scales)
+    for t in (y, total, codes, scales):
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip((y, total, codes, scales), want))
+
+
+# ------------------------------------------------------------------ into the layers
+
+def _bf16(gen, *s):
+    return (torch.randn(*s, generator=gen) * s[-1] ** -0.5).to(torch.bfloat16).cuda()
+
+
+@pytest.mark.parametrize("T,d,f,m,k,ns,fs,act", [(16, 256, 320, 8, 2, 0, 0, moe.SWIGLU), (3, 128, 64, 4, 4, 1, 96, moe.RELU),
+                                                 (300, 256, 192, 6, 2, 2, 160, moe.SWIGLU),
+                                                 (8200, 64, 64, 8, 1, 0, 0, moe.SWIGLU)])
+def test_fp8_layer_on_given_codes(T, d, f, m, k, ns, fs, act):
+    """With the codes that the 8-bit layer would make itself, the outputs are the same bits."""
+    gen = torch.Generator().manual_seed(T + d)
+    up = act == moe.SWIGLU
+    w = [_bf16(gen, m, f, d), _bf16(gen, m, f, d) if up else None, _bf16(gen, m, d, f)]
+    sh = [_bf16(gen, ns, fs, d), _bf16(gen, ns, fs, d) if up else None, _bf16(gen, ns, d, fs)] if ns else [None] * 3
+    wq = moe.quantize_experts(*w, *sh)
+    c = moe.make_config(T, d, f, m, k, n_shared=ns, f_shared=fs, act=act)
+    x, wr = _bf16(gen, T, d) * 16, _bf16(gen, m, d)
+    codes, scales = torch.empty(T, d, dtype=torch.uint8, device="cuda"), torch.empty(T, device="cuda")
+    moe.moe_quantize_e4m3(x, codes, scales)
+    a, b, ws = torch.empty_like(x), torch.empty_like(x), moe.fp8_workspace(c)
+    moe.moe_layer_forward_fp8(c, x, wr, None, wq, a, ws)
+    moe.moe_layer_forward_fp8_codes(c, x, codes, scales, wr, None, wq, b, ws)
+    assert moe.moe_read_device_status(ws) == moe.OK
+    assert torch.equal(a, b)
+
+
+def test_block_norm_then_8_bit_and_4_bit_layers():
+    """The block as a server runs it: sum and norm, then the layer, then the next block's sum and norm."""
+    gen = torch.Generator().manual_seed(77)
+    T, d, f, m, k = 24, 512, 640, 8, 2
+    w = [_bf16(gen, m, f, d), _bf16(gen, m, f, d), _bf16(gen, m, d, f)]
+    wr, weight = _bf16(gen, m, d), (1 + 0.1 * torch.randn(d, generator=gen)).to(torch.bfloat16).cuda()
+    x, res = (torch.randn(T, d, generator=gen).to(torch.bfloat16).cuda() for _ in range(2))
+    c = moe.make_config(T, d, f, m, k, renormalize=True)
+    y, codes, scales = torch.empty_like(x), torch.empty(T, d, dtype=torch.uint8, device="cuda"), torch.empty(T, device="cuda")
+    stream = res.clone()
+    moe.moe_add_rmsnorm(x, stream, weight, 1e-5, y, sum_out=stream, codes=codes, scales=scales)
+    out = {}
+    ref = torch.empty_like(x)
+    moe.moe_layer_forward(c, y, wr, None, *w, None, None, None, ref, moe.workspace(c))
+    q8, q4 = moe.quantize_experts(*w), moe.quantize_experts_w4(*w, group=32)
+    for name in ("fp8", "w4"):
+        out[name] = torch.empty_like(x)
+    moe.moe_layer_forward_fp8_codes(c, y, codes, scales, wr, None, q8, out["fp8"], moe.fp8_workspace(c))
+    moe.moe_layer_forward_w4(c, y, wr, None, q4, out["w4"], moe.w4_workspace(c))
+    # the weights' own steps dominate: E4M3 rounds x, W and h by at most 2^-4 each, three
+    # factors in each of two products; a 4-bit code is off by at most half a step of max/7
+    # a group, 1/14 of the group's largest weight, which for 32 normal weights is below
+    # 4 of their standard deviations: 0.29 of a typical weight at most, in three matrices.
+    # As 2-norms over independent roundings (uniform: 1/sqrt(3) of the half step, and the
+    # largest of 32 normals at 2.1 standard deviations): fp8 < sqrt(6) 2^-4 / sqrt(3),
+    # w4 < sqrt(3) (2.1 / 14) / sqrt(3) with half as much again for the silu's slope.
+    far = lambda a: ((a.float() - ref.float()).norm() / ref.float().norm()).item()  # noqa: E731
+    assert far(out["fp8"]) < 0.09 and far(out["w4"]) < 0.23
+    # the next block
+    nxt = torch.empty_like(x)
+    moe.moe_add_rmsnorm(out["w4"], stream, weight, 1e-5, nxt, sum_out=stream)
+    s = (x.float() + res.float()).to(torch.bfloat16)
+    assert torch.equal(stream, (out["w4"].float() + s.float()).to(torch.bfloat16))

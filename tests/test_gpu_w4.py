@@ -1,0 +1,417 @@
+"""4-bit expert weights on the GPU against plain formulas in 64 bits.
+
+- Quantizer: codes and scales bit-exact (one IEEE fp32 division each, then roundings).
+- Dequantizer: bit-exact.
+- Expert products: every output element within a bound built from what the kernels may
+  round, elementwise and without statistics (u = 2^-8, bf16's half step):
+    out   is rounded to bf16 once:                       u |out|
+    h     is rounded to bf16 once:                       u sum_j |h_j| |W_down j|
+    sums  are fp32 over K terms, any order, at most one rounding a term and one for each
+          group's scale: 2 K 2^-24 times the sum of the absolute terms; for h through
+          |d silu| <= 1.1, and 2^-18 relative for the exponential and the division.
+  Scales with more than 5 significant bits are a weight of 8 more bits that may be
+  rounded to bf16: u sum |x| |W| more in each sum.
+"""
+import numpy as np
+import pytest
+import torch
+
+import sparse_mixture_experts_08_b200 as moe
+from gpu_helpers import require_gpu
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -8
+F64 = torch.float64
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _gpu():
+    require_gpu()
+
+
+# ------------------------------------------------------------------ the format, in torch
+
+def pack_ref(v, group):
+    """Codes (as whole numbers [n, rows, cols]) and scales [n, ng, rows] of v (bf16) by the format's rules."""
+    n, rows, cols = v.shape
+    ng = -(-cols // group)
+    f = torch.nn.functional.pad(v.float(), (0, ng * group - cols)).view(n, rows, ng, group)
+    mant, ex = torch.frexp(f.abs().amax(3) / 7)
+    scale = torch.ldexp(torch.round(mant * 32) / 32, ex)
+    scale = torch.where(scale >= 2.0 ** -126, scale, torch.ones_like(scale))
+    q = torch.round(f / scale[..., None]).view(n, rows, ng * group)[:, :, :cols]
+    return q.to(torch.int32), scale.to(torch.bfloat16).transpose(1, 2).contiguous()
+
+
+def encode(q):
+    """Whole numbers [n, rows, cols] -> codes [n, rows, cols / 2]."""
+    n, rows, cols = q.shape
+    w = (q + 8).view(n, rows, cols // 8, 8)
+    word = torch.zeros(n, rows, cols // 8, dtype=torch.int32, device=q.device)
+    for c in range(8):
+        word |= w[..., c] << ((16 if c & 1 else 0) + 4 * (c >> 1))
+    return word.view(torch.uint8)
+
+
+def values64(q, scales, group):
+    cols = q.shape[2]
+    return q.to(F64) * scales.to(F64).transpose(1, 2).repeat_interleave(group, 2)[:, :, :cols]
+
+
+def make_matrix(gen, n, rows, cols, group, five_bits=True):
+    v = (torch.randn(n, rows, cols, generator=gen) * cols ** -0.5).to(torch.bfloat16).cuda()
+    q, s = pack_ref(v, group)
+    if not five_bits:  # scales of another origin: all 8 bits of a bf16, and code -8
+        s = (s.float() * (1 + torch.rand(s.shape, generator=gen).cuda() / 16)).to(torch.bfloat16)
+        q[:, ::3, ::5] = -8
+    return encode(q), s, values64(q, s, group)
+
+
+def make_experts(gen, m, d, f, group, act, ns=0, fs=0, five_bits=True):
+    wq, val = {"group": group}, {}
+    for key, n, rows, cols in (("gate", m, f, d), ("up", m, f, d), ("down", m, d, f), ("sh_gate", ns, fs, d),
+                               ("sh_up", ns, fs, d), ("sh_down", ns, d, fs)):
+        if n and not (key.endswith("up") and act == moe.RELU):
+            wq[key], wq[key + "_scale"], val[key] = make_matrix(gen, n, rows, cols, group, five_bits)
+    return wq, val
+
+
+def ffn64(x, val, pre, e, act, extra=0.0):
+    """(y, bound of |kernel - y|) of expert e for rows x (fp64 of bf16 values)."""
+    wg, wd = val[pre + "gate"][e], val[pre + "down"][e]
+    d, f = wg.shape[1], wd.shape[1]
+    eps = 2 * d * 2.0 ** -24 + extra
+    g, ga = x @ wg.t(), (x.abs() @ wg.abs().t()) * eps
+    if act == moe.SWIGLU:
+        wu = val[pre + "up"][e]
+        u, ua = x @ wu.t(), (x.abs() @ wu.abs().t()) * eps
+        sg = torch.sigmoid(g)
+        h = g * sg * u
+        eh = (1.1 * ga) * (u.abs() + ua) + (g * sg).abs() * ua + 2.0 ** -18 * h.abs()
+    else:
+        h, eh = g.clamp_min(0), ga
+    eh = eh + U * (h.abs() + eh)
+    y = h @ wd.t()
+    return y, eh @ wd.abs().t() + (2 * f * 2.0 ** -24 + extra) * ((h.abs() + eh) @ wd.abs().t())
+
+
+def check(got, ref, bound, what=""):
+    over = ((got.to(F64) - ref).abs() - bound).max().item()
+    assert torch.isfinite(got.float()).all(), what
+    assert over <= 0, f"{what}: an element is {over:.3e} over its bound"
+
+
+# ------------------------------------------------------------------ quantizer
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("shape", [(1, 8, 32), (3, 40, 96), (2, 264, 1376), (1, 72, 4096), (5, 16, 544)])
+def test_quantizer_and_dequantizer_are_bit_exact(shape, group):
+    gen = torch.Generator().manual_seed(shape[1] * 131 + shape[2] + group)
+    v = torch.randn(shape, generator=gen) * torch.exp2(torch.randint(-30, 30, shape[:2] + (1,), generator=gen).float())
+    v[0, 0] = 0.0                                              # scale 1
+    v[0, 1] = -0.0
+    v[0, 2] = torch.randint(-3, 4, shape[2:], generator=gen) * 2.0 ** -130   # below the smallest scale
+    v[0, 3] = torch.randint(-14, 15, shape[2:], generator=gen) * 0.5         # ties between codes
+    v[0, 4, :] = 3.0e38                                        # the largest scale
+    v[0, 5, 0] = 1.0e30                                        # one large value
+    v = v.to(torch.bfloat16).cuda()
+    n, rows, cols = shape
+    codes = torch.full((n, rows, cols // 2), 0x5A, dtype=torch.uint8, device="cuda")
+    scales = torch.full((n, -(-cols // group), rows), -1.0, dtype=torch.bfloat16, device="cuda")
+    moe.moe_quantize_w4(v, group, codes, scales)
+    q, s = pack_ref(v, group)
+    assert torch.equal(scales.view(torch.int16), s.view(torch.int16))
+    assert torch.equal(codes, encode(q))
+    back = torch.empty_like(v)
+    moe.moe_dequantize_w4(codes, scales, group, back)
+    ref = values64(q, s, group)
+    assert torch.equal(back.to(F64), ref)  # code x scale is a bf16 number: no rounding
+    # and within half a step of the weight
+    step = s.to(F64).transpose(1, 2).repeat_interleave(group, 2)[:, :, :cols]
+    assert ((ref - v.to(F64)).abs() <= step / 2 * (1 + 2.0 ** -20)).all()
+
+
+def test_dequantizer_rounds_scales_of_another_origin_once():
+    gen = torch.Generator().manual_seed(5)
+    codes, scales, ref = make_matrix(gen, 2, 24, 160, 64, five_bits=False)
+    out = torch.empty(2, 24, 160, dtype=torch.bfloat16, device="cuda")
+    moe.moe_dequantize_w4(codes, scales, 64, out)
+    assert torch.equal(out, ref.float().to(torch.bfloat16))  # a product of 4 and 8 bits is exact in fp32
+
+
+def test_quantizer_takes_infinities_and_nan_without_writing_elsewhere():
+    v = torch.randn(1, 16, 128).to(torch.bfloat16)
+    v[0, 3, 7], v[0, 5, 64] = float("inf"), float("nan")
+    v = v.cuda()
+    codes = torch.empty(1, 16, 64, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(1, 4, 16, dtype=torch.bfloat16, device="cuda")
+    moe.moe_quantize_w4(v, 32, codes, scales)
+    q, s = pack_ref(v[:, [0, 1, 2, 4, 6, 7]], 32)
+    keep = torch.tensor([0, 1, 2, 4, 6, 7], device="cuda")
+    assert torch.equal(codes[:, keep], encode(q)) and torch.equal(scales[:, :, keep], s)
+
+
+# ------------------------------------------------------------------ grouped products
+
+def _segments(lengths):
+    return torch.tensor([0] + np.cumsum(lengths).tolist(), dtype=torch.int32, device="cuda")
+
+
+GROUPED = [
+    # lengths of the segments, d, f, group, act
+    ([1], 32, 32, 32, moe.SWIGLU),
+    ([0, 1, 0, 3], 64, 96, 64, moe.SWIGLU),
+    ([8, 9, 0, 16, 17, 7], 160, 224, 32, moe.SWIGLU),
+    ([5, 0, 2], 4096, 512, 128, moe.SWIGLU),
+    ([33, 0, 31, 64, 65, 1], 288, 416, 64, moe.SWIGLU),
+    ([2, 130, 0, 257, 15], 512, 1408, 128, moe.SWIGLU),
+    ([40, 3, 12], 2080, 1376, 32, moe.RELU),
+    ([0, 0, 19], 96, 2080, 128, moe.RELU),
+    ([300, 1, 0, 513], 224, 352, 64, moe.RELU),
+    ([129, 128, 127, 256], 1056, 544, 128, moe.SWIGLU),
+]
+
+
+@pytest.mark.parametrize("lengths,d,f,group,act", GROUPED)
+def test_grouped_ffn(lengths, d, f, group, act):
+    gen = torch.Generator().manual_seed(sum(lengths) * 7 + d + f + group)
+    m, rows = len(lengths), sum(lengths)
+    wq, val = make_experts(gen, m, d, f, group, act)
+    x = torch.randn(rows, d, generator=gen).to(torch.bfloat16).cuda()
+    offsets = _segments(lengths)
+    # two tasks more than the segments hold: rows behind the last segment stay as they were
+    c = moe.make_config(rows + 2, d, f, m, 1, act=act)
+    xp = torch.cat([x, torch.full((2, d), float("nan"), dtype=torch.bfloat16, device="cuda")])
+    ws = moe.w4_workspace(c)
+    y = torch.full((rows + 2, d), -7.0, dtype=torch.float32, device="cuda")
+    moe.moe_grouped_ffn_w4(c, xp, offsets, wq, None, None, y, ws)
+    assert moe.moe_read_device_status(ws) == moe.OK
+    assert (y[rows:] == -7.0).all()
+    # and with task weights, in another row order
+    perm = torch.randperm(rows + 2, generator=gen).to(torch.int32).cuda()
+    task_w = torch.rand(rows + 2, generator=gen).cuda()
+    yw = torch.empty_like(y)
+    moe.moe_grouped_ffn_w4(c, xp, offsets, wq, task_w, perm, yw, ws)
+    a = 0
+    for e, n in enumerate(lengths):
+        if n:
+            ref, bound = ffn64(x[a:a + n].to(F64), val, "", e, act)
+            check(y[a:a + n], ref, bound, f"expert {e}")
+            w = task_w[perm[a:a + n].long()].to(F64)[:, None]
+            check(yw[a:a + n], ref * w, bound * w * (1 + 2.0 ** -20) + 2.0 ** -23 * (ref * w).abs(), f"weighted {e}")
+        a += n
+
+
+@pytest.mark.parametrize("rows", [3, 300])
+def test_scales_of_another_origin(rows):
+    gen = torch.Generator().manual_seed(rows)
+    d, f, group = 320, 256, 64
+    wq, val = make_experts(gen, 2, d, f, group, moe.SWIGLU, five_bits=False)
+    x = torch.randn(2 * rows, d, generator=gen).to(torch.bfloat16).cuda()
+    c = moe.make_config(2 * rows, d, f, 2, 1)
+    y = torch.empty(2 * rows, d, dtype=torch.float32, device="cuda")
+    moe.moe_grouped_ffn_w4(c, x, _segments([rows, rows]), wq, None, None, y, moe.w4_workspace(c))
+    for e in range(2):
+        ref, bound = ffn64(x[e * rows:(e + 1) * rows].to(F64), val, "", e, moe.SWIGLU, extra=U)
+        check(y[e * rows:(e + 1) * rows], ref, bound)
+
+
+@pytest.mark.parametrize("rows", [6, 200])
+def test_infinities_and_nan_stay_in_their_rows(rows):
+    gen = torch.Generator().manual_seed(rows + 1)
+    d, f = 256, 320
+    wq, _ = make_experts(gen, 2, d, f, 64, moe.SWIGLU)
+    x = torch.randn(2 * rows, d, generator=gen).to(torch.bfloat16).cuda()
+    bad = x.clone()
+    bad[2, 5], bad[rows + 1, 17] = float("nan"), float("inf")
+    c = moe.make_config(2 * rows, d, f, 2, 1)
+    y, yb = (torch.empty(2 * rows, d, dtype=torch.float32, device="cuda") for _ in range(2))
+    ws = moe.w4_workspace(c)
+    moe.moe_grouped_ffn_w4(c, x, _segments([rows, rows]), wq, None, None, y, ws)
+    moe.moe_grouped_ffn_w4(c, bad, _segments([rows, rows]), wq, None, None, yb, ws)
+    keep = torch.ones(2 * rows, dtype=torch.bool, device="cuda")
+    keep[2] = keep[rows + 1] = False
+    assert torch.equal(y[keep], yb[keep])
+    assert torch.isnan(yb[2]).all() and not torch.isfinite(yb[rows + 1]).all()
+
+
+def test_bad_offsets_are_reported_and_nothing_is_written():
+    gen = torch.Generator().manual_seed(3)
+    wq, _ = make_experts(gen, 3, 64, 96, 32, moe.RELU)
+    c = moe.make_config(4, 64, 96, 3, 1, act=moe.RELU)
+    x = torch.randn(4, 64, generator=gen).to(torch.bfloat16).cuda()
+    for offsets in ([0, 2, 5, 5], [0, 3, 2, 4], [-1, 1, 2, 3]):
+        ws = moe.w4_workspace(c)
+        y = torch.full((4, 64), -7.0, device="cuda")
+        moe.moe_grouped_ffn_w4(c, x, torch.tensor(offsets, dtype=torch.int32, device="cuda"), wq, None, None, y, ws)
+        assert moe.moe_read_device_status(ws) == moe.ERR_DEVICE_INDEX
+        assert torch.isfinite(y).all()
+        # the same workspace works again afterwards
+        moe.moe_grouped_ffn_w4(c, x, _segments([1, 2, 1]), wq, None, None, y, ws)
+        assert moe.moe_read_device_status(ws) == moe.OK
+
+
+def test_codes_past_4_gib():
+    """The last expert's codes lie behind the 32-bit range of bytes."""
+    m, d, f, group = 70, 8192, 15360, 128
+    assert m * f * d // 2 > 1 << 32
+    gen = torch.Generator().manual_seed(9)
+    wq = {"group": group}
+    val = {}
+    for key, rows, cols in (("gate", f, d), ("down", d, f)):
+        codes = torch.zeros(m, rows, cols // 2, dtype=torch.uint8, device="cuda")
+        scales = torch.zeros(m, cols // group, rows, dtype=torch.bfloat16, device="cuda")
+        codes[-1:], scales[-1:], val[key] = make_matrix(gen, 1, rows, cols, group)
+        wq[key], wq[key + "_scale"] = codes, scales
+    for n in (3, 150):
+        x = torch.randn(n, d, generator=gen).to(torch.bfloat16).cuda()
+        c = moe.make_config(n, d, f, m, 1, act=moe.RELU)
+        y = torch.empty(n, d, dtype=torch.float32, device="cuda")
+        moe.moe_grouped_ffn_w4(c, x, _segments([0] * (m - 1) + [n]), wq, None, None, y, moe.w4_workspace(c))
+        ref, bound = ffn64(x.to(F64), val, "", 0, moe.RELU)
+        check(y, ref, bound)
+
+
+# ------------------------------------------------------------------ the layer
+
+def layer_ref(x, idx, w, val, c, act):
+    """(out, bound) in 64 bits from the routing that the call reports."""
+    x64 = x.to(F64)
+    ref = torch.zeros_like(x64)
+    bound = torch.zeros_like(x64)
+    for e in range(c.m):
+        for s in range(c.k):
+            t = torch.nonzero(idx[:, s] == e)[:, 0]
+            if len(t):
+                y, b = ffn64(x64[t], val, "", e, act)
+                g = w[t, s].to(F64)[:, None]
+                ref[t] += g * y
+                bound[t] += g * b + 2.0 ** -22 * (g * y).abs()
+    for e in range(c.n_shared):
+        y, b = ffn64(x64, val, "sh_", e, act)
+        ref += y
+        bound += b + 2.0 ** -22 * y.abs()
+    return ref, bound + U * (ref.abs() + bound)
+
+
+def run_layer(c, x, wr, bias, wq, ws=None, stream=None):
+    ws = moe.w4_workspace(c) if ws is None else ws
+    out = torch.empty_like(x)
+    r = {"logits": torch.empty(c.T, c.m, device="cuda"),
+         "idx": torch.empty(c.T, c.k, dtype=torch.int32, device="cuda"), "w": torch.empty(c.T, c.k, device="cuda"),
+         "counts": torch.empty(c.m, dtype=torch.int32, device="cuda"), "lis": moe.lis_buffer(), "out": out, "ws": ws}
+    moe.moe_layer_forward_w4(c, x, wr, bias, wq, out, ws, logits_out=r["logits"], topk_idx_out=r["idx"],
+                             topk_w_out=r["w"], counts_out=r["counts"], lis_out=r["lis"], stream=stream)
+    return r
+
+
+LAYERS = [
+    # T, d, f, m, k, n_shared, f_shared, group, act, renormalize
+    (1, 256, 352, 8, 2, 0, 0, 128, moe.SWIGLU, True),
+    (1, 64, 64, 1, 1, 0, 0, 32, moe.RELU, False),
+    (16, 512, 1408, 64, 6, 2, 1408, 64, moe.SWIGLU, False),
+    (7, 160, 224, 5, 5, 1, 96, 32, moe.SWIGLU, True),
+    (61, 288, 544, 12, 1, 0, 0, 64, moe.RELU, False),
+    (173, 416, 352, 12, 3, 0, 0, 32, moe.RELU, False),
+    (500, 256, 224, 4, 2, 2, 160, 128, moe.SWIGLU, True),
+    (2048, 128, 160, 16, 4, 0, 0, 64, moe.SWIGLU, False),
+    (8300, 64, 96, 8, 2, 1, 64, 32, moe.SWIGLU, True),
+    (33, 128, 128, 700, 8, 0, 0, 128, moe.SWIGLU, False),
+]
+
+
+def _layer_case(case, seed=0):
+    T, d, f, m, k, ns, fs, group, act, renorm = case
+    gen = torch.Generator().manual_seed(T + d + m + seed)
+    c = moe.make_config(T, d, f, m, k, n_shared=ns, f_shared=fs, act=act, renormalize=renorm)
+    wq, val = make_experts(gen, m, d, f, group, act, ns, fs)
+    x = torch.randn(T, d, generator=gen).to(torch.bfloat16).cuda()
+    wr = (torch.randn(m, d, generator=gen) * d ** -0.5).to(torch.bfloat16).cuda()
+    bias = (-0.5 * torch.log(1 + torch.arange(m).float())).cuda()
+    return c, wq, val, x, wr, bias, act
+
+
+@pytest.mark.parametrize("case", LAYERS)
+def test_layer(case):
+    c, wq, val, x, wr, bias, act = _layer_case(case)
+    r = run_layer(c, x, wr, bias, wq)
+    assert moe.moe_read_device_status(r["ws"]) == moe.OK
+    # the router is the bf16 layer's
+    idx, w = torch.empty_like(r["idx"]), torch.empty_like(r["w"])
+    moe.moe_route(c, x, wr, bias, None, None, idx, w, moe.workspace(c))
+    assert torch.equal(idx, r["idx"]) and torch.equal(w, r["w"])
+    assert torch.equal(r["counts"].long(), torch.bincount(r["idx"].flatten().long(), minlength=c.m))
+    assert moe.unpack_lis(r["lis"])[0] == int(r["counts"].max())
+    ref, bound = layer_ref(x, r["idx"], r["w"], val, c, act)
+    check(r["out"], ref, bound)
+    # the same call again gives the same bits
+    assert torch.equal(run_layer(c, x, wr, bias, wq, ws=r["ws"])["out"], r["out"])
+
+
+def test_quantized_weights_of_a_bf16_layer():
+    """quantize_experts_w4 and the layer: against the bf16 layer run on the values that the codes stand for."""
+    gen = torch.Generator().manual_seed(21)
+    T, d, f, m, k, ns, fs = 40, 256, 384, 6, 2, 1, 192
+    dev = lambda *s: (torch.randn(*s, generator=gen) * s[-1] ** -0.5).to(torch.bfloat16).cuda()  # noqa: E731
+    w = {"gate": dev(m, f, d), "up": dev(m, f, d), "down": dev(m, d, f), "sh_gate": dev(ns, fs, d),
+         "sh_up": dev(ns, fs, d), "sh_down": dev(ns, d, fs)}
+    wq = moe.quantize_experts_w4(*w.values(), group=64)
+    val = {}
+    for key in w:
+        back = torch.empty_like(w[key])
+        moe.moe_dequantize_w4(wq[key], wq[key + "_scale"], 64, back)
+        val[key] = back
+    c = moe.make_config(T, d, f, m, k, n_shared=ns, f_shared=fs)
+    x, wr = torch.randn(T, d, generator=gen).to(torch.bfloat16).cuda(), dev(m, d)
+    r = run_layer(c, x, wr, None, wq)
+    ref, bound = layer_ref(x, r["idx"], r["w"], {key: v.to(F64) for key, v in val.items()}, c, moe.SWIGLU)
+    check(r["out"], ref, bound)
+    out = torch.empty_like(x)
+    moe.moe_layer_forward(c, x, wr, None, *(val[key] for key in ("gate", "up", "down", "sh_gate", "sh_up", "sh_down")),
+                          out, moe.workspace(c))
+    check(out, ref, bound)
+
+
+@pytest.mark.parametrize("case", [LAYERS[2], LAYERS[6]])
+def test_captured_on_a_side_stream_and_replayed(case):
+    c, wq, _, x, wr, bias, _ = _layer_case(case)
+    want = run_layer(c, x, wr, bias, wq)["out"]
+    x2 = torch.flip(x, [0]).contiguous()
+    want2 = run_layer(c, x2, wr, bias, wq)["out"]
+    xs, ws, out = x.clone(), moe.w4_workspace(c), torch.empty_like(x)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        moe.moe_layer_forward_w4(c, xs, wr, bias, wq, out, ws)
+    for src, ref in ((x, want), (x2, want2), (x, want)):
+        xs.copy_(src)
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref)
+    assert moe.moe_read_device_status(ws) == moe.OK
+
+
+def test_two_streams_with_workspaces_of_their_own():
+    c, wq, _, x, wr, bias, _ = _layer_case(LAYERS[2])
+    want = run_layer(c, x, wr, bias, wq)["out"]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [moe.w4_workspace(c) for _ in range(2)]
+    outs = [torch.empty_like(x) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, ws, out in zip(streams, spaces, outs):
+            moe.moe_layer_forward_w4(c, x, wr, bias, wq, out, ws, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(out, want) for out in outs)
+
+
+def test_fp8_refuses_and_w4_accepts_the_same_widths():
+    """d, f multiples of 32; anything else is refused before a launch."""
+    ok = moe.make_config(4, 96, 160, 3, 1)
+    assert moe.moe_w4_workspace_size(ok) > 0
+    with pytest.raises(moe.MoEError):
+        moe.moe_w4_workspace_size(moe.make_config(4, 48, 160, 3, 1))

@@ -1,0 +1,165 @@
+"""The 4-bit and norm entry points without a GPU: sizes, and every refusal that the host
+makes before it touches the device."""
+import ctypes
+
+import pytest
+
+import sparse_mixture_experts_08_b200 as moe
+from sparse_mixture_experts_08_b200.moe import MoEConfig, MoEW4Experts
+
+A = ctypes.c_void_p(1 << 24)
+ODD = ctypes.c_void_p((1 << 24) + 8)
+
+
+def test_struct_layout():
+    # int32 group, padded to the pointers' alignment, then 12 pointers
+    assert ctypes.sizeof(MoEW4Experts) == 8 + 12 * 8
+
+
+@pytest.mark.parametrize("args,code", [
+    ((-1, 8, 64, 32), moe.ERR_INVALID_ARG),
+    ((1, -8, 64, 32), moe.ERR_INVALID_ARG),
+    ((1, 8, 0, 32), moe.ERR_INVALID_ARG),
+    ((1, 8, 64, 48), moe.ERR_UNSUPPORTED),       # groups of 32, 64, 128
+    ((1, 8, 64, 0), moe.ERR_UNSUPPORTED),
+    ((1, 12, 64, 32), moe.ERR_UNSUPPORTED),      # rows % 8
+    ((1, 8, 48, 32), moe.ERR_UNSUPPORTED),       # cols % 32
+    ((65536, 8, 64, 32), moe.ERR_UNSUPPORTED),
+    ((1, 1 << 21, 64, 32), moe.ERR_UNSUPPORTED),
+    ((0, 8, 64, 32), moe.OK),                    # nothing to do
+    ((3, 0, 64, 32), moe.OK),
+])
+def test_quantizer_sizes(args, code):
+    lib = moe.moe.lib()
+    assert lib.moe_quantize_w4(*args, A if code else None, A, A, None) == code
+    assert lib.moe_dequantize_w4(*args, A if code else None, A, A, None) == code
+
+
+def test_quantizer_pointers():
+    lib = moe.moe.lib()
+    for bad in range(3):
+        for p in (None, ODD):
+            args = [A, A, A]
+            args[bad] = p
+            assert lib.moe_quantize_w4(1, 8, 64, 32, *args, None) == moe.ERR_INVALID_ARG
+            assert lib.moe_dequantize_w4(1, 8, 64, 32, *args, None) == moe.ERR_INVALID_ARG
+
+
+def _norm(rows=4, d=64, dtype=moe.BF16, eps=1e-5, x=A, residual=None, weight=A, total=None, y=A, codes=None,
+          scales=None):
+    return moe.moe.lib().moe_add_rmsnorm(rows, d, dtype, eps, x, residual, weight, total, y, codes, scales, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=-1), moe.ERR_INVALID_ARG),
+    (dict(d=0), moe.ERR_INVALID_ARG),
+    (dict(dtype=2), moe.ERR_INVALID_ARG),
+    (dict(dtype=-1), moe.ERR_INVALID_ARG),
+    (dict(eps=-1e-5), moe.ERR_INVALID_ARG),
+    (dict(eps=float("nan")), moe.ERR_INVALID_ARG),
+    (dict(eps=float("inf")), moe.ERR_INVALID_ARG),
+    (dict(y=None), moe.ERR_INVALID_ARG),                              # no output
+    (dict(codes=A), moe.ERR_INVALID_ARG),                             # codes without scales
+    (dict(scales=A), moe.ERR_INVALID_ARG),
+    (dict(x=None), moe.ERR_INVALID_ARG),
+    (dict(weight=None), moe.ERR_INVALID_ARG),
+    (dict(x=ODD), moe.ERR_INVALID_ARG),
+    (dict(residual=ODD), moe.ERR_INVALID_ARG),
+    (dict(weight=ODD), moe.ERR_INVALID_ARG),
+    (dict(total=ODD), moe.ERR_INVALID_ARG),
+    (dict(y=ODD), moe.ERR_INVALID_ARG),
+    (dict(codes=ODD, scales=A), moe.ERR_INVALID_ARG),
+    (dict(codes=A, scales=ctypes.c_void_p((1 << 24) + 2)), moe.ERR_INVALID_ARG),
+    (dict(total=ctypes.c_void_p(1 << 25), y=ctypes.c_void_p(1 << 25)), moe.ERR_INVALID_ARG),
+    (dict(d=68), moe.ERR_UNSUPPORTED),
+    (dict(d=72, codes=A, scales=A), moe.ERR_UNSUPPORTED),             # 16-byte code rows
+    (dict(d=32776), moe.ERR_UNSUPPORTED),
+    (dict(rows=0, x=None), moe.OK),
+])
+def test_norm_refusals(kw, code):
+    assert _norm(**kw) == code
+
+
+OK_CFG = (16, 256, 320, 4, 2, 1, 64, moe.BF16, moe.SWIGLU, 0)
+
+
+def test_workspace_size_and_widths():
+    lib = moe.moe.lib()
+    n = ctypes.c_size_t(0)
+    assert lib.moe_w4_workspace_size(ctypes.byref(MoEConfig(*OK_CFG)), ctypes.byref(n)) == moe.OK and n.value > 0
+    assert lib.moe_w4_workspace_size(ctypes.byref(MoEConfig(*OK_CFG)), None) == moe.ERR_INVALID_ARG
+    assert lib.moe_w4_workspace_size(None, ctypes.byref(n)) == moe.ERR_INVALID_ARG
+    for at, value, code in ((7, moe.F32, moe.ERR_UNSUPPORTED), (1, 272, moe.ERR_UNSUPPORTED),
+                            (2, 336, moe.ERR_UNSUPPORTED), (6, 80, moe.ERR_UNSUPPORTED), (0, 0, moe.ERR_INVALID_ARG),
+                            (4, 5, moe.ERR_INVALID_ARG)):
+        bad = list(OK_CFG)
+        bad[at] = value
+        assert lib.moe_w4_workspace_size(ctypes.byref(MoEConfig(*bad)), ctypes.byref(n)) == code, (at, value)
+
+
+def _experts(group=64, **kw):
+    full = {name: 1 << 24 for name, _ in MoEW4Experts._fields_[1:]}
+    full.update(kw)
+    return MoEW4Experts(group=group, **full)
+
+
+def test_layer_and_grouped_refusals():
+    lib = moe.moe.lib()
+    c = MoEConfig(*OK_CFG)
+    n = ctypes.c_size_t(0)
+    lib.moe_w4_workspace_size(ctypes.byref(c), ctypes.byref(n))
+
+    def layer(cfg=c, x=A, wr=A, w=None, out=A, ws=A, size=None):
+        w = _experts() if w is None else w
+        return lib.moe_layer_forward_w4(ctypes.byref(cfg), x, wr, None, ctypes.byref(w), out, None, None, None, None,
+                                        None, ws, n.value if size is None else size, None)
+
+    def grouped(cfg=c, x=A, off=A, w=None, task_w=None, perm=None, y=A, ws=A, size=1 << 30):
+        w = _experts() if w is None else w
+        return lib.moe_grouped_ffn_w4(ctypes.byref(cfg), x, off, ctypes.byref(w), task_w, perm, y, ws, size, None)
+
+    for kw in (dict(x=None), dict(wr=None), dict(out=None), dict(x=ODD), dict(wr=ODD), dict(out=ODD), dict(ws=None),
+               dict(ws=ctypes.c_void_p((1 << 24) + 16))):
+        assert layer(**kw) == moe.ERR_INVALID_ARG, kw
+    assert layer(size=n.value - 256) == moe.ERR_WORKSPACE
+    for kw in (dict(x=None), dict(off=None), dict(y=None), dict(task_w=A), dict(x=ODD), dict(off=ODD), dict(y=ODD),
+               dict(ws=None)):
+        assert grouped(**kw) == moe.ERR_INVALID_ARG, kw
+    assert grouped(size=1024) == moe.ERR_WORKSPACE
+    for name, _ in MoEW4Experts._fields_[1:]:
+        assert layer(w=_experts(**{name: None})) == moe.ERR_INVALID_ARG, name
+        assert layer(w=_experts(**{name: (1 << 24) + 8})) == moe.ERR_INVALID_ARG, name
+        if not name.startswith("sh_"):
+            assert grouped(w=_experts(**{name: None})) == moe.ERR_INVALID_ARG, name
+    for group in (0, 16, 96, 256, -32):
+        assert layer(w=_experts(group=group)) == moe.ERR_UNSUPPORTED
+        assert grouped(w=_experts(group=group)) == moe.ERR_UNSUPPORTED
+    assert lib.moe_layer_forward_w4(ctypes.byref(c), A, A, None, None, A, None, None, None, None, None, A, n.value,
+                                    None) == moe.ERR_INVALID_ARG
+    # ReLU experts have no up matrix, a layer without shared experts no sh_ ones: the
+    # pointers are complete, and what is refused is the workspace
+    relu = MoEConfig(16, 256, 320, 4, 2, 0, 0, moe.BF16, moe.RELU, 0)
+    bare = _experts(up=None, up_scale=None, **{k: None for k, _ in MoEW4Experts._fields_[1:] if k.startswith("sh_")})
+    assert layer(cfg=relu, w=bare, size=256) == moe.ERR_WORKSPACE
+
+
+def test_fp8_codes_refusals():
+    lib = moe.moe.lib()
+    c = MoEConfig(*OK_CFG)
+    full = moe.moe.MoEFp8Experts(**{f: 1 << 24 for f, _ in moe.moe.MoEFp8Experts._fields_})
+
+    def call(codes=A, scales=A, x=A, size=1 << 30):
+        return lib.moe_layer_forward_fp8_codes(ctypes.byref(c), x, codes, scales, A, None, ctypes.byref(full), A, None,
+                                               None, None, None, None, None, None, None, A, size, None)
+
+    for kw in (dict(codes=None), dict(scales=None), dict(codes=ODD), dict(scales=ctypes.c_void_p((1 << 24) + 2)),
+               dict(x=None)):
+        assert call(**kw) == moe.ERR_INVALID_ARG, kw
+    assert call(size=256) == moe.ERR_WORKSPACE
+
+
+def test_binding_refuses_other_types():
+    import torch
+    x = torch.zeros(2, 16, dtype=torch.float16)
+    with pytest.raises(moe.MoEError):
+        moe.moe_add_rmsnorm(x, None, x, 1e-5, x, stream=0)
