@@ -18,7 +18,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
 SOURCES = ["tc_gemm.cu", "route.cu", "simt_gemm.cu", "atomic.cu", "floe.cu", "quant.cu", "norm.cu", "w4.cu", "api.cu",
            "noalloc.cu"]
-HEADERS = [os.path.join(CSRC, "common.cuh"), os.path.join(CSRC, "atomic.cuh"), os.path.join(CSRC, "w4.cuh"),
+HEADERS = [os.path.join(CSRC, "common.cuh"), os.path.join(CSRC, "atomic.cuh"), os.path.join(CSRC, "tc.cuh"),
+           os.path.join(CSRC, "w4.cuh"),
            os.path.join(ROOT, "include", "moe.h")]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

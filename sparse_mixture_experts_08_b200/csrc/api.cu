@@ -116,7 +116,9 @@ static Layout make_layout(const moe_config_t& c, const Plan& p) {
   };
   const size_t Tk = (size_t)c.T * c.k;
   const size_t T = (size_t)c.T;
-  L.status = take(256);
+  // the status word, then (offset 256, in every layer's workspace alike) the counters of
+  // the 4-bit products: two sets that the two products of a call use in turn
+  L.status = take(256 + 2 * W4_COUNTERS * sizeof(unsigned));
   L.logits = take(T * c.m * 4);
   L.idx = take(Tk * 4);
   L.w = take(Tk * 4);
@@ -300,6 +302,7 @@ struct FfnIo {
   float* y_sh;            // [n_shared T, d]
   const Fp8Io* q8;        // 8-bit experts (nullable)
   const moe_w4_experts_t* w4;  // 4-bit experts (nullable)
+  float* w4_partial;           // and their partial sums
 };
 
 static void fill_common(GemmParams& p, int* status) {
@@ -309,6 +312,8 @@ static void fill_common(GemmParams& p, int* status) {
 
 // The two products with 4-bit expert weights (routed and shared classes in one launch
 // each); the down projection is not split over K.
+static int w4_bn(const moe_config_t& c) { return w4_pick_bn(c.T, (double)c.T * c.k / c.m); }
+
 static moe_status_t run_ffn_w4(const moe_config_t& c, const FfnIo& io, int* status, cudaStream_t s,
                                bool stage_marks) {
   const moe_w4_experts_t& w = *io.w4;
@@ -319,7 +324,11 @@ static moe_status_t run_ffn_w4(const moe_config_t& c, const FfnIo& io, int* stat
   p.group = w.group;
   p.status = status;
   p.wait_limit_ns = g_wait_limit_ns;
+  p.partial = io.w4_partial;
+  const int bn = w4_bn(c);
   for (int down = 0; down < 2; ++down) {
+    p.counters = reinterpret_cast<unsigned*>(status) + 64 + down * W4_COUNTERS;
+    p.counters_next = reinterpret_cast<unsigned*>(status) + 64 + (1 - down) * W4_COUNTERS;
     int n = 0;
     if (io.n_routed > 0) {
       W4Class& g = p.cls[n++];
@@ -354,7 +363,7 @@ static moe_status_t run_ffn_w4(const moe_config_t& c, const FfnIo& io, int* stat
     }
     p.n_classes = n;
     const int epi = down ? EPI_DOWN : swiglu ? EPI_SWIGLU : EPI_RELU;
-    MOE_CUDA(launch_w4_gemm(epi, p, c.T, (double)c.T * c.k / c.m, s));
+    MOE_CUDA(launch_w4_gemm(epi, bn, p, s));
     if (!down && stage_marks) MOE_TRY(mark_stage(5, s));
   }
   return MOE_OK;
@@ -764,6 +773,7 @@ static moe_status_t layer_forward_impl(const moe_config_t& c, const void* x, con
   FfnIo io;
   std::memset(&io, 0, sizeof(io));
   io.w4 = w4;
+  io.w4_partial = at<float>(ws, L.total);
   io.n_routed = c.m;
   io.offsets = offsets;
   io.x_perm = at<void>(ws, L.x_perm);
@@ -978,6 +988,9 @@ static moe_status_t check_w4_cfg(const moe_config_t* cfg) {
   const moe_config_t& c = *cfg;
   if (c.dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
   if (c.d % 32 || c.f % 32 || (c.n_shared && c.f_shared % 32)) return MOE_ERR_UNSUPPORTED;  // 16-byte code rows
+  // weight rows and groups are 32-bit coordinates
+  const long long n = std::max(c.m, c.n_shared), r = std::max(c.d, std::max(c.f, c.n_shared ? c.f_shared : 0));
+  if (n * r >= (1LL << 31)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -999,9 +1012,16 @@ static moe_status_t check_w4_experts(const moe_config_t& c, const moe_w4_experts
   return MOE_OK;
 }
 
+// The bf16 layer's workspace, then the partial sums.
+static size_t w4_ws_bytes(const moe_config_t& c) {
+  return make_layout(c, make_plan(c)).total + align256(w4_partial_bytes(w4_bn(c)));
+}
+
 moe_status_t moe_w4_workspace_size(const moe_config_t* cfg, size_t* bytes) {
   MOE_TRY(check_w4_cfg(cfg));
-  return moe_workspace_size(cfg, bytes);
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = w4_ws_bytes(*cfg);
+  return MOE_OK;
 }
 
 moe_status_t moe_grouped_ffn_w4(const moe_config_t* cfg, const void* x_perm, const int32_t* offsets,
@@ -1016,11 +1036,12 @@ moe_status_t moe_grouped_ffn_w4(const moe_config_t* cfg, const void* x_perm, con
     if (p && !aligned16(p)) return MOE_ERR_INVALID_ARG;
   const Plan pl = make_plan(c);
   const Layout L = make_layout(c, pl);
-  MOE_TRY(check_ws(c, ws, ws_bytes, L.h + align256((size_t)c.T * c.k * c.f * pl.es)));
+  MOE_TRY(check_ws(c, ws, ws_bytes, w4_ws_bytes(c)));
   MOE_TRY(check_device());
   FfnIo io;
   std::memset(&io, 0, sizeof(io));
   io.w4 = wq;
+  io.w4_partial = at<float>(ws, L.total);
   io.n_routed = c.m;
   io.offsets = offsets;
   io.x_perm = x_perm;
@@ -1044,7 +1065,7 @@ moe_status_t moe_layer_forward_w4(const moe_config_t* cfg, const void* x, const 
                         (const void*)topk_idx_out, (const void*)topk_w_out, (const void*)counts_out,
                         (const void*)lis_out})
     if (p && !aligned16(p)) return MOE_ERR_INVALID_ARG;
-  MOE_TRY(check_ws(c, ws, ws_bytes, make_layout(c, make_plan(c)).total));
+  MOE_TRY(check_ws(c, ws, ws_bytes, w4_ws_bytes(c)));
   MOE_TRY(check_device());
   return layer_forward_impl(c, x, w_router, bias, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, out,
                             logits_out, topk_idx_out, topk_w_out, counts_out, lis_out, nullptr, nullptr, nullptr,

@@ -10,6 +10,7 @@
 #include <algorithm>
 #include <cstring>
 
+#include "tc.cuh"
 #include "w4.cuh"
 
 namespace moe {
@@ -126,371 +127,820 @@ __global__ void __launch_bounds__(QW_WARPS * 32)
   }
 }
 
-// ------------------------------------------------------------------ products over short segments
-// y = x . W^T for a few rows of x per expert, where the codes' bytes are what counts.
+// ------------------------------------------------------------------ expert products
+// out rows = epi(rows of x . W_g^T), every group in one persistent launch, on the
+// 5th-generation tensor cores.
 //
-// A block of 16 warps takes a unit: a block of weight rows of one matrix (or of the gate
-// and up matrices together) and a tile of at most 8 NT input rows, over the whole
-// reduction length. A warp holds 32 weight rows (16 of gate and 16 of up, or 32 of down)
-// and every KW-th chunk of 128 columns; the KW warps' sums meet in shared memory. The
-// codes stream through a ring of STAGES chunks a warp filled by 16-byte asynchronous
-// copies, which runs on across units, so the loads of the next unit are in flight while
-// this one is summed up. In registers a word becomes four bf16 pairs (code - 8, exact)
-// for mma.m16n8k16 with the input rows as the N side; the fp32 sum of a group is then
-// multiplied by the group's scale in fp32, so no weight is rounded. (The matrix unit of
-// this kernel is the warp-level one: with N = 8..32 it is far from its rate, operands
-// come straight from the registers that unpack them, and no wait between warps is
-// needed; long segments go to the tcgen05 kernel.)
+// The weights are the matrix instruction's A operand (M = 256 rows over a pair of CTAs,
+// 128 in each), the segment's input rows its B operand (N = up to BN, half of them in
+// each CTA): a pair reads each input row once for 256 weight rows, and a few rows waste
+// no M tile. The codes travel as they are, HBM -> shared memory (TMA); eight warps turn
+// them into bf16 values (code - 8 is exact in bf16, times the scale is one rounding, none
+// for the quantizer's scales) and put them straight into TENSOR MEMORY, from where the
+// matrix instruction takes its A operand. So the expanded weights never touch shared
+// memory: per 128 columns of K an SM's shared memory sees 9 KB of codes and scales and
+// BN / 2 rows of x, where bf16 tiles of the same shape would bring 32 KB of weights more.
 //
-// A lane (g = lane / 4, t = lane % 4) takes the word t of each 32-column granule for the
-// rows g and g + 8, and 16 bytes of input row g at the same columns: the four pairs of a
-// word are the k pairs of two products on both sides.
-constexpr int SG_WARPS = 16;
-constexpr int SG_CHUNK = 128;                   // columns a stage
-constexpr int SG_STAGES = 4;
-constexpr int SG_CODE_BYTES = 2 * 16 * 64;      // two 16-row tiles x 64 bytes
-constexpr int SG_STAGE_BYTES = SG_CODE_BYTES + 2 * 4 * 32;  // and up to 4 groups' scales of each tile's rows
-constexpr int SG_MAX_GROUPS = 1040;
+// Tile: 256 weight rows x up to BN input rows x the whole K. SwiGLU tiles hold 128
+// features: of each CTA's 128 rows, lane quarter q (32 lanes of tensor memory) holds 16
+// gate rows, then the same features' 16 up rows, so one shuffle across 16 lanes brings a
+// feature's two sums together and one accumulator serves both matrices.
+//
+// Schedule (device side, from the segment offsets): the tiles of all groups, tallest
+// first. Whole tiles go round the pairs in alternating direction, so that pairs working
+// at the same time share an expert's rows in L2; the last one to two rounds (everything,
+// when there are fewer tiles than pairs, as in decode) are cut into equal runs of
+// 128-column chunks, one per pair. A tile cut between pairs is joined through fp32
+// partial sums in the workspace: whichever warp finishes last adds them in the order of
+// K, so the result does not depend on who that is, and no one waits.
+//
+// Warps (448 threads): 0 TMA producer, 1 matrix issuer (in the leader CTA) and owner of
+// the tensor memory, 2..5 and 6..9 expand alternate chunks, 10..13 epilogue. Barriers of
+// a stage of the ring: codes (local) -> expanders; x rows of both CTAs (at the leader) ->
+// issuer; free (both CTAs, by the issuer's commit). Barriers of the A slots in tensor
+// memory: full (at the leader, 4 warps of each CTA), free (commit). Every wait is bounded
+// in time as in tc_gemm.cu.
+constexpr int WT_BK = 128;          // columns of K a stage
+constexpr int WT_THREADS = 448;
+constexpr int WT_EXPAND_WARP = 2, WT_EPI_WARP = 10;
+constexpr int WT_SMEM_BUDGET = 196 * 1024;
+constexpr int WT_CODE_BYTES = 128 * WT_BK / 2;
+constexpr int WT_SCALE_BYTES = 1024;  // up to 4 groups x 128 rows
+constexpr int WT_A_COLS = WT_BK / 2;  // tensor-memory columns of an A slot (two bf16 each)
+constexpr int WT_MAX_GROUPS = 1040;
+constexpr int WT_MIN_SHARE = 4;       // least chunks a pair takes of the cut tiles
+constexpr unsigned long long WT_DRAIN_LIMIT_NS = 200ull * 1000 * 1000;
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+template <int BN>
+struct WtShape {
+  static constexpr int B_ROWS = BN / 2;                // input rows a CTA
+  static constexpr int BOX = BN / 8 < 8 ? 8 : BN / 8;  // input rows of a TMA box
+  static constexpr int B_HALF = B_ROWS * 128;          // 64 columns of K: 128-byte rows
+  static constexpr int STAGE_BYTES = 2 * B_HALF + WT_CODE_BYTES + WT_SCALE_BYTES;
+  static constexpr int STAGES_RAW = WT_SMEM_BUDGET / STAGE_BYTES;
+  static constexpr int STAGES = STAGES_RAW > 16 ? 16 : STAGES_RAW;
+  static constexpr int NUM_ACC = 2 * BN + 2 * WT_A_COLS <= 512 ? 2 : 1;
+  static constexpr int A_SLOTS_RAW = (512 - NUM_ACC * BN) / WT_A_COLS;
+  static constexpr int A_SLOTS = A_SLOTS_RAW > 6 ? 6 : A_SLOTS_RAW;
+  static constexpr int DYN_SMEM = STAGES * STAGE_BYTES + 1024;
+  static_assert(BN % 16 == 0 && BN >= 16 && BN <= 256 && B_ROWS % BOX == 0 && BOX % 8 == 0, "tile");
+  static_assert(STAGE_BYTES % 1024 == 0 && STAGES >= 2 && A_SLOTS >= 2, "ring");
+};
+
+struct WtMaps {
+  CUtensorMap codes[2][2], scales[2][2];  // [class][matrix]
+  CUtensorMap x[2];
+};
+
+struct WtSched {
+  long long cost_start[WT_MAX_GROUPS + 1];
+  int tile_start[WT_MAX_GROUPS + 1];
+  int gid[WT_MAX_GROUPS], rows[WT_MAX_GROUPS], brow[WT_MAX_GROUPS];
+  int total, rounds, t0;   // tiles; rounds of whole tiles; first cut tile
+  long long base, cut, per;  // cost before t0, of the cut tiles, of a pair's share
+};
+
+template <int BN>
+__device__ __forceinline__ int wt_height(int rows) {
+  const int nt = (rows + BN - 1) / BN;
+  return nt > 0 ? min(BN, (((rows + nt - 1) / nt) + 15) & ~15) : 0;
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// Cost of a chunk of a tile of `height` rows: the matrix instruction's time, at least
+// that of expanding 256 x 128 codes (as long as 64 rows take).
+__device__ __forceinline__ int wt_weight(int height) { return max(height >> 4, 4); }
+
+struct WtItem {
+  int cls, g, mt, rows, n_inst, b_row, out_row, nc, c0, c1;
+  int wa, wb;  // pairs that share the tile
+};
+
+// The list of a pair's pieces of work, walked alike by every role.
+template <int BN>
+struct WtWalk {
+  const W4Params& p;
+  const WtSched& s;
+  int G, walker, walkers, tile_f;
+  int r;
+  int t;            // next cut tile (-1: not looked up yet)
+  long long at;     // its cost, from the first cut tile on
+
+  __device__ __forceinline__ WtWalk(const W4Params& p_, const WtSched& s_, int G_, int w, int ws, int tf)
+      : p(p_), s(s_), G(G_), walker(w), walkers(ws), tile_f(tf), r(0), t(-1), at(0) {}
+
+  __device__ __forceinline__ int decode(int tile, WtItem& it) const {
+    int lo = 0, hi = G - 1;  // largest position with tile_start[pos] <= tile
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s.tile_start[mid] <= tile) lo = mid; else hi = mid - 1;
+    }
+    const int gi = s.gid[lo], G0 = p.cls[0].n_groups;
+    it.cls = gi < G0 ? 0 : 1;
+    it.g = gi - (it.cls ? G0 : 0);
+    const W4Class& c = p.cls[it.cls];
+    const int rows = s.rows[gi], NT = (rows + BN - 1) / BN, h = wt_height<BN>(rows);
+    const int local = tile - s.tile_start[lo], nt = local % NT;
+    it.mt = local / NT;
+    it.rows = min(h, rows - nt * h);
+    it.n_inst = (it.rows + 15) & ~15;
+    it.b_row = s.brow[gi] + nt * h;
+    it.out_row = (c.seg_off ? s.brow[gi] : it.g * c.out_group_stride) + nt * h;
+    it.nc = (c.K + WT_BK - 1) / WT_BK;
+    return wt_weight(h);
+  }
+
+  __device__ __forceinline__ bool next(WtItem& it) {
+    if (r < s.rounds) {
+      decode(r * walkers + ((r & 1) ? walkers - 1 - walker : walker), it);
+      ++r;
+      it.c0 = 0;
+      it.c1 = it.nc;
+      it.wa = it.wb = walker;
+      return true;
+    }
+    const long long lo = walker * s.per, hi = min(lo + s.per, s.cut);
+    if (t < 0) {
+      if (lo >= hi) return false;
+      int a = 0, b = G - 1;  // largest position with cost_start[pos] <= base + lo
+      while (a < b) {
+        const int mid = (a + b + 1) >> 1;
+        if (s.cost_start[mid] <= s.base + lo) a = mid; else b = mid - 1;
+      }
+      const int h = wt_height<BN>(s.rows[s.gid[a]]);
+      const W4Class& c = p.cls[s.gid[a] < p.cls[0].n_groups ? 0 : 1];
+      const long long tc = (long long)((c.K + WT_BK - 1) / WT_BK) * wt_weight(h);
+      const long long k = (s.base + lo - s.cost_start[a]) / tc;
+      t = s.tile_start[a] + (int)k;
+      at = s.cost_start[a] + k * tc - s.base;
+    }
+    while (at < hi) {
+      const int w = decode(t, it);
+      const long long c0 = lo > at ? (lo - at + w - 1) / w : 0, c1 = (hi - at + w - 1) / w;
+      it.c0 = (int)c0;
+      it.c1 = (int)min(c1, (long long)it.nc);
+      it.wa = (int)(at / s.per);
+      it.wb = (int)((at + (long long)(it.nc - 1) * w) / s.per);
+      at += (long long)it.nc * w;
+      ++t;
+      if (it.c0 < it.c1) return true;
+    }
+    return false;
+  }
+};
+
+// D (+)= A . B^T over the pair, A in tensor memory.
+__device__ __forceinline__ void umma_ts_pair(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(acc)
+      : "memory");
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+// Arrive on the barrier at this offset in both CTAs once every product so far completed.
+__device__ __forceinline__ void umma_commit_both(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_x32(uint32_t t, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(t),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
-__device__ __forceinline__ float lds_bf16(uint32_t a) {
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
   uint16_t v;
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-  return bf16_bits_to_f32(v);
-}
-__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                          uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  return v;
 }
 
-// Active groups in order: gid[pos], its first unit, rows and first input row.
-struct SgSched {
-  int start[SG_MAX_GROUPS + 1];
-  int gid[SG_MAX_GROUPS], rows[SG_MAX_GROUPS], brow[SG_MAX_GROUPS];
-  int n;
-};
+template <int BN, int EPI>
+__global__ void __launch_bounds__(WT_THREADS, 1)
+    w4_gemm_kernel(const __grid_constant__ WtMaps maps, const __grid_constant__ W4Params p) {
+  using S = WtShape<BN>;
+  constexpr int MATS = EPI == EPI_SWIGLU ? 2 : 1;
+  constexpr int STAGES = S::STAGES, A_SLOTS = S::A_SLOTS;
+  constexpr int TILE_F = MATS == 2 ? 128 : 256;  // output features a tile
+  __shared__ WtSched sched;
+  __shared__ __align__(8) uint64_t code_full[STAGES], x_full[STAGES], stage_free[STAGES], a_full[A_SLOTS],
+      a_free[A_SLOTS], acc_full[2], acc_free[2], drain_bar;
+  __shared__ __align__(16) __nv_bfloat16 stg[4][16][32];  // epilogue warp: 16 output rows, SwiGLU or ReLU
+  __shared__ uint32_t tmem_base_s;
+  __shared__ int abort_s;
+  extern __shared__ uint8_t dyn_smem[];
 
-struct SgUnit {
-  int cls, g, row0, tok0, ntok, brow;  // weight row of the block, input rows tok0.. (brow: of the segment)
-};
-
-template <int NT>
-__device__ __forceinline__ SgUnit sg_unit(const W4Params& p, const SgSched& s, int& pos, int u, int rpu) {
-  while (s.start[pos + 1] <= u) ++pos;
-  SgUnit r;
-  const int gi = s.gid[pos], G0 = p.cls[0].n_groups;
-  r.cls = gi < G0 ? 0 : 1;
-  r.g = gi - (r.cls ? G0 : 0);
-  const int tiles = (s.rows[pos] + 8 * NT - 1) / (8 * NT), local = u - s.start[pos];
-  r.tok0 = (local % tiles) * 8 * NT;  // a block of weights meets all its input tiles in a row (L2)
-  r.row0 = (local / tiles) * rpu;
-  r.ntok = min(8 * NT, s.rows[pos] - r.tok0);
-  r.brow = s.brow[pos];
-  return r;
-}
-
-template <int NT, int MATS, int EPI>
-__global__ void __launch_bounds__(SG_WARPS * 32, 1) w4_stream_kernel(const __grid_constant__ W4Params p, int kw_log2) {
-  constexpr int TILE_ROWS = MATS == 2 ? 16 : 32;  // output features a warp
-  constexpr int NBUF = NT <= 2 ? 2 : 1;           // buffers of partial sums
-  extern __shared__ __align__(128) uint8_t dyn[];
-  __shared__ SgSched sched;
-  uint8_t* ring_gen = dyn;
-  float* part = reinterpret_cast<float*>(dyn + SG_WARPS * SG_STAGES * SG_STAGE_BYTES);  // [NBUF][warp][8 NT][32]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int KW = 1 << kw_log2, RW = SG_WARPS >> kw_log2;
-  const int rw = warp >> kw_log2, kw = warp & (KW - 1);
-  const int rpu = RW * TILE_ROWS;  // output features a unit
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int walker = (int)cluster_id_x(), walkers = (int)nclusters_x();
+  const uint32_t smem_base = (smem_u32(dyn_smem) + 1023u) & ~1023u;
+  uint8_t* smem_gen = dyn_smem + (smem_base - smem_u32(dyn_smem));
   const int G0 = p.cls[0].n_groups, G = G0 + (p.n_classes > 1 ? p.cls[1].n_groups : 0);
+  volatile int* abort_flag = &abort_s;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(&code_full[i], 1);
+      mbar_init(&x_full[i], 1);
+      mbar_init(&stage_free[i], 1);
+    }
+    for (int i = 0; i < A_SLOTS; ++i) {
+      mbar_init(&a_full[i], 8);  // 4 expanding warps of each CTA
+      mbar_init(&a_free[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_free[i], 8);  // 4 epilogue warps of each CTA
+    }
+    mbar_init(&drain_bar, 1);
+    abort_s = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&maps.codes[0][0]);
+    tma_prefetch_desc(&maps.x[0]);
+  }
+  if (warp == 1) {
+    tmem_alloc_g<true>(&tmem_base_s, 512);
+    tmem_relinquish_g<true>();
+  }
+  __syncwarp();
+  cluster_sync_all();  // the peer's barriers are initialised before either CTA signals them
   pdl_launch_dependents();
   pdl_wait();
-  if (warp == 0) {  // the units of every group with rows: a prefix sum over 32 runs of groups
-    const int per = (G + 31) / 32, lo = lane * per, hi = min(G, lo + per);
-    int n = 0, units = 0;
-    auto seg = [&](int gi, int& rows, int& brow) {
+  // the counters of the next launch on this workspace (two sets, used in turn): zero
+  // whatever this launch, or one that was cut short, leaves in its own
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < W4_COUNTERS; i += WT_THREADS) p.counters_next[i] = 0u;
+  if (warp == 0) {
+    constexpr int NB = BN / 16 + 1;  // bucket = tile height / 16 (0: a group without rows)
+    const int per = (G + 31) / 32;
+    const int lo = min(G, lane * per), hi = min(G, lo + per);
+    auto group_tiles = [&](const int gi, const int rows) {
+      return ((p.cls[gi < G0 ? 0 : 1].R + TILE_F - 1) / TILE_F) * ((rows + BN - 1) / BN);
+    };
+    int cnt[NB], tl[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) cnt[b] = tl[b] = 0;
+    for (int gi = lo; gi < hi; ++gi) {
       const int cl = gi < G0 ? 0 : 1, g = gi - (cl ? G0 : 0);
       const W4Class& c = p.cls[cl];
+      int rows, brow;
       if (c.seg_off) {
         const int a = c.seg_off[g], b = c.seg_off[g + 1];
-        const bool bad = a < 0 || b < a || b > c.max_row;
-        if (bad) set_status(p.status, MOE_ERR_DEVICE_INDEX);
-        rows = bad ? 0 : b - a;
-        brow = bad ? 0 : a;
+        rows = b - a;
+        brow = a;
+        if (a < 0 || b < a || b > c.max_row) {
+          set_status(p.status, MOE_ERR_DEVICE_INDEX);
+          rows = brow = 0;
+        }
       } else {
         rows = c.const_rows;
         brow = g * c.b_group_stride;
       }
-      return ((rows + 8 * NT - 1) / (8 * NT)) * ((c.R + rpu - 1) / rpu);
-    };
-    for (int gi = lo; gi < hi; ++gi) {
-      int rows, brow;
-      const int k = seg(gi, rows, brow);
-      units += k;
-      n += k > 0;
+      sched.rows[gi] = rows;
+      sched.brow[gi] = brow;
+      const int key = wt_height<BN>(rows) / 16, tiles = group_tiles(gi, rows);
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        if (b == key) {
+          ++cnt[b];
+          tl[b] += tiles;
+        }
     }
-    int in = n, iu = units;
+    int base_c = 0, base_t = 0;
+#pragma unroll
+    for (int b = NB - 1; b >= 0; --b) {
+      int ic = cnt[b], itl = tl[b];
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int vc = __shfl_up_sync(0xffffffffu, ic, off), vt = __shfl_up_sync(0xffffffffu, itl, off);
+        if (lane >= off) {
+          ic += vc;
+          itl += vt;
+        }
+      }
+      const int sum_c = __shfl_sync(0xffffffffu, ic, 31), sum_t = __shfl_sync(0xffffffffu, itl, 31);
+      cnt[b] = base_c + ic - cnt[b];
+      tl[b] = base_t + itl - tl[b];
+      base_c += sum_c;
+      base_t += sum_t;
+    }
+    for (int gi = lo; gi < hi; ++gi) {
+      const int rows = sched.rows[gi];
+      const int key = wt_height<BN>(rows) / 16, tiles = group_tiles(gi, rows);
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        if (b == key) {
+          sched.gid[cnt[b]] = gi;
+          sched.tile_start[cnt[b]] = tl[b];
+          ++cnt[b];
+          tl[b] += tiles;
+        }
+    }
+    if (lane == 0) sched.tile_start[G] = base_t;
+    __syncwarp();
+    // cost before each position, and the split into whole and cut tiles
+    auto tile_cost = [&](const int gi) {
+      const int K = p.cls[gi < G0 ? 0 : 1].K;
+      return (long long)((K + WT_BK - 1) / WT_BK) * wt_weight(wt_height<BN>(sched.rows[gi]));
+    };
+    long long sum = 0;
+    for (int i = lo; i < hi; ++i)
+      sum += (sched.tile_start[i + 1] - sched.tile_start[i]) * tile_cost(sched.gid[i]);
+    long long inc = sum;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const int a = __shfl_up_sync(0xffffffffu, in, off), b = __shfl_up_sync(0xffffffffu, iu, off);
-      if (lane >= off) {
-        in += a;
-        iu += b;
-      }
+      const long long v = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += v;
     }
-    int pos = in - n, u = iu - units;
-    for (int gi = lo; gi < hi; ++gi) {
-      int rows, brow;
-      const int k = seg(gi, rows, brow);
-      if (!k) continue;
-      sched.start[pos] = u;
-      sched.gid[pos] = gi;
-      sched.rows[pos] = rows;
-      sched.brow[pos] = brow;
-      ++pos;
-      u += k;
+    long long run = inc - sum;
+    for (int i = lo; i < hi; ++i) {
+      sched.cost_start[i] = run;
+      run += (sched.tile_start[i + 1] - sched.tile_start[i]) * tile_cost(sched.gid[i]);
     }
-    if (lane == 31) {
-      // an earlier kernel of the layer flagged a device error: its tables are not used
+    if (lane == 31) sched.cost_start[G] = inc;
+    __syncwarp();
+    if (lane == 0) {
+      // an earlier kernel of the call flagged a device error: its tables are not used
       const int prior = p.status ? *reinterpret_cast<volatile int*>(p.status) : 0;
-      sched.n = prior ? 0 : in;
-      sched.start[in] = iu;
+      const int total = prior ? 0 : base_t;
+      int rounds = total / walkers;
+      if (rounds > 0 && total % walkers) --rounds;
+      const int t0 = rounds * walkers;
+      long long base = 0, cut = 0;
+      if (t0 < total) {
+        int a = 0, b = G - 1;
+        while (a < b) {
+          const int mid = (a + b + 1) >> 1;
+          if (sched.tile_start[mid] <= t0) a = mid; else b = mid - 1;
+        }
+        base = sched.cost_start[a] + (t0 - sched.tile_start[a]) * tile_cost(sched.gid[a]);
+        cut = sched.cost_start[G] - base;
+      }
+      sched.total = total;
+      sched.rounds = rounds;
+      sched.t0 = t0;
+      sched.base = base;
+      sched.cut = cut;
+      // (at least one chunk of the heaviest tile, so that every pair between a tile's
+      // first and last one has a part of it)
+      sched.per = max((cut + walkers - 1) / walkers, (long long)(WT_MIN_SHARE * max(BN / 16, 4)));
     }
   }
+  __syncwarp();
+  tc_fence_before();
   __syncthreads();
-  const int total = sched.n ? sched.start[sched.n] : 0;
-  const int gpc = SG_CHUNK / p.group;  // groups a chunk
-  const uint32_t ring = smem_u32(ring_gen) + warp * SG_STAGES * SG_STAGE_BYTES;
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_s;
+  const unsigned long long lim = p.wait_limit_ns;
+  WtWalk<BN> walk(p, sched, G, walker, walkers, TILE_F);
+  WtItem it;
+  bool ok = true;
 
-  // ---- producer state: the next chunk this warp loads
-  int pu = blockIdx.x, ppos = 0, pc = kw, pnc = 0, slot_in = 0;
-  SgUnit pun;
-  bool have = false;
-  auto issue = [&]() {
-    while (pu < total) {
-      if (!have) {
-        pun = sg_unit<NT>(p, sched, ppos, pu, rpu);
-        pnc = (p.cls[pun.cls].K + SG_CHUNK - 1) / SG_CHUNK;
-        pc = kw;
-        have = true;
-      }
-      if (pc < pnc) break;
-      have = false;
-      pu += gridDim.x;
-    }
-    if (pu < total) {
-      const W4Class& c = p.cls[pun.cls];
-      const uint32_t st = ring + slot_in * SG_STAGE_BYTES;
-      const int row0 = pun.row0 + rw * TILE_ROWS, kb = c.K >> 1;
+  if (warp == 0 && lane == 0) {
+    // ---------------------------------------------------------------- producer
+    int st = 0;
+    uint32_t ph = 0;
+    int last[STAGES];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int id = i * 32 + lane, tile = id >> 6, r = (id >> 2) & 15, gr = id & 3;
-        const int byte = pc * (SG_CHUNK / 2) + gr * 16;
-        const uint8_t* base = MATS == 2 && tile ? c.a1.codes : c.a0.codes;
-        const int row = min(row0 + (MATS == 2 ? 0 : tile * 16) + r, c.R - 1);  // rows past the matrix: not stored
-        if (byte < kb)
-          cp_async16(st + tile * 1024 + r * 64 + ((gr ^ ((r >> 1) & 3)) << 4),
-                     base + ((size_t)pun.g * c.R + row) * kb + byte);
-      }
-      if (lane < 4 * gpc) {  // [tile][group][16 rows] scales, two 16-byte halves each
-        const int half = lane & 1, tile = (lane >> 1) & 1, q = lane >> 2;
-        const int ng = (c.K + p.group - 1) / p.group, grp = pc * gpc + q;
-        const __nv_bfloat16* base = MATS == 2 && tile ? c.a1.scales : c.a0.scales;
-        const int row = min(row0 + (MATS == 2 ? 0 : tile * 16) + half * 8, c.R - 8);
-        if (grp < ng)
-          cp_async16(st + SG_CODE_BYTES + (tile * 4 + q) * 32 + half * 16,
-                     base + ((size_t)pun.g * ng + grp) * c.R + row);
-      }
-      pc += KW;
-    }
-    cp_async_commit();
-    if (++slot_in == SG_STAGES) slot_in = 0;
-  };
-#pragma unroll 1
-  for (int i = 0; i < SG_STAGES - 1; ++i) issue();
-
-  const int g8 = lane >> 2, t4 = lane & 3;
-  int cpos = 0, slot = 0, buf = 0;
-#pragma unroll 1
-  for (int u = blockIdx.x; u < total; u += gridDim.x) {
-    const SgUnit un = sg_unit<NT>(p, sched, cpos, u, rpu);
-    const W4Class& c = p.cls[un.cls];
-    const int nc = (c.K + SG_CHUNK - 1) / SG_CHUNK;
-    const int nt_n = (un.ntok + 7) >> 3;
-    float tot[2][NT][4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) tot[i][j][e] = 0.f;
-    const __nv_bfloat16* xr = c.b + (size_t)(un.brow + un.tok0 + g8) * c.K + t4 * 8;
-#pragma unroll 1
-    for (int ch = kw; ch < nc; ch += KW) {
-      cp_async_wait<SG_STAGES - 2>();
-      __syncwarp();
-      issue();  // into the slot that was read before the last __syncwarp
-      const uint32_t st = ring + slot * SG_STAGE_BYTES;
-      if (++slot == SG_STAGES) slot = 0;
-      float acc[2][NT][4];
-#pragma unroll
-      for (int gr = 0; gr < 4; ++gr) {
-        const int k = ch * SG_CHUNK + gr * 32;
-        if (k >= c.K) break;
-        if (((gr * 32) & (p.group - 1)) == 0) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
+    for (int i = 0; i < STAGES; ++i) last[i] = -1;
+    const int gpc = WT_BK / p.group;
+    while (ok && walk.next(it)) {
+      const W4Class& c = p.cls[it.cls];
+      const CUtensorMap *mc0 = &maps.codes[it.cls][0], *mc1 = &maps.codes[it.cls][1];
+      const CUtensorMap *ms0 = &maps.scales[it.cls][0], *ms1 = &maps.scales[it.cls][1], *mx = &maps.x[it.cls];
+      const int f0 = it.mt * TILE_F + (int)rank * (TILE_F / 2);
+      const bool live = f0 < c.R;  // a CTA whose rows lie behind the matrix loads no weights
+      const int ng = (c.K + p.group - 1) / p.group;
+      const int half_rows = it.n_inst >> 1, nbox = (half_rows + S::BOX - 1) / S::BOX;
+      const int x_row = it.b_row + (int)rank * half_rows;
+      for (int ch = it.c0; ch < it.c1; ++ch) {
+        if (!mbar_wait(&stage_free[st], ph ^ 1u, lim, abort_flag)) {
+          ok = false;
+          break;
         }
-        uint4 b[NT];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          b[j] = make_uint4(0u, 0u, 0u, 0u);
-          if (j * 8 + g8 < un.ntok) b[j] = *reinterpret_cast<const uint4*>(xr + (size_t)j * 8 * c.K + k);
+        uint8_t* xs = smem_gen + st * S::STAGE_BYTES;
+        uint8_t* cs = xs + 2 * S::B_HALF;
+        uint8_t* ss = cs + WT_CODE_BYTES;
+        const int halves = c.K - ch * WT_BK > 64 ? 2 : 1;
+        if (live) {
+          mbar_arrive_expect_tx(&code_full[st], WT_CODE_BYTES + gpc * 256);
+          const int y = it.g * c.R + f0, ys = it.g * ng + ch * gpc;
+          tma_load_2d(mc0, &code_full[st], cs, ch * (WT_BK / 2), y);
+          tma_load_2d(ms0, &code_full[st], ss, f0, ys);
+          if (MATS == 2) {
+            tma_load_2d(mc1, &code_full[st], cs + WT_CODE_BYTES / 2, ch * (WT_BK / 2), y);
+            tma_load_2d(ms1, &code_full[st], ss + WT_SCALE_BYTES / 2, f0, ys);
+          }
+        } else {
+          mbar_arrive(&code_full[st]);
         }
+        if (leader) mbar_arrive_expect_tx(&x_full[st], 2 * halves * nbox * S::BOX * 128);
+        const uint32_t xb = mapa_shared(smem_u32(&x_full[st]), 0);
+        for (int h = 0; h < halves; ++h)
+          for (int b = 0; b < nbox; ++b)
+            tma_load_2d_pair(mx, xb, xs + h * S::B_HALF + b * S::BOX * 128, ch * WT_BK + h * 64, x_row + b * S::BOX);
+        last[st] = (int)ph;
+        if (++st == STAGES) {
+          st = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+    if (!ok) {
+      set_status(p.status, MOE_ERR_TIMEOUT);
+      abort_s = 1;
+    }
+    // every issued copy lands before the CTA may exit (the leader's barriers count both
+    // CTAs' rows of x; the peer waits for the leader at the last cluster barrier)
+    for (int i = 0; i < STAGES; ++i)
+      if (last[i] >= 0) {
+        const volatile int never = 0;
+        if (!mbar_wait(&code_full[i], (uint32_t)last[i], WT_DRAIN_LIMIT_NS, &never) ||
+            (leader && !mbar_wait(&x_full[i], (uint32_t)last[i], WT_DRAIN_LIMIT_NS, &never)))
+          set_status(p.status, MOE_ERR_TIMEOUT);
+      }
+  } else if (warp == 1 && lane == 0 && leader) {
+    // ---------------------------------------------------------------- matrix issuer
+    int st = 0, as = 0, acc = 0;
+    uint32_t ph = 0, aph = 0, accph = 0;
+    while (ok && walk.next(it)) {
+      if (!mbar_wait(&acc_free[acc], accph ^ 1u, lim, abort_flag)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t d = tmem + (uint32_t)(acc * BN);
+      const uint32_t idesc = idesc_bf16(256, it.n_inst);
+      const int K = p.cls[it.cls].K;
+      for (int ch = it.c0; ch < it.c1; ++ch) {
+        if (!mbar_wait(&x_full[st], ph, lim, abort_flag) || !mbar_wait(&a_full[as], aph, lim, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t bd = sdesc_sw128(smem_base + st * S::STAGE_BYTES);
+        const uint32_t a = tmem + (uint32_t)(S::NUM_ACC * BN + as * WT_A_COLS);
+        const int steps = min(WT_BK / 16, (K - ch * WT_BK) >> 4);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t a = st + i * 1024 + g8 * 64 + ((gr ^ ((g8 >> 1) & 3)) << 4) + t4 * 4;
-          const uint32_t w0 = lds32(a), w1 = lds32(a + 512);
+        for (int kk = 0; kk < WT_BK / 16; ++kk)
+          if (kk < steps)
+            umma_ts_pair(d, a + 8 * kk, bd + (kk >> 2) * (S::B_HALF >> 4) + 2 * (kk & 3), idesc,
+                         (ch > it.c0 || kk > 0) ? 1u : 0u);
+        umma_commit_both(&stage_free[st]);
+        umma_commit_both(&a_free[as]);
+        if (++st == STAGES) {
+          st = 0;
+          ph ^= 1u;
+        }
+        if (++as == A_SLOTS) {
+          as = 0;
+          aph ^= 1u;
+        }
+      }
+      if (!ok) break;
+      umma_commit_both(&acc_full[acc]);
+      if (++acc == S::NUM_ACC) {
+        acc = 0;
+        accph ^= 1u;
+      }
+    }
+    if (!ok) {
+      set_status(p.status, MOE_ERR_TIMEOUT);
+      abort_s = 1;
+    }
+    umma_commit_pair(smem_u32(&drain_bar));
+    const volatile int never = 0;
+    if (!mbar_wait(&drain_bar, 0, WT_DRAIN_LIMIT_NS, &never)) set_status(p.status, MOE_ERR_TIMEOUT);
+  } else if (warp >= WT_EXPAND_WARP && warp < WT_EPI_WARP) {
+    // ---------------------------------------------------------------- expanders
+    const int grp = (warp - WT_EXPAND_WARP) >> 2, q = warp & 3;
+    const int row = MATS == 2 ? (lane >> 4) * 64 + q * 16 + (lane & 15) : q * 32 + lane;  // of the staged codes
+    const uint32_t code_off = 2 * S::B_HALF + row * (WT_BK / 2), sw = (row >> 1) & 3;
+    // scales: [matrix][group][64 rows] or [group][128 rows]
+    const uint32_t scale_off = 2 * S::B_HALF + WT_CODE_BYTES +
+                               (MATS == 2 ? (lane >> 4) * (WT_SCALE_BYTES / 2) + (q * 16 + (lane & 15)) * 2 : row * 2);
+    constexpr int SCALE_PITCH = MATS == 2 ? 128 : 256;
+    const int gl2 = 31 - __clz(p.group);
+    const uint32_t t_lane = tmem + ((uint32_t)(q * 32) << 16) + S::NUM_ACC * BN;
+    int st = 0, as = 0, turn = 0;
+    uint32_t ph = 0, aph = 0;
+    while (ok && walk.next(it)) {
+      for (int ch = it.c0; ch < it.c1; ++ch) {
+        if (turn == grp) {
+          // (the vote keeps the warp together on a failed wait)
+          if (!__all_sync(0xffffffffu, mbar_wait(&code_full[st], ph, lim, abort_flag))) {
+            ok = false;
+            break;
+          }
+          const uint32_t base = smem_base + st * S::STAGE_BYTES;
+          uint4 cw[4];
+          uint32_t sc[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            cw[i] = lds128(base + code_off + ((i ^ sw) << 4));
+            sc[i] = lds16(base + scale_off + ((i * 32) >> gl2) * SCALE_PITCH);
+          }
+          if (!__all_sync(0xffffffffu, mbar_wait(&a_free[as], aph ^ 1u, lim, abort_flag))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t a0 = w4_pair(w0 >> (8 * h)), a1 = w4_pair(w1 >> (8 * h));
-            const uint32_t a2 = w4_pair(w0 >> (8 * h + 4)), a3 = w4_pair(w1 >> (8 * h + 4));
+            uint32_t v[32];
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-              if (j < nt_n) mma_16816(acc[i][j], a0, a1, a2, a3, h ? b[j].z : b[j].x, h ? b[j].w : b[j].y);
+            for (int i = 0; i < 2; ++i) {
+              const uint4 c4 = cw[2 * h + i];
+              const uint32_t w[4] = {c4.x, c4.y, c4.z, c4.w};
+              const uint32_t ss = sc[2 * h + i] * 0x10001u;
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[i * 16 + j * 4 + e] = mul_bf16x2(w4_pair(w[j] >> (4 * e)), ss);
+            }
+            tmem_st_x32(t_lane + as * WT_A_COLS + h * 32, v);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (leader)
+              mbar_arrive(&a_full[as]);
+            else
+              mbar_arrive_cluster(mapa_shared(smem_u32(&a_full[as]), 0));
           }
         }
-        if ((((gr + 1) * 32) & (p.group - 1)) == 0 || k + 32 >= c.K) {  // the group (or the row) ends
-          const int q = (gr * 32) / p.group;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t a = st + SG_CODE_BYTES + (i * 4 + q) * 32 + g8 * 2;
-            const float s0 = lds_bf16(a), s1 = lds_bf16(a + 16);
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              tot[i][j][0] = fmaf(acc[i][j][0], s0, tot[i][j][0]);
-              tot[i][j][1] = fmaf(acc[i][j][1], s0, tot[i][j][1]);
-              tot[i][j][2] = fmaf(acc[i][j][2], s1, tot[i][j][2]);
-              tot[i][j][3] = fmaf(acc[i][j][3], s1, tot[i][j][3]);
+        turn ^= 1;
+        if (++st == STAGES) {
+          st = 0;
+          ph ^= 1u;
+        }
+        if (++as == A_SLOTS) {
+          as = 0;
+          aph ^= 1u;
+        }
+      }
+    }
+    if (!ok) {
+      set_status(p.status, MOE_ERR_TIMEOUT);
+      abort_s = 1;
+    }
+  } else if (warp >= WT_EPI_WARP) {
+    // ---------------------------------------------------------------- epilogue
+    const int q = warp & 3;
+    int acc = 0;
+    uint32_t accph = 0;
+    while (ok && walk.next(it)) {
+      const W4Class& c = p.cls[it.cls];
+      const int f0 = it.mt * TILE_F + (int)rank * (TILE_F / 2);
+      const int rows = it.rows;
+      // 16 rows' sums of this lane's weight row -> output rows [c0, c0 + 16)
+      auto emit = [&](const int c0, const float (&v)[16]) {
+        const int jn = min(16, rows - c0);
+        if (EPI == EPI_DOWN) {
+          const int feat = f0 + q * 32 + lane;
+          const long long r0 = it.out_row + c0;
+          float wv = 1.f;
+          if (lane < jn) {
+            if (c.row_w) {
+              wv = c.row_w[r0 + lane];
+            } else if (c.task_w) {
+              const int qk = c.perm[r0 + lane];
+              wv = qk >= 0 && qk < c.max_row ? c.task_w[qk] : 0.f;
             }
           }
+          float* o = reinterpret_cast<float*>(c.out) + r0 * c.R + feat;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float w = __shfl_sync(0xffffffffu, wv, j);
+            if (j < jn && feat < c.R) o[(long long)j * c.R] = v[j] * w;
+          }
+        } else if (EPI == EPI_SWIGLU) {
+          // lanes 0..15 hold the gate sums of 16 features, lanes 16..31 their up sums: the
+          // lower half takes the even rows, the upper half the odd ones
+          const bool up = lane >= 16;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float got = __shfl_xor_sync(0xffffffffu, up ? v[2 * j] : v[2 * j + 1], 16);
+            const float g = up ? got : v[2 * j], u = up ? v[2 * j + 1] : got;
+            // h is rounded to bf16: it is the next product's tensor-core operand
+            stg[q][2 * j + up][lane & 15] = __float2bfloat16_rn(__fdividef(g, 1.f + __expf(-g)) * u);
+          }
+          __syncwarp();
+          const int j = lane >> 1, f = f0 + q * 16 + (lane & 1) * 8;
+          if (j < jn && f < c.R)
+            *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(c.out) + (long long)(it.out_row + c0 + j) * c.R +
+                                      f) = *reinterpret_cast<const uint4*>(&stg[q][j][(lane & 1) * 8]);
+          __syncwarp();
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) stg[q][j][lane] = __float2bfloat16_rn(v[j] < 0.f ? 0.f : v[j]);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int j = (lane >> 2) + 8 * i, f = f0 + q * 32 + (lane & 3) * 8;
+            if (j < jn && f < c.R)
+              *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(c.out) +
+                                        (long long)(it.out_row + c0 + j) * c.R + f) =
+                  *reinterpret_cast<const uint4*>(&stg[q][j][(lane & 3) * 8]);
+          }
+          __syncwarp();
         }
+      };
+      const bool whole = it.wa == it.wb;
+      // this warp's part of a pair's partial sums: [row][128 lanes]
+      auto part_of = [&](const int w, const int slot) {
+        return p.partial + ((((size_t)w * 2 + slot) * 2 + rank) * BN) * 128 + q * 32 + lane;
+      };
+      float* mine = whole ? nullptr : part_of(walker, it.wa < walker ? 0 : 1);
+      if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[acc], accph, lim, abort_flag))) {
+        ok = false;
+        break;
       }
-    }
-    // the KW partial sums of each output meet in shared memory, in fragment order
-    float* pw = part + ((size_t)buf * SG_WARPS + warp) * (8 * NT * 32) + lane;
+      tc_fence_after();
+      const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
+      uint32_t ra[16], rb[16];
+      auto use = [&](const int c0, const uint32_t (&r)[16]) {
+        float v[16];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
+        if (whole) {
+          emit(c0, v);
+        } else {
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) pw[((i * NT + j) * 4 + e) * 32] = tot[i][j][e];
-    __syncthreads();
-    // frag f = (tile, j, e): one warp-wide run of 32 values a fragment and source warp
-    constexpr int FR = 4 * NT * (MATS == 2 ? 1 : 2);  // output fragments a row block
-    const float* pb = part + (size_t)buf * SG_WARPS * (8 * NT * 32) + lane;
+          for (int j = 0; j < 16; ++j) __stcg(mine + (c0 + j) * 128, v[j]);
+        }
+        __syncwarp();
+      };
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (leader)
+            mbar_arrive_relaxed(&acc_free[acc]);
+          else
+            mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&acc_free[acc]), 0));
+        }
+      };
+      // the loads of one 16-column chunk are in flight while the one before is used
+      tmem_ld_x16(t_row, ra);
 #pragma unroll 1
-    for (int id = warp; id < RW * FR; id += SG_WARPS) {
-      const int rb = id / FR, f = id % FR;
-      const int tile = MATS == 2 ? 0 : f / (4 * NT), j = (f / 4) % NT, e = f & 3;
-      const int tok = j * 8 + 2 * t4 + (e & 1);
-      const int feat = un.row0 + rb * TILE_ROWS + tile * 16 + g8 + ((e & 2) ? 8 : 0);
-      if (tok >= un.ntok || feat >= c.R) continue;
-      const float* q = pb + (size_t)(rb << kw_log2) * (8 * NT * 32);
-      float v0 = 0.f, v1 = 0.f;
-#pragma unroll 4
-      for (int w = 0; w < KW; ++w) {
-        v0 += q[(size_t)w * (8 * NT * 32) + f * 32];
-        if (MATS == 2) v1 += q[(size_t)w * (8 * NT * 32) + (4 * NT + f) * 32];
+      for (int c0 = 0; c0 < rows; c0 += 32) {
+        tmem_ld_wait_keep(ra);
+        if (c0 + 16 < rows) tmem_ld_x16(t_row + c0 + 16, rb); else release();
+        use(c0, ra);
+        if (c0 + 16 >= rows) break;
+        tmem_ld_wait_keep(rb);
+        if (c0 + 32 < rows) tmem_ld_x16(t_row + c0 + 32, ra); else release();
+        use(c0 + 16, rb);
       }
-      const long long orow =
-          (long long)(c.seg_off ? un.brow : un.g * c.out_group_stride) + un.tok0 + tok;
-      if (EPI == EPI_DOWN) {
-        float wgt = 1.f;
-        if (c.row_w) {
-          wgt = c.row_w[orow];
-        } else if (c.task_w) {
-          const int qk = c.perm[orow];
-          wgt = qk >= 0 && qk < c.max_row ? c.task_w[qk] : 0.f;
+      if (++acc == S::NUM_ACC) {
+        acc = 0;
+        accph ^= 1u;
+      }
+      if (!whole) {
+        // the last of the tile's pairs to get here adds the parts, in the order of K
+        __threadfence();
+        __syncwarp();
+        unsigned n = 0;
+        if (lane == 0) n = atomicAdd(&p.counters[(it.wa * 2 + (int)rank) * 4 + q], 1u);
+        n = __shfl_sync(0xffffffffu, n, 0);
+        if (n == (unsigned)(it.wb - it.wa)) {
+          __threadfence();
+#pragma unroll 1
+          for (int c0 = 0; c0 < rows; c0 += 16) {
+            float v[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = 0.f;
+#pragma unroll 1
+            for (int w = it.wa; w <= it.wb; ++w) {
+              const float* o = part_of(w, w == it.wa ? 1 : 0) + c0 * 128;
+#pragma unroll
+              for (int j = 0; j < 16; ++j) v[j] += __ldcg(o + j * 128);
+            }
+            emit(c0, v);
+          }
         }
-        reinterpret_cast<float*>(c.out)[orow * c.R + feat] = v0 * wgt;
-      } else {
-        // h is rounded to bf16: it is the next product's tensor-core operand
-        const float h = EPI == EPI_SWIGLU ? v0 / (1.f + __expf(-v0)) * v1 : (v0 < 0.f ? 0.f : v0);
-        reinterpret_cast<__nv_bfloat16*>(c.out)[orow * c.R + feat] = __float2bfloat16_rn(h);
       }
     }
-    if (NBUF == 2)
-      buf ^= 1;  // the next write of this buffer is two barriers away
-    else
-      __syncthreads();
+    if (!ok) {
+      set_status(p.status, MOE_ERR_TIMEOUT);
+      abort_s = 1;
+    }
   }
-  cp_async_wait<0>();
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // neither CTA leaves while the other may signal it or read its memory
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_g<true>(tmem, 512);
+  }
 }
 
-template <int NT, int MATS, int EPI>
-cudaError_t launch_stream(const W4Params& p, int kw_log2, cudaStream_t s) {
-  constexpr size_t SMEM = SG_WARPS * SG_STAGES * SG_STAGE_BYTES +
-                          (NT <= 2 ? 2 : 1) * SG_WARPS * (8 * NT * 32) * sizeof(float);
-  auto kern = w4_stream_kernel<NT, MATS, EPI>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
+bool make_map_2d(CUtensorMap* m, const void* ptr, CUtensorMapDataType type, long long inner, long long rows,
+                 long long pitch, int box_inner, int box_rows, CUtensorMapSwizzle swizzle) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc || !ptr || inner <= 0 || rows <= 0 || pitch % 16) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)pitch};
+  const cuuint32_t box[2] = {(cuuint32_t)box_inner, (cuuint32_t)box_rows}, es[2] = {1, 1};
+  return enc(m, type, 2, const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BN, int EPI>
+cudaError_t launch_impl(const W4Params& p, cudaStream_t s) {
+  using S = WtShape<BN>;
+  constexpr int MATS = EPI == EPI_SWIGLU ? 2 : 1, ROWS = MATS == 2 ? 64 : 128;
+  WtMaps maps;
+  for (int i = 0; i < 2; ++i) {
+    const W4Class& c = p.cls[i < p.n_classes ? i : 0];
+    const int ng = (c.K + p.group - 1) / p.group;
+    for (int j = 0; j < 2; ++j) {
+      const W4Matrix& a = MATS == 2 && j ? c.a1 : c.a0;
+      if (!make_map_2d(&maps.codes[i][j], a.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.K / 2, (long long)c.n_groups * c.R,
+                       c.K / 2, WT_BK / 2, ROWS, CU_TENSOR_MAP_SWIZZLE_64B) ||
+          !make_map_2d(&maps.scales[i][j], a.scales, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, c.R, (long long)c.n_groups * ng,
+                       2LL * c.R, ROWS, WT_BK / p.group, CU_TENSOR_MAP_SWIZZLE_NONE))
+        return cudaErrorInvalidValue;
+    }
+    if (!make_map_2d(&maps.x[i], c.b, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, c.K, c.b_rows, 2LL * c.K, 64, S::BOX,
+                     CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+  }
+  auto kern = w4_gemm_kernel<BN, EPI>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(WT_THREADS);
+  cfg.dynamicSmemBytes = S::DYN_SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  static int max_pairs[64] = {0};  // a device: pairs that can be resident at once
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  e = launch_k(kern, dim3(num_sms()), dim3(SG_WARPS * 32), SMEM, s, p, kw_log2);
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!max_pairs[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::DYN_SMEM);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(num_sms() & ~1);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;  // the occupancy query takes the cluster shape alone
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+    if (e != cudaSuccess) return e;
+    max_pairs[dev] = std::max(1, std::min(n, W4_MAX_PAIRS));
+  }
+  cfg.gridDim = dim3(2 * max_pairs[dev]);
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, kern, maps, p);
   count_launch();
   return e;
 }
 
-// The 16 warps of a block split the reduction KW ways and the rows 16 / KW ways. KW is
-// the power of two that leaves the fewest chunk slots unused (chunks of the last round),
-// the larger one on a tie: units of fewer rows spread more evenly over the SMs.
-int pick_kw_log2(const W4Params& p) {
-  int best = 4;
-  double best_cost = 1e30;
-  for (int l = 4; l >= 1; --l) {
-    const int nc = (p.cls[0].K + SG_CHUNK - 1) / SG_CHUNK, kw = 1 << l;
-    const double cost = (double)((nc + kw - 1) / kw * kw) / nc;
-    if (cost < best_cost - 1e-9) {
-      best_cost = cost;
-      best = l;
-    }
-  }
-  return best;
-}
-
 }  // namespace
 
-cudaError_t launch_w4_gemm(int epi, const W4Params& p, int max_rows, double avg_rows, cudaStream_t s) {
-  const int kw = pick_kw_log2(p);
-  (void)avg_rows;
-#define MOE_W4_STREAM(NT_)                                                                 \
-  do {                                                                                     \
-    if (epi == EPI_SWIGLU) return launch_stream<NT_, 2, EPI_SWIGLU>(p, kw, s);             \
-    if (epi == EPI_RELU) return launch_stream<NT_, 1, EPI_RELU>(p, kw, s);                 \
-    if (epi == EPI_DOWN) return launch_stream<NT_, 1, EPI_DOWN>(p, kw, s);                 \
-    return cudaErrorInvalidValue;                                                          \
-  } while (0)
-  if (max_rows <= 8) MOE_W4_STREAM(1);
-  if (max_rows <= 16) MOE_W4_STREAM(2);
-  MOE_W4_STREAM(4);
-#undef MOE_W4_STREAM
+// Input rows a tile: enough for most segments to be one tile (every further tile of a
+// segment expands the expert's weights again), no more than that (a stage's bytes).
+int w4_pick_bn(long long T, double avg_rows) {
+  const double want = std::min((double)T, 2.5 * avg_rows);
+  return want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : want <= 128 ? 128 : 256;
+}
+
+size_t w4_partial_bytes(int bn) { return (size_t)W4_MAX_PAIRS * 2 * 2 * bn * 128 * sizeof(float); }
+
+cudaError_t launch_w4_gemm(int epi, int bn, const W4Params& p, cudaStream_t s) {
+#define MOE_W4_CASE(BN_)                                                  \
+  if (bn == BN_) {                                                        \
+    if (epi == EPI_SWIGLU) return launch_impl<BN_, EPI_SWIGLU>(p, s);     \
+    if (epi == EPI_RELU) return launch_impl<BN_, EPI_RELU>(p, s);         \
+    if (epi == EPI_DOWN) return launch_impl<BN_, EPI_DOWN>(p, s);         \
+  }
+  MOE_W4_CASE(16)
+  MOE_W4_CASE(32)
+  MOE_W4_CASE(64)
+  MOE_W4_CASE(128)
+  MOE_W4_CASE(256)
+#undef MOE_W4_CASE
+  return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_quantize_w4(long long n, int rows, int cols, int group, const void* src, uint8_t* codes,

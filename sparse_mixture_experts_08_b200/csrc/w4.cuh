@@ -36,17 +36,24 @@ struct W4Class {
   const int* perm;
 };
 
+constexpr int W4_MAX_PAIRS = 80;                 // CTA pairs of a launch
+constexpr int W4_COUNTERS = W4_MAX_PAIRS * 2 * 4;  // [pair][CTA][lane quarter]
+
 struct W4Params {
   W4Class cls[2];
   int n_classes;
   int group;    // 32, 64 or 128
+  float* partial;            // w4_partial_bytes(): sums of tiles that pairs of CTAs share
+  unsigned* counters;        // [W4_COUNTERS], zero: warps that have left their sums of a tile
+  unsigned* counters_next;   // [W4_COUNTERS]: zeroed here, used by the next launch
   int* status;
   unsigned long long wait_limit_ns;
 };
 
-// max_rows: an upper bound on a group's rows that the host knows (the batch); avg_rows:
-// the routed segments' mean length.
-cudaError_t launch_w4_gemm(int epi, const W4Params& p, int max_rows, double avg_rows, cudaStream_t s);
+// Input rows of a tile (16 .. 256) for segments of at most T and on average avg_rows rows.
+int w4_pick_bn(long long T, double avg_rows);
+size_t w4_partial_bytes(int bn);
+cudaError_t launch_w4_gemm(int epi, int bn, const W4Params& p, cudaStream_t s);
 cudaError_t launch_quantize_w4(long long n, int rows, int cols, int group, const void* src, uint8_t* codes,
                                void* scales, cudaStream_t s);
 cudaError_t launch_dequantize_w4(long long n, int rows, int cols, int group, const uint8_t* codes, const void* scales,
