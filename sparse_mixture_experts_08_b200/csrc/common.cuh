@@ -62,6 +62,16 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, unsign
 }
 
 
+// The same wait for pipelines that hand over every few hundred cycles: the first polls do
+// without the abort flag and the clock, whose reads alone cost about as much.
+__device__ __forceinline__ bool mbar_wait_poll(uint64_t* bar, uint32_t parity, unsigned long long limit_ns,
+                                               const volatile int* abort_flag) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, limit_ns, abort_flag);
+}
+
 // Bulk copy global -> shared (the copy engine, no tensor map): bytes % 16 == 0, both
 // addresses 16-byte aligned; completion counted on `bar`.
 __device__ __forceinline__ void bulk_copy_g2s(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {

@@ -154,15 +154,15 @@ __global__ void __launch_bounds__(QW_WARPS * 32)
 // partial sums in the workspace: whichever warp finishes last adds them in the order of
 // K, so the result does not depend on who that is, and no one waits.
 //
-// Warps (448 threads): 0 TMA producer, 1 matrix issuer (in the leader CTA) and owner of
-// the tensor memory, 2..5 and 6..9 expand alternate chunks, 10..13 epilogue. Barriers of
+// Warps (480 threads): 0 and 14 TMA producers, 1 matrix issuer (in the leader CTA) and
+// owner of the tensor memory, 2..5 and 6..9 expand alternate chunks, 10..13 epilogue. Barriers of
 // a stage of the ring: codes (local) -> expanders; x rows of both CTAs (at the leader) ->
 // issuer; free (both CTAs, by the issuer's commit). Barriers of the A slots in tensor
 // memory: full (at the leader, 4 warps of each CTA), free (commit). Every wait is bounded
 // in time as in tc_gemm.cu.
 constexpr int WT_BK = 128;          // columns of K a stage
-constexpr int WT_THREADS = 448;
-constexpr int WT_EXPAND_WARP = 2, WT_EPI_WARP = 10;
+constexpr int WT_THREADS = 480;
+constexpr int WT_EXPAND_WARP = 2, WT_EPI_WARP = 10, WT_X_WARP = 14;
 constexpr int WT_SMEM_BUDGET = 196 * 1024;
 constexpr int WT_CODE_BYTES = 128 * WT_BK / 2;
 constexpr int WT_SCALE_BYTES = 1024;  // up to 4 groups x 128 rows
@@ -341,7 +341,9 @@ __global__ void __launch_bounds__(WT_THREADS, 1)
   __shared__ int abort_s;
   extern __shared__ uint8_t dyn_smem[];
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (the shuffle tells the compiler that the role is the whole warp's: loop state and
+  // descriptors then live in uniform registers)
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const int walker = (int)cluster_id_x(), walkers = (int)nclusters_x();
@@ -508,50 +510,59 @@ __global__ void __launch_bounds__(WT_THREADS, 1)
   WtItem it;
   bool ok = true;
 
-  if (warp == 0 && lane == 0) {
-    // ---------------------------------------------------------------- producer
-    int st = 0;
+  if (warp == 0 || warp == WT_X_WARP) {
+    // ---------------------------------------------------------------- producers
+    // Warp 0 fetches codes and scales, WT_X_WARP the input rows (one warp's issue slots
+    // would bound the short tiles). As in the issuer, the whole warp walks and waits and
+    // one lane issues.
+    const bool codes = warp == 0;
+    int st = 0, used = 0;
     uint32_t ph = 0;
-    int last[STAGES];
-#pragma unroll
-    for (int i = 0; i < STAGES; ++i) last[i] = -1;
     const int gpc = WT_BK / p.group;
     while (ok && walk.next(it)) {
       const W4Class& c = p.cls[it.cls];
-      const CUtensorMap *mc0 = &maps.codes[it.cls][0], *mc1 = &maps.codes[it.cls][1];
-      const CUtensorMap *ms0 = &maps.scales[it.cls][0], *ms1 = &maps.scales[it.cls][1], *mx = &maps.x[it.cls];
-      const int f0 = it.mt * TILE_F + (int)rank * (TILE_F / 2);
+      const int K = c.K, f0 = it.mt * TILE_F + (int)rank * (TILE_F / 2);
       const bool live = f0 < c.R;  // a CTA whose rows lie behind the matrix loads no weights
-      const int ng = (c.K + p.group - 1) / p.group;
+      const int y = it.g * c.R + f0, ys = it.g * ((K + p.group - 1) / p.group);
       const int half_rows = it.n_inst >> 1, nbox = (half_rows + S::BOX - 1) / S::BOX;
       const int x_row = it.b_row + (int)rank * half_rows;
       for (int ch = it.c0; ch < it.c1; ++ch) {
-        if (!mbar_wait(&stage_free[st], ph ^ 1u, lim, abort_flag)) {
+        if (!__all_sync(0xffffffffu, mbar_wait_poll(&stage_free[st], ph ^ 1u, lim, abort_flag))) {
           ok = false;
           break;
         }
         uint8_t* xs = smem_gen + st * S::STAGE_BYTES;
-        uint8_t* cs = xs + 2 * S::B_HALF;
-        uint8_t* ss = cs + WT_CODE_BYTES;
-        const int halves = c.K - ch * WT_BK > 64 ? 2 : 1;
-        if (live) {
-          mbar_arrive_expect_tx(&code_full[st], WT_CODE_BYTES + gpc * 256);
-          const int y = it.g * c.R + f0, ys = it.g * ng + ch * gpc;
-          tma_load_2d(mc0, &code_full[st], cs, ch * (WT_BK / 2), y);
-          tma_load_2d(ms0, &code_full[st], ss, f0, ys);
-          if (MATS == 2) {
-            tma_load_2d(mc1, &code_full[st], cs + WT_CODE_BYTES / 2, ch * (WT_BK / 2), y);
-            tma_load_2d(ms1, &code_full[st], ss + WT_SCALE_BYTES / 2, f0, ys);
+        if (elect_one()) {
+          if (codes) {
+            uint8_t* cs = xs + 2 * S::B_HALF;
+            uint8_t* ss = cs + WT_CODE_BYTES;
+            if (live) {
+              mbar_arrive_expect_tx(&code_full[st], WT_CODE_BYTES + gpc * 256);
+              tma_load_2d(&maps.codes[it.cls][0], &code_full[st], cs, ch * (WT_BK / 2), y);
+              if (MATS == 2)
+                tma_load_2d(&maps.codes[it.cls][1], &code_full[st], cs + WT_CODE_BYTES / 2, ch * (WT_BK / 2), y);
+              tma_load_2d(&maps.scales[it.cls][0], &code_full[st], ss, f0, ys + ch * gpc);
+              if (MATS == 2)
+                tma_load_2d(&maps.scales[it.cls][1], &code_full[st], ss + WT_SCALE_BYTES / 2, f0, ys + ch * gpc);
+            } else {
+              mbar_arrive(&code_full[st]);
+            }
+          } else {
+            const int halves = K - ch * WT_BK > 64 ? 2 : 1;
+            if (leader) mbar_arrive_expect_tx(&x_full[st], 2 * halves * nbox * S::BOX * 128);
+            const uint32_t xb = mapa_shared(smem_u32(&x_full[st]), 0);
+#pragma unroll
+            for (int b = 0; b < S::B_ROWS / S::BOX; ++b)
+              if (b < nbox) {
+                tma_load_2d_pair(&maps.x[it.cls], xb, xs + b * S::BOX * 128, ch * WT_BK, x_row + b * S::BOX);
+                if (halves == 2)
+                  tma_load_2d_pair(&maps.x[it.cls], xb, xs + S::B_HALF + b * S::BOX * 128, ch * WT_BK + 64,
+                                   x_row + b * S::BOX);
+              }
           }
-        } else {
-          mbar_arrive(&code_full[st]);
         }
-        if (leader) mbar_arrive_expect_tx(&x_full[st], 2 * halves * nbox * S::BOX * 128);
-        const uint32_t xb = mapa_shared(smem_u32(&x_full[st]), 0);
-        for (int h = 0; h < halves; ++h)
-          for (int b = 0; b < nbox; ++b)
-            tma_load_2d_pair(mx, xb, xs + h * S::B_HALF + b * S::BOX * 128, ch * WT_BK + h * 64, x_row + b * S::BOX);
-        last[st] = (int)ph;
+        __syncwarp();
+        ++used;
         if (++st == STAGES) {
           st = 0;
           ph ^= 1u;
@@ -563,66 +574,81 @@ __global__ void __launch_bounds__(WT_THREADS, 1)
       abort_s = 1;
     }
     // every issued copy lands before the CTA may exit (the leader's barriers count both
-    // CTAs' rows of x; the peer waits for the leader at the last cluster barrier)
-    for (int i = 0; i < STAGES; ++i)
-      if (last[i] >= 0) {
+    // CTAs' rows of x; the peer waits for the leader at the last cluster barrier): the
+    // last use of stage i was fill number (used - 1 - i) / STAGES of it
+    if (lane == 0 && (codes || leader))
+      for (int i = 0; i < STAGES && i < used; ++i) {
         const volatile int never = 0;
-        if (!mbar_wait(&code_full[i], (uint32_t)last[i], WT_DRAIN_LIMIT_NS, &never) ||
-            (leader && !mbar_wait(&x_full[i], (uint32_t)last[i], WT_DRAIN_LIMIT_NS, &never)))
+        if (!mbar_wait(codes ? &code_full[i] : &x_full[i], (uint32_t)((used - 1 - i) / STAGES) & 1u,
+                       WT_DRAIN_LIMIT_NS, &never))
           set_status(p.status, MOE_ERR_TIMEOUT);
       }
-  } else if (warp == 1 && lane == 0 && leader) {
+  } else if (warp == 1) {
     // ---------------------------------------------------------------- matrix issuer
-    int st = 0, as = 0, acc = 0;
-    uint32_t ph = 0, aph = 0, accph = 0;
-    while (ok && walk.next(it)) {
-      if (!mbar_wait(&acc_free[acc], accph ^ 1u, lim, abort_flag)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      const uint32_t d = tmem + (uint32_t)(acc * BN);
-      const uint32_t idesc = idesc_bf16(256, it.n_inst);
-      const int K = p.cls[it.cls].K;
-      for (int ch = it.c0; ch < it.c1; ++ch) {
-        if (!mbar_wait(&x_full[st], ph, lim, abort_flag) || !mbar_wait(&a_full[as], aph, lim, abort_flag)) {
+    if (leader) {
+      int st = 0, as = 0, acc = 0;
+      uint32_t ph = 0, aph = 0, accph = 0;
+      while (ok && walk.next(it)) {
+        if (!__all_sync(0xffffffffu, mbar_wait_poll(&acc_free[acc], accph ^ 1u, lim, abort_flag))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint64_t bd = sdesc_sw128(smem_base + st * S::STAGE_BYTES);
-        const uint32_t a = tmem + (uint32_t)(S::NUM_ACC * BN + as * WT_A_COLS);
-        const int steps = min(WT_BK / 16, (K - ch * WT_BK) >> 4);
+        const uint32_t d = tmem + (uint32_t)(acc * BN);
+        const uint32_t idesc = idesc_bf16(256, it.n_inst);
+        const int K = p.cls[it.cls].K;
+        for (int ch = it.c0; ch < it.c1; ++ch) {
+          if (!__all_sync(0xffffffffu, mbar_wait_poll(&x_full[st], ph, lim, abort_flag) &&
+                                           mbar_wait_poll(&a_full[as], aph, lim, abort_flag))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t bd = sdesc_sw128(smem_base + st * S::STAGE_BYTES);
+            const uint32_t a = tmem + (uint32_t)(S::NUM_ACC * BN + as * WT_A_COLS);
+            const int left = K - ch * WT_BK;
+            if (left >= WT_BK) {
 #pragma unroll
-        for (int kk = 0; kk < WT_BK / 16; ++kk)
-          if (kk < steps)
-            umma_ts_pair(d, a + 8 * kk, bd + (kk >> 2) * (S::B_HALF >> 4) + 2 * (kk & 3), idesc,
-                         (ch > it.c0 || kk > 0) ? 1u : 0u);
-        umma_commit_both(&stage_free[st]);
-        umma_commit_both(&a_free[as]);
-        if (++st == STAGES) {
-          st = 0;
-          ph ^= 1u;
+              for (int kk = 0; kk < WT_BK / 16; ++kk)
+                umma_ts_pair(d, a + 8 * kk, bd + (kk >> 2) * (S::B_HALF >> 4) + 2 * (kk & 3), idesc,
+                             kk > 0 ? 1u : (uint32_t)(ch > it.c0));
+            } else {
+#pragma unroll 1
+              for (int kk = 0; kk < (left >> 4); ++kk)
+                umma_ts_pair(d, a + 8 * kk, bd + (kk >> 2) * (S::B_HALF >> 4) + 2 * (kk & 3), idesc,
+                             (ch > it.c0 || kk > 0) ? 1u : 0u);
+            }
+            umma_commit_both(&stage_free[st]);
+            umma_commit_both(&a_free[as]);
+            if (ch + 1 == it.c1) umma_commit_both(&acc_full[acc]);
+          }
+          __syncwarp();
+          if (++st == STAGES) {
+            st = 0;
+            ph ^= 1u;
+          }
+          if (++as == A_SLOTS) {
+            as = 0;
+            aph ^= 1u;
+          }
         }
-        if (++as == A_SLOTS) {
-          as = 0;
-          aph ^= 1u;
+        if (!ok) break;
+        if (++acc == S::NUM_ACC) {
+          acc = 0;
+          accph ^= 1u;
         }
       }
-      if (!ok) break;
-      umma_commit_both(&acc_full[acc]);
-      if (++acc == S::NUM_ACC) {
-        acc = 0;
-        accph ^= 1u;
+      if (!ok) {
+        set_status(p.status, MOE_ERR_TIMEOUT);
+        abort_s = 1;
+      }
+      if (elect_one()) {
+        umma_commit_pair(smem_u32(&drain_bar));
+        const volatile int never = 0;
+        if (!mbar_wait(&drain_bar, 0, WT_DRAIN_LIMIT_NS, &never)) set_status(p.status, MOE_ERR_TIMEOUT);
       }
     }
-    if (!ok) {
-      set_status(p.status, MOE_ERR_TIMEOUT);
-      abort_s = 1;
-    }
-    umma_commit_pair(smem_u32(&drain_bar));
-    const volatile int never = 0;
-    if (!mbar_wait(&drain_bar, 0, WT_DRAIN_LIMIT_NS, &never)) set_status(p.status, MOE_ERR_TIMEOUT);
   } else if (warp >= WT_EXPAND_WARP && warp < WT_EPI_WARP) {
     // ---------------------------------------------------------------- expanders
     const int grp = (warp - WT_EXPAND_WARP) >> 2, q = warp & 3;
@@ -640,7 +666,7 @@ __global__ void __launch_bounds__(WT_THREADS, 1)
       for (int ch = it.c0; ch < it.c1; ++ch) {
         if (turn == grp) {
           // (the vote keeps the warp together on a failed wait)
-          if (!__all_sync(0xffffffffu, mbar_wait(&code_full[st], ph, lim, abort_flag))) {
+          if (!__all_sync(0xffffffffu, mbar_wait_poll(&code_full[st], ph, lim, abort_flag))) {
             ok = false;
             break;
           }
@@ -652,7 +678,7 @@ __global__ void __launch_bounds__(WT_THREADS, 1)
             cw[i] = lds128(base + code_off + ((i ^ sw) << 4));
             sc[i] = lds16(base + scale_off + ((i * 32) >> gl2) * SCALE_PITCH);
           }
-          if (!__all_sync(0xffffffffu, mbar_wait(&a_free[as], aph ^ 1u, lim, abort_flag))) {
+          if (!__all_sync(0xffffffffu, mbar_wait_poll(&a_free[as], aph ^ 1u, lim, abort_flag))) {
             ok = false;
             break;
           }
@@ -675,11 +701,13 @@ __global__ void __launch_bounds__(WT_THREADS, 1)
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
+          // (relaxed: the stores to tensor memory have completed, and a release at
+          // cluster scope would wait for much more)
           if (lane == 0) {
             if (leader)
-              mbar_arrive(&a_full[as]);
+              mbar_arrive_relaxed(&a_full[as]);
             else
-              mbar_arrive_cluster(mapa_shared(smem_u32(&a_full[as]), 0));
+              mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&a_full[as]), 0));
           }
         }
         turn ^= 1;
@@ -765,7 +793,7 @@ __global__ void __launch_bounds__(WT_THREADS, 1)
         return p.partial + ((((size_t)w * 2 + slot) * 2 + rank) * BN) * 128 + q * 32 + lane;
       };
       float* mine = whole ? nullptr : part_of(walker, it.wa < walker ? 0 : 1);
-      if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[acc], accph, lim, abort_flag))) {
+      if (!__all_sync(0xffffffffu, mbar_wait_poll(&acc_full[acc], accph, lim, abort_flag))) {
         ok = false;
         break;
       }
