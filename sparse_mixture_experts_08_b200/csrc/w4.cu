@@ -131,60 +131,68 @@ __global__ void __launch_bounds__(QW_WARPS * 32)
 // out rows = epi(rows of x . W_g^T), every group in one persistent launch, on the
 // 5th-generation tensor cores.
 //
-// The weights are the matrix instruction's A operand (M = 256 rows over a pair of CTAs,
-// 128 in each), the segment's input rows its B operand (N = up to BN, half of them in
-// each CTA): a pair reads each input row once for 256 weight rows, and a few rows waste
-// no M tile. The codes travel as they are, HBM -> shared memory (TMA); eight warps turn
-// them into bf16 values (code - 8 is exact in bf16, times the scale is one rounding, none
-// for the quantizer's scales) and put them straight into TENSOR MEMORY, from where the
-// matrix instruction takes its A operand. So the expanded weights never touch shared
-// memory: per 128 columns of K an SM's shared memory sees 9 KB of codes and scales and
-// BN / 2 rows of x, where bf16 tiles of the same shape would bring 32 KB of weights more.
+// The weights are the matrix instruction's A operand (M = 128 rows a CTA), the segment's
+// input rows its B operand (N = up to BN), so a few rows waste no M tile. The codes travel
+// as they are, HBM -> shared memory (TMA); groups of four warps turn them into bf16 values
+// (code - 8 is exact in bf16, times the scale is one rounding, none for the quantizer's
+// scales) and put them straight into TENSOR MEMORY, from where the matrix instruction
+// takes its A operand. So the expanded weights never touch shared memory: per 128 columns
+// of K it sees 9 KB of codes and scales and the input rows, where bf16 tiles of the same
+// shape would bring 32 KB of weights more.
 //
-// Tile: 256 weight rows x up to BN input rows x the whole K. SwiGLU tiles hold 128
-// features: of each CTA's 128 rows, lane quarter q (32 lanes of tensor memory) holds 16
-// gate rows, then the same features' 16 up rows, so one shuffle across 16 lanes brings a
+// Tile: 128 weight rows (PAIR, long segments: 256 over two CTAs, which then read half of
+// the input rows each) x up to BN input rows x the whole K. SwiGLU tiles hold half as many
+// features: of a CTA's 128 rows, lane quarter q (32 lanes of tensor memory) holds 16 gate
+// rows, then the same features' 16 up rows, so one shuffle across 16 lanes brings a
 // feature's two sums together and one accumulator serves both matrices.
 //
 // Schedule (device side, from the segment offsets): the tiles of all groups, tallest
-// first. Whole tiles go round the pairs in alternating direction, so that pairs working
-// at the same time share an expert's rows in L2; the last one to two rounds (everything,
-// when there are fewer tiles than pairs, as in decode) are cut into equal runs of
-// 128-column chunks, one per pair. A tile cut between pairs is joined through fp32
-// partial sums in the workspace: whichever warp finishes last adds them in the order of
-// K, so the result does not depend on who that is, and no one waits.
+// first. Whole tiles go round the walkers (CTAs or pairs) in alternating direction, so
+// that those working at the same time share an expert's rows in L2; the last one to two
+// rounds (everything, when there are fewer tiles than walkers, as in decode) are cut into
+// equal runs of chunks of K, one a walker. A tile cut between walkers is joined through
+// fp32 partial sums in the workspace: whichever warp finishes last adds them in the order
+// of K, so the result does not depend on who that is, and no one waits.
 //
-// Warps (480 threads): 0 and 14 TMA producers, 1 matrix issuer (in the leader CTA) and
-// owner of the tensor memory, 2..5 and 6..9 expand alternate chunks, 10..13 epilogue. Barriers of
-// a stage of the ring: codes (local) -> expanders; x rows of both CTAs (at the leader) ->
-// issuer; free (both CTAs, by the issuer's commit). Barriers of the A slots in tensor
-// memory: full (at the leader, 4 warps of each CTA), free (commit). Every wait is bounded
-// in time as in tc_gemm.cu.
-constexpr int WT_BK = 128;          // columns of K a stage
-constexpr int WT_THREADS = 480;
-constexpr int WT_EXPAND_WARP = 2, WT_EPI_WARP = 10, WT_X_WARP = 14;
+// Warps: 0 and 2 TMA producers (codes and scales; input rows), 1 matrix issuer (PAIR: in
+// the leader CTA) and owner of the tensor memory, then NG groups of four that expand
+// alternate chunks, then the epilogue's. The issuer's instruction stream is what bounded
+// the first forms of this kernel (a ready barrier costs it 84 cycles, a product 20, a
+// commit 46, and some hundred a turn of a long loop), so it commits once a chunk.
+// Barriers of a stage of the ring: codes (local) -> expanders; input rows (PAIR: of both
+// CTAs, at the leader) -> issuer; expanded (PAIR: at the leader) -> issuer; free: the
+// issuer's commit. A chunk's slot in tensor memory is free once the chunk A_SLOTS before
+// it is done, which that chunk's stage barrier tells (STAGES >= A_SLOTS: it cannot be a
+// phase further yet). Every wait is bounded in time as in tc_gemm.cu.
+constexpr int WT_EXPAND_WARP = 4;
 constexpr int WT_SMEM_BUDGET = 196 * 1024;
-constexpr int WT_CODE_BYTES = 128 * WT_BK / 2;
-constexpr int WT_SCALE_BYTES = 1024;  // up to 4 groups x 128 rows
-constexpr int WT_A_COLS = WT_BK / 2;  // tensor-memory columns of an A slot (two bf16 each)
 constexpr int WT_MAX_GROUPS = 1040;
-constexpr int WT_MIN_SHARE = 4;       // least chunks a pair takes of the cut tiles
 constexpr unsigned long long WT_DRAIN_LIMIT_NS = 200ull * 1000 * 1000;
 
 template <int BN>
 struct WtShape {
-  static constexpr int B_ROWS = BN / 2;                // input rows a CTA
+  static constexpr bool PAIR = BN >= 64;
+  static constexpr int BK = PAIR ? 128 : 256;          // columns of K a stage
+  static constexpr int NG = PAIR ? 2 : 3;              // groups of expanding warps
+  static constexpr int EW = PAIR ? 8 : 4;              // epilogue warps
+  static constexpr int EPI_WARP = WT_EXPAND_WARP + 4 * NG;
+  static constexpr int THREADS = 32 * (EPI_WARP + EW);
+  static constexpr int B_ROWS = PAIR ? BN / 2 : BN;    // input rows a CTA
   static constexpr int BOX = BN / 8 < 8 ? 8 : BN / 8;  // input rows of a TMA box
-  static constexpr int B_HALF = B_ROWS * 128;          // 64 columns of K: 128-byte rows
-  static constexpr int STAGE_BYTES = 2 * B_HALF + WT_CODE_BYTES + WT_SCALE_BYTES;
+  static constexpr int X_SUB = B_ROWS * 128;           // 64 columns of K: 128-byte rows
+  static constexpr int X_BYTES = BK / 64 * X_SUB;
+  static constexpr int CODE_BYTES = 128 * BK / 2;
+  static constexpr int SCALE_BYTES = 128 * 2 * BK / 32;  // at most, groups of 32
+  static constexpr int STAGE_BYTES = X_BYTES + CODE_BYTES + SCALE_BYTES;
   static constexpr int STAGES_RAW = WT_SMEM_BUDGET / STAGE_BYTES;
-  static constexpr int STAGES = STAGES_RAW > 16 ? 16 : STAGES_RAW;
-  static constexpr int NUM_ACC = 2 * BN + 2 * WT_A_COLS <= 512 ? 2 : 1;
-  static constexpr int A_SLOTS_RAW = (512 - NUM_ACC * BN) / WT_A_COLS;
-  static constexpr int A_SLOTS = A_SLOTS_RAW > 6 ? 6 : A_SLOTS_RAW;
+  static constexpr int STAGES = STAGES_RAW > 12 ? 12 : STAGES_RAW;
+  static constexpr int NUM_ACC = 2;
+  static constexpr int A_COLS = BK / 2;  // tensor-memory columns of an A slot (two bf16 each)
+  static constexpr int A_SLOTS_RAW = (512 - NUM_ACC * BN) / A_COLS;
+  static constexpr int A_SLOTS = A_SLOTS_RAW > 8 ? 8 : A_SLOTS_RAW;
   static constexpr int DYN_SMEM = STAGES * STAGE_BYTES + 1024;
   static_assert(BN % 16 == 0 && BN >= 16 && BN <= 256 && B_ROWS % BOX == 0 && BOX % 8 == 0, "tile");
-  static_assert(STAGE_BYTES % 1024 == 0 && STAGES >= 2 && A_SLOTS >= 2, "ring");
+  static_assert(STAGE_BYTES % 1024 == 0 && A_SLOTS >= 2 && STAGES >= A_SLOTS, "ring");
 };
 
 struct WtMaps {
@@ -197,7 +205,7 @@ struct WtSched {
   int tile_start[WT_MAX_GROUPS + 1];
   int gid[WT_MAX_GROUPS], rows[WT_MAX_GROUPS], brow[WT_MAX_GROUPS];
   int total, rounds, t0;   // tiles; rounds of whole tiles; first cut tile
-  long long base, cut, per;  // cost before t0, of the cut tiles, of a pair's share
+  long long base, cut, per;  // cost before t0, of the cut tiles, of a walker's share
 };
 
 template <int BN>
@@ -206,26 +214,26 @@ __device__ __forceinline__ int wt_height(int rows) {
   return nt > 0 ? min(BN, (((rows + nt - 1) / nt) + 15) & ~15) : 0;
 }
 // Cost of a chunk of a tile of `height` rows: the matrix instruction's time, at least
-// that of expanding 256 x 128 codes (as long as 64 rows take).
+// that of expanding the codes (as long as 64 rows take).
 __device__ __forceinline__ int wt_weight(int height) { return max(height >> 4, 4); }
 
 struct WtItem {
   int cls, g, mt, rows, n_inst, b_row, out_row, nc, c0, c1;
-  int wa, wb;  // pairs that share the tile
+  int wa, wb;  // walkers that share the tile
 };
 
-// The list of a pair's pieces of work, walked alike by every role.
+// The list of a walker's pieces of work, walked alike by every role.
 template <int BN>
 struct WtWalk {
   const W4Params& p;
   const WtSched& s;
-  int G, walker, walkers, tile_f;
+  int G, walker, walkers;
   int r;
   int t;            // next cut tile (-1: not looked up yet)
   long long at;     // its cost, from the first cut tile on
 
-  __device__ __forceinline__ WtWalk(const W4Params& p_, const WtSched& s_, int G_, int w, int ws, int tf)
-      : p(p_), s(s_), G(G_), walker(w), walkers(ws), tile_f(tf), r(0), t(-1), at(0) {}
+  __device__ __forceinline__ WtWalk(const W4Params& p_, const WtSched& s_, int G_, int w, int ws)
+      : p(p_), s(s_), G(G_), walker(w), walkers(ws), r(0), t(-1), at(0) {}
 
   __device__ __forceinline__ int decode(int tile, WtItem& it) const {
     int lo = 0, hi = G - 1;  // largest position with tile_start[pos] <= tile
@@ -244,7 +252,7 @@ struct WtWalk {
     it.n_inst = (it.rows + 15) & ~15;
     it.b_row = s.brow[gi] + nt * h;
     it.out_row = (c.seg_off ? s.brow[gi] : it.g * c.out_group_stride) + nt * h;
-    it.nc = (c.K + WT_BK - 1) / WT_BK;
+    it.nc = (c.K + WtShape<BN>::BK - 1) / WtShape<BN>::BK;
     return wt_weight(h);
   }
 
@@ -267,7 +275,7 @@ struct WtWalk {
       }
       const int h = wt_height<BN>(s.rows[s.gid[a]]);
       const W4Class& c = p.cls[s.gid[a] < p.cls[0].n_groups ? 0 : 1];
-      const long long tc = (long long)((c.K + WT_BK - 1) / WT_BK) * wt_weight(h);
+      const long long tc = (long long)((c.K + WtShape<BN>::BK - 1) / WtShape<BN>::BK) * wt_weight(h);
       const long long k = (s.base + lo - s.cost_start[a]) / tc;
       t = s.tile_start[a] + (int)k;
       at = s.cost_start[a] + k * tc - s.base;
@@ -287,22 +295,35 @@ struct WtWalk {
   }
 };
 
-// D (+)= A . B^T over the pair, A in tensor memory.
-__device__ __forceinline__ void umma_ts_pair(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
-      "r"(a), "l"(bdesc), "r"(idesc), "r"(acc)
-      : "memory");
+// D (+)= A . B^T, A in tensor memory (PAIR: over both CTAs).
+template <bool PAIR>
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  if (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+        "r"(a), "l"(bdesc), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+        "r"(a), "l"(bdesc), "r"(idesc), "r"(acc)
+        : "memory");
 }
-// Arrive on the barrier at this offset in both CTAs once every product so far completed.
-__device__ __forceinline__ void umma_commit_both(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_u32(bar)),
-      "h"((uint16_t)3)
-      : "memory");
+// Arrive on the barrier (PAIR: at this offset in both CTAs) once every product so far completed.
+template <bool PAIR>
+__device__ __forceinline__ void umma_commit_all(uint64_t* bar) {
+  if (PAIR)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    umma_commit(bar);
 }
 __device__ __forceinline__ void tmem_st_x32(uint32_t t, const uint32_t (&r)[32]) {
   asm volatile(
@@ -327,16 +348,19 @@ __device__ __forceinline__ uint32_t lds16(uint32_t a) {
 }
 
 template <int BN, int EPI>
-__global__ void __launch_bounds__(WT_THREADS, 1)
+__global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
     w4_gemm_kernel(const __grid_constant__ WtMaps maps, const __grid_constant__ W4Params p) {
   using S = WtShape<BN>;
   constexpr int MATS = EPI == EPI_SWIGLU ? 2 : 1;
-  constexpr int STAGES = S::STAGES, A_SLOTS = S::A_SLOTS;
-  constexpr int TILE_F = MATS == 2 ? 128 : 256;  // output features a tile
+  constexpr bool PAIR = S::PAIR;
+  constexpr int CTAS = PAIR ? 2 : 1;
+  constexpr int STAGES = S::STAGES, A_SLOTS = S::A_SLOTS, BK = S::BK, EW = S::EW;
+  constexpr int CTA_F = MATS == 2 ? 64 : 128;  // output features of a CTA's rows
+  constexpr int TILE_F = CTAS * CTA_F;
   __shared__ WtSched sched;
-  __shared__ __align__(8) uint64_t code_full[STAGES], x_full[STAGES], stage_free[STAGES], a_full[A_SLOTS],
-      a_free[A_SLOTS], acc_full[2], acc_free[2], drain_bar;
-  __shared__ __align__(16) __nv_bfloat16 stg[4][16][32];  // epilogue warp: 16 output rows, SwiGLU or ReLU
+  __shared__ __align__(8) uint64_t code_full[STAGES], x_full[STAGES], a_full[STAGES], stage_free[STAGES],
+      acc_full[2], acc_free[2], drain_bar;
+  __shared__ __align__(16) __nv_bfloat16 stg[EPI == EPI_DOWN ? 1 : EW][16][32];  // epilogue warp: 16 output rows
   __shared__ uint32_t tmem_base_s;
   __shared__ int abort_s;
   extern __shared__ uint8_t dyn_smem[];
@@ -344,9 +368,10 @@ __global__ void __launch_bounds__(WT_THREADS, 1)
   // (the shuffle tells the compiler that the role is the whole warp's: loop state and
   // descriptors then live in uniform registers)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
   const bool leader = rank == 0;
-  const int walker = (int)cluster_id_x(), walkers = (int)nclusters_x();
+  const int walker = PAIR ? (int)cluster_id_x() : (int)blockIdx.x;
+  const int walkers = PAIR ? (int)nclusters_x() : (int)gridDim.x;
   const uint32_t smem_base = (smem_u32(dyn_smem) + 1023u) & ~1023u;
   uint8_t* smem_gen = dyn_smem + (smem_base - smem_u32(dyn_smem));
   const int G0 = p.cls[0].n_groups, G = G0 + (p.n_classes > 1 ? p.cls[1].n_groups : 0);
@@ -356,15 +381,12 @@ __global__ void __launch_bounds__(WT_THREADS, 1)
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(&code_full[i], 1);
       mbar_init(&x_full[i], 1);
+      mbar_init(&a_full[i], 4 * CTAS);  // four expanding warps of each CTA
       mbar_init(&stage_free[i], 1);
-    }
-    for (int i = 0; i < A_SLOTS; ++i) {
-      mbar_init(&a_full[i], 8);  // 4 expanding warps of each CTA
-      mbar_init(&a_free[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_free[i], 8);  // 4 epilogue warps of each CTA
+      mbar_init(&acc_free[i], EW * CTAS);  // the epilogue warps of each CTA
     }
     mbar_init(&drain_bar, 1);
     abort_s = 0;
@@ -373,17 +395,17 @@ __global__ void __launch_bounds__(WT_THREADS, 1)
     tma_prefetch_desc(&maps.x[0]);
   }
   if (warp == 1) {
-    tmem_alloc_g<true>(&tmem_base_s, 512);
-    tmem_relinquish_g<true>();
+    tmem_alloc_g<PAIR>(&tmem_base_s, 512);
+    tmem_relinquish_g<PAIR>();
   }
   __syncwarp();
-  cluster_sync_all();  // the peer's barriers are initialised before either CTA signals them
+  if (PAIR) cluster_sync_all();  // the peer's barriers are initialised before either CTA signals them
   pdl_launch_dependents();
   pdl_wait();
   // the counters of the next launch on this workspace (two sets, used in turn): zero
   // whatever this launch, or one that was cut short, leaves in its own
   if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < W4_COUNTERS; i += WT_THREADS) p.counters_next[i] = 0u;
+    for (int i = threadIdx.x; i < W4_COUNTERS; i += S::THREADS) p.counters_next[i] = 0u;
   if (warp == 0) {
     constexpr int NB = BN / 16 + 1;  // bucket = tile height / 16 (0: a group without rows)
     const int per = (G + 31) / 32;
@@ -455,7 +477,7 @@ __global__ void __launch_bounds__(WT_THREADS, 1)
     // cost before each position, and the split into whole and cut tiles
     auto tile_cost = [&](const int gi) {
       const int K = p.cls[gi < G0 ? 0 : 1].K;
-      return (long long)((K + WT_BK - 1) / WT_BK) * wt_weight(wt_height<BN>(sched.rows[gi]));
+      return (long long)((K + S::BK - 1) / S::BK) * wt_weight(wt_height<BN>(sched.rows[gi]));
     };
     long long sum = 0;
     for (int i = lo; i < hi; ++i)
@@ -495,9 +517,9 @@ __global__ void __launch_bounds__(WT_THREADS, 1)
       sched.t0 = t0;
       sched.base = base;
       sched.cut = cut;
-      // (at least one chunk of the heaviest tile, so that every pair between a tile's
+      // (at least 512 columns of the heaviest tile, so that every walker between a tile's
       // first and last one has a part of it)
-      sched.per = max((cut + walkers - 1) / walkers, (long long)(WT_MIN_SHARE * max(BN / 16, 4)));
+      sched.per = max((cut + walkers - 1) / walkers, (long long)(512 / BK * max(BN / 16, 4)));
     }
   }
   __syncwarp();
@@ -506,59 +528,62 @@ __global__ void __launch_bounds__(WT_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_base_s;
   const unsigned long long lim = p.wait_limit_ns;
-  WtWalk<BN> walk(p, sched, G, walker, walkers, TILE_F);
+  WtWalk<BN> walk(p, sched, G, walker, walkers);
   WtItem it;
   bool ok = true;
 
-  if (warp == 0 || warp == WT_X_WARP) {
+  if (warp == 0 || warp == 2) {
     // ---------------------------------------------------------------- producers
-    // Warp 0 fetches codes and scales, WT_X_WARP the input rows (one warp's issue slots
+    // Warp 0 fetches codes and scales, warp 2 the input rows (one warp's issue slots
     // would bound the short tiles). As in the issuer, the whole warp walks and waits and
     // one lane issues.
     const bool codes = warp == 0;
     int st = 0, used = 0;
     uint32_t ph = 0;
-    const int gpc = WT_BK / p.group;
+    const int gpc = BK / p.group;
     while (ok && walk.next(it)) {
       const W4Class& c = p.cls[it.cls];
-      const int K = c.K, f0 = it.mt * TILE_F + (int)rank * (TILE_F / 2);
+      const int K = c.K, f0 = it.mt * TILE_F + (int)rank * CTA_F;
       const bool live = f0 < c.R;  // a CTA whose rows lie behind the matrix loads no weights
       const int y = it.g * c.R + f0, ys = it.g * ((K + p.group - 1) / p.group);
-      const int half_rows = it.n_inst >> 1, nbox = (half_rows + S::BOX - 1) / S::BOX;
-      const int x_row = it.b_row + (int)rank * half_rows;
+      const int cta_rows = it.n_inst / CTAS, nbox = (cta_rows + S::BOX - 1) / S::BOX;
+      const int x_row = it.b_row + (int)rank * cta_rows;
       for (int ch = it.c0; ch < it.c1; ++ch) {
-        if (!__all_sync(0xffffffffu, mbar_wait_poll(&stage_free[st], ph ^ 1u, lim, abort_flag))) {
+        if (!mbar_wait_warp(&stage_free[st], ph ^ 1u, lim, abort_flag)) {
           ok = false;
           break;
         }
         uint8_t* xs = smem_gen + st * S::STAGE_BYTES;
         if (elect_one()) {
           if (codes) {
-            uint8_t* cs = xs + 2 * S::B_HALF;
-            uint8_t* ss = cs + WT_CODE_BYTES;
+            uint8_t* cs = xs + S::X_BYTES;
+            uint8_t* ss = cs + S::CODE_BYTES;
             if (live) {
-              mbar_arrive_expect_tx(&code_full[st], WT_CODE_BYTES + gpc * 256);
-              tma_load_2d(&maps.codes[it.cls][0], &code_full[st], cs, ch * (WT_BK / 2), y);
+              mbar_arrive_expect_tx(&code_full[st], S::CODE_BYTES + gpc * 256);
+              tma_load_2d(&maps.codes[it.cls][0], &code_full[st], cs, ch * (BK / 2), y);
               if (MATS == 2)
-                tma_load_2d(&maps.codes[it.cls][1], &code_full[st], cs + WT_CODE_BYTES / 2, ch * (WT_BK / 2), y);
+                tma_load_2d(&maps.codes[it.cls][1], &code_full[st], cs + S::CODE_BYTES / 2, ch * (BK / 2), y);
               tma_load_2d(&maps.scales[it.cls][0], &code_full[st], ss, f0, ys + ch * gpc);
               if (MATS == 2)
-                tma_load_2d(&maps.scales[it.cls][1], &code_full[st], ss + WT_SCALE_BYTES / 2, f0, ys + ch * gpc);
+                tma_load_2d(&maps.scales[it.cls][1], &code_full[st], ss + S::SCALE_BYTES / 2, f0, ys + ch * gpc);
             } else {
               mbar_arrive(&code_full[st]);
             }
           } else {
-            const int halves = K - ch * WT_BK > 64 ? 2 : 1;
-            if (leader) mbar_arrive_expect_tx(&x_full[st], 2 * halves * nbox * S::BOX * 128);
-            const uint32_t xb = mapa_shared(smem_u32(&x_full[st]), 0);
+            // (columns behind K read as zero)
+            if (leader) mbar_arrive_expect_tx(&x_full[st], CTAS * nbox * S::BOX * BK * 2);
+            const uint32_t xb = PAIR ? mapa_shared(smem_u32(&x_full[st]), 0) : 0u;
 #pragma unroll
-            for (int b = 0; b < S::B_ROWS / S::BOX; ++b)
-              if (b < nbox) {
-                tma_load_2d_pair(&maps.x[it.cls], xb, xs + b * S::BOX * 128, ch * WT_BK, x_row + b * S::BOX);
-                if (halves == 2)
-                  tma_load_2d_pair(&maps.x[it.cls], xb, xs + S::B_HALF + b * S::BOX * 128, ch * WT_BK + 64,
-                                   x_row + b * S::BOX);
-              }
+            for (int h = 0; h < BK / 64; ++h)
+#pragma unroll
+              for (int b = 0; b < S::B_ROWS / S::BOX; ++b)
+                if (b < nbox) {
+                  uint8_t* dst = xs + h * S::X_SUB + b * S::BOX * 128;
+                  if (PAIR)
+                    tma_load_2d_pair(&maps.x[it.cls], xb, dst, ch * BK + h * 64, x_row + b * S::BOX);
+                  else
+                    tma_load_2d(&maps.x[it.cls], &x_full[st], dst, ch * BK + h * 64, x_row + b * S::BOX);
+                }
           }
         }
         __syncwarp();
@@ -573,9 +598,9 @@ __global__ void __launch_bounds__(WT_THREADS, 1)
       set_status(p.status, MOE_ERR_TIMEOUT);
       abort_s = 1;
     }
-    // every issued copy lands before the CTA may exit (the leader's barriers count both
-    // CTAs' rows of x; the peer waits for the leader at the last cluster barrier): the
-    // last use of stage i was fill number (used - 1 - i) / STAGES of it
+    // every issued copy lands before the CTA may exit (PAIR: the leader's barriers count
+    // both CTAs' rows; the peer waits for the leader at the last cluster barrier): the
+    // last use of stage i was its fill number (used - 1 - i) / STAGES
     if (lane == 0 && (codes || leader))
       for (int i = 0; i < STAGES && i < used; ++i) {
         const volatile int never = 0;
@@ -587,50 +612,37 @@ __global__ void __launch_bounds__(WT_THREADS, 1)
     // ---------------------------------------------------------------- matrix issuer
     if (leader) {
       int st = 0, as = 0, acc = 0;
-      uint32_t ph = 0, aph = 0, accph = 0;
+      uint32_t ph = 0, accph = 0;
       while (ok && walk.next(it)) {
-        if (!__all_sync(0xffffffffu, mbar_wait_poll(&acc_free[acc], accph ^ 1u, lim, abort_flag))) {
+        if (!mbar_wait_warp(&acc_free[acc], accph ^ 1u, lim, abort_flag)) {
           ok = false;
           break;
         }
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(acc * BN);
-        const uint32_t idesc = idesc_bf16(256, it.n_inst);
-        const int K = p.cls[it.cls].K;
+        const uint32_t idesc = idesc_bf16(128 * CTAS, it.n_inst);
+#pragma unroll 1
         for (int ch = it.c0; ch < it.c1; ++ch) {
-          if (!__all_sync(0xffffffffu, mbar_wait_poll(&x_full[st], ph, lim, abort_flag) &&
-                                           mbar_wait_poll(&a_full[as], aph, lim, abort_flag))) {
+          if (!mbar_wait_warp(&x_full[st], ph, lim, abort_flag) || !mbar_wait_warp(&a_full[st], ph, lim, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
           if (elect_one()) {
             const uint64_t bd = sdesc_sw128(smem_base + st * S::STAGE_BYTES);
-            const uint32_t a = tmem + (uint32_t)(S::NUM_ACC * BN + as * WT_A_COLS);
-            const int left = K - ch * WT_BK;
-            if (left >= WT_BK) {
+            const uint32_t a = tmem + (uint32_t)(S::NUM_ACC * BN + as * S::A_COLS);
 #pragma unroll
-              for (int kk = 0; kk < WT_BK / 16; ++kk)
-                umma_ts_pair(d, a + 8 * kk, bd + (kk >> 2) * (S::B_HALF >> 4) + 2 * (kk & 3), idesc,
-                             kk > 0 ? 1u : (uint32_t)(ch > it.c0));
-            } else {
-#pragma unroll 1
-              for (int kk = 0; kk < (left >> 4); ++kk)
-                umma_ts_pair(d, a + 8 * kk, bd + (kk >> 2) * (S::B_HALF >> 4) + 2 * (kk & 3), idesc,
-                             (ch > it.c0 || kk > 0) ? 1u : 0u);
-            }
-            umma_commit_both(&stage_free[st]);
-            umma_commit_both(&a_free[as]);
-            if (ch + 1 == it.c1) umma_commit_both(&acc_full[acc]);
+            for (int kk = 0; kk < BK / 16; ++kk)
+              umma_ts<PAIR>(d, a + 8 * kk, bd + (kk >> 2) * (S::X_SUB >> 4) + 2 * (kk & 3), idesc,
+                            kk > 0 ? 1u : (uint32_t)(ch > it.c0));
+            umma_commit_all<PAIR>(&stage_free[st]);
+            if (ch + 1 == it.c1) umma_commit_all<PAIR>(&acc_full[acc]);
           }
           __syncwarp();
+          if (++as == A_SLOTS) as = 0;
           if (++st == STAGES) {
             st = 0;
             ph ^= 1u;
-          }
-          if (++as == A_SLOTS) {
-            as = 0;
-            aph ^= 1u;
           }
         }
         if (!ok) break;
@@ -644,59 +656,56 @@ __global__ void __launch_bounds__(WT_THREADS, 1)
         abort_s = 1;
       }
       if (elect_one()) {
-        umma_commit_pair(smem_u32(&drain_bar));
+        if (PAIR)
+          umma_commit_pair(smem_u32(&drain_bar));
+        else
+          umma_commit(&drain_bar);
         const volatile int never = 0;
         if (!mbar_wait(&drain_bar, 0, WT_DRAIN_LIMIT_NS, &never)) set_status(p.status, MOE_ERR_TIMEOUT);
       }
     }
-  } else if (warp >= WT_EXPAND_WARP && warp < WT_EPI_WARP) {
+  } else if (warp >= WT_EXPAND_WARP && warp < S::EPI_WARP) {
     // ---------------------------------------------------------------- expanders
     const int grp = (warp - WT_EXPAND_WARP) >> 2, q = warp & 3;
     const int row = MATS == 2 ? (lane >> 4) * 64 + q * 16 + (lane & 15) : q * 32 + lane;  // of the staged codes
-    const uint32_t code_off = 2 * S::B_HALF + row * (WT_BK / 2), sw = (row >> 1) & 3;
+    const uint32_t code_off = S::X_BYTES + row * (BK / 2);
+    const uint32_t sw = BK == 256 ? row & 7 : (row >> 1) & 3;  // the TMA's 128- or 64-byte swizzle
     // scales: [matrix][group][64 rows] or [group][128 rows]
-    const uint32_t scale_off = 2 * S::B_HALF + WT_CODE_BYTES +
-                               (MATS == 2 ? (lane >> 4) * (WT_SCALE_BYTES / 2) + (q * 16 + (lane & 15)) * 2 : row * 2);
+    const uint32_t scale_off = S::X_BYTES + S::CODE_BYTES +
+                               (MATS == 2 ? (lane >> 4) * (S::SCALE_BYTES / 2) + (q * 16 + (lane & 15)) * 2 : row * 2);
     constexpr int SCALE_PITCH = MATS == 2 ? 128 : 256;
     const int gl2 = 31 - __clz(p.group);
     const uint32_t t_lane = tmem + ((uint32_t)(q * 32) << 16) + S::NUM_ACC * BN;
-    int st = 0, as = 0, turn = 0;
-    uint32_t ph = 0, aph = 0;
+    int st = 0, as = 0, turn = 0, old = STAGES - A_SLOTS;  // old: the stage A_SLOTS chunks ago
+    uint32_t ph = 0, old_ph = 1;                            // (before the first such chunk: passes at once)
     while (ok && walk.next(it)) {
+      const int K = p.cls[it.cls].K, ng = (K + p.group - 1) >> gl2;
+#pragma unroll 1
       for (int ch = it.c0; ch < it.c1; ++ch) {
         if (turn == grp) {
-          // (the vote keeps the warp together on a failed wait)
-          if (!__all_sync(0xffffffffu, mbar_wait_poll(&code_full[st], ph, lim, abort_flag))) {
-            ok = false;
-            break;
-          }
-          const uint32_t base = smem_base + st * S::STAGE_BYTES;
-          uint4 cw[4];
-          uint32_t sc[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            cw[i] = lds128(base + code_off + ((i ^ sw) << 4));
-            sc[i] = lds16(base + scale_off + ((i * 32) >> gl2) * SCALE_PITCH);
-          }
-          if (!__all_sync(0xffffffffu, mbar_wait_poll(&a_free[as], aph ^ 1u, lim, abort_flag))) {
+          if (!mbar_wait_warp(&code_full[st], ph, lim, abort_flag) ||
+              !mbar_wait_warp(&stage_free[old], old_ph, lim, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
+          const uint32_t base = smem_base + st * S::STAGE_BYTES;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < BK / 64; ++h) {  // 64 columns at a time
             uint32_t v[32];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const uint4 c4 = cw[2 * h + i];
+              const uint4 c4 = lds128(base + code_off + (((2 * h + i) ^ sw) << 4));
+              const int gi = (h * 64 + i * 32) >> gl2;
+              uint32_t ss = lds16(base + scale_off + gi * SCALE_PITCH) * 0x10001u;
+              if (ch * (BK >> gl2) + gi >= ng) ss = 0u;  // behind K: x is zero there, the scale not this row's
               const uint32_t w[4] = {c4.x, c4.y, c4.z, c4.w};
-              const uint32_t ss = sc[2 * h + i] * 0x10001u;
 #pragma unroll
               for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[i * 16 + j * 4 + e] = mul_bf16x2(w4_pair(w[j] >> (4 * e)), ss);
             }
-            tmem_st_x32(t_lane + as * WT_A_COLS + h * 32, v);
+            tmem_st_x32(t_lane + as * S::A_COLS + h * 32, v);
           }
           tmem_st_wait();
           tc_fence_before();
@@ -705,19 +714,20 @@ __global__ void __launch_bounds__(WT_THREADS, 1)
           // cluster scope would wait for much more)
           if (lane == 0) {
             if (leader)
-              mbar_arrive_relaxed(&a_full[as]);
+              mbar_arrive_relaxed(&a_full[st]);
             else
-              mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&a_full[as]), 0));
+              mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&a_full[st]), 0));
           }
         }
-        turn ^= 1;
+        if (++turn == S::NG) turn = 0;
+        if (++as == A_SLOTS) as = 0;
+        if (++old == STAGES) {
+          old = 0;
+          old_ph ^= 1u;
+        }
         if (++st == STAGES) {
           st = 0;
           ph ^= 1u;
-        }
-        if (++as == A_SLOTS) {
-          as = 0;
-          aph ^= 1u;
         }
       }
     }
@@ -725,14 +735,17 @@ __global__ void __launch_bounds__(WT_THREADS, 1)
       set_status(p.status, MOE_ERR_TIMEOUT);
       abort_s = 1;
     }
-  } else if (warp >= WT_EPI_WARP) {
+  } else if (warp >= S::EPI_WARP) {
     // ---------------------------------------------------------------- epilogue
-    const int q = warp & 3;
+    // (the EW / 4 warps of a lane quarter take alternate chunks of 16 rows)
+    const int q = warp & 3, ew = warp - S::EPI_WARP;
+    const int cfirst = 16 * (ew >> 2);
+    constexpr int CSTEP = 16 * (EW / 4);
     int acc = 0;
     uint32_t accph = 0;
     while (ok && walk.next(it)) {
       const W4Class& c = p.cls[it.cls];
-      const int f0 = it.mt * TILE_F + (int)rank * (TILE_F / 2);
+      const int f0 = it.mt * TILE_F + (int)rank * CTA_F;
       const int rows = it.rows;
       // 16 rows' sums of this lane's weight row -> output rows [c0, c0 + 16)
       auto emit = [&](const int c0, const float (&v)[16]) {
@@ -764,17 +777,17 @@ __global__ void __launch_bounds__(WT_THREADS, 1)
             const float got = __shfl_xor_sync(0xffffffffu, up ? v[2 * j] : v[2 * j + 1], 16);
             const float g = up ? got : v[2 * j], u = up ? v[2 * j + 1] : got;
             // h is rounded to bf16: it is the next product's tensor-core operand
-            stg[q][2 * j + up][lane & 15] = __float2bfloat16_rn(__fdividef(g, 1.f + __expf(-g)) * u);
+            stg[ew][2 * j + up][lane & 15] = __float2bfloat16_rn(__fdividef(g, 1.f + __expf(-g)) * u);
           }
           __syncwarp();
           const int j = lane >> 1, f = f0 + q * 16 + (lane & 1) * 8;
           if (j < jn && f < c.R)
             *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(c.out) + (long long)(it.out_row + c0 + j) * c.R +
-                                      f) = *reinterpret_cast<const uint4*>(&stg[q][j][(lane & 1) * 8]);
+                                      f) = *reinterpret_cast<const uint4*>(&stg[ew][j][(lane & 1) * 8]);
           __syncwarp();
         } else {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) stg[q][j][lane] = __float2bfloat16_rn(v[j] < 0.f ? 0.f : v[j]);
+          for (int j = 0; j < 16; ++j) stg[ew][j][lane] = __float2bfloat16_rn(v[j] < 0.f ? 0.f : v[j]);
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -782,18 +795,18 @@ __global__ void __launch_bounds__(WT_THREADS, 1)
             if (j < jn && f < c.R)
               *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(c.out) +
                                         (long long)(it.out_row + c0 + j) * c.R + f) =
-                  *reinterpret_cast<const uint4*>(&stg[q][j][(lane & 3) * 8]);
+                  *reinterpret_cast<const uint4*>(&stg[ew][j][(lane & 3) * 8]);
           }
           __syncwarp();
         }
       };
       const bool whole = it.wa == it.wb;
-      // this warp's part of a pair's partial sums: [row][128 lanes]
+      // this warp's part of a walker's partial sums: [row][128 lanes]
       auto part_of = [&](const int w, const int slot) {
-        return p.partial + ((((size_t)w * 2 + slot) * 2 + rank) * BN) * 128 + q * 32 + lane;
+        return p.partial + ((((size_t)w * 2 + slot) * CTAS + rank) * BN) * 128 + q * 32 + lane;
       };
       float* mine = whole ? nullptr : part_of(walker, it.wa < walker ? 0 : 1);
-      if (!__all_sync(0xffffffffu, mbar_wait_poll(&acc_full[acc], accph, lim, abort_flag))) {
+      if (!mbar_wait_warp<true>(&acc_full[acc], accph, lim, abort_flag)) {
         ok = false;
         break;
       }
@@ -823,32 +836,32 @@ __global__ void __launch_bounds__(WT_THREADS, 1)
         }
       };
       // the loads of one 16-column chunk are in flight while the one before is used
-      tmem_ld_x16(t_row, ra);
+      if (cfirst < rows) tmem_ld_x16(t_row + cfirst, ra); else release();
 #pragma unroll 1
-      for (int c0 = 0; c0 < rows; c0 += 32) {
+      for (int c0 = cfirst; c0 < rows; c0 += 2 * CSTEP) {
         tmem_ld_wait_keep(ra);
-        if (c0 + 16 < rows) tmem_ld_x16(t_row + c0 + 16, rb); else release();
+        if (c0 + CSTEP < rows) tmem_ld_x16(t_row + c0 + CSTEP, rb); else release();
         use(c0, ra);
-        if (c0 + 16 >= rows) break;
+        if (c0 + CSTEP >= rows) break;
         tmem_ld_wait_keep(rb);
-        if (c0 + 32 < rows) tmem_ld_x16(t_row + c0 + 32, ra); else release();
-        use(c0 + 16, rb);
+        if (c0 + 2 * CSTEP < rows) tmem_ld_x16(t_row + c0 + 2 * CSTEP, ra); else release();
+        use(c0 + CSTEP, rb);
       }
       if (++acc == S::NUM_ACC) {
         acc = 0;
         accph ^= 1u;
       }
       if (!whole) {
-        // the last of the tile's pairs to get here adds the parts, in the order of K
+        // the last of the tile's walkers to get here adds the parts, in the order of K
         __threadfence();
         __syncwarp();
         unsigned n = 0;
-        if (lane == 0) n = atomicAdd(&p.counters[(it.wa * 2 + (int)rank) * 4 + q], 1u);
+        if (lane == 0) n = atomicAdd(&p.counters[(it.wa * CTAS + (int)rank) * EW + ew], 1u);
         n = __shfl_sync(0xffffffffu, n, 0);
         if (n == (unsigned)(it.wb - it.wa)) {
           __threadfence();
 #pragma unroll 1
-          for (int c0 = 0; c0 < rows; c0 += 16) {
+          for (int c0 = cfirst; c0 < rows; c0 += CSTEP) {
             float v[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] = 0.f;
@@ -871,10 +884,10 @@ __global__ void __launch_bounds__(WT_THREADS, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();  // neither CTA leaves while the other may signal it or read its memory
+  if (PAIR) cluster_sync_all();  // neither CTA leaves while the other may signal it or read its memory
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_g<true>(tmem, 512);
+    tmem_dealloc_g<PAIR>(tmem, 512);
   }
 }
 
@@ -899,9 +912,10 @@ cudaError_t launch_impl(const W4Params& p, cudaStream_t s) {
     for (int j = 0; j < 2; ++j) {
       const W4Matrix& a = MATS == 2 && j ? c.a1 : c.a0;
       if (!make_map_2d(&maps.codes[i][j], a.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.K / 2, (long long)c.n_groups * c.R,
-                       c.K / 2, WT_BK / 2, ROWS, CU_TENSOR_MAP_SWIZZLE_64B) ||
+                       c.K / 2, S::BK / 2, ROWS,
+                       S::BK == 256 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) ||
           !make_map_2d(&maps.scales[i][j], a.scales, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, c.R, (long long)c.n_groups * ng,
-                       2LL * c.R, ROWS, WT_BK / p.group, CU_TENSOR_MAP_SWIZZLE_NONE))
+                       2LL * c.R, ROWS, S::BK / p.group, CU_TENSOR_MAP_SWIZZLE_NONE))
         return cudaErrorInvalidValue;
     }
     if (!make_map_2d(&maps.x[i], c.b, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, c.K, c.b_rows, 2LL * c.K, 64, S::BOX,
@@ -910,35 +924,37 @@ cudaError_t launch_impl(const W4Params& p, cudaStream_t s) {
   }
   auto kern = w4_gemm_kernel<BN, EPI>;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(WT_THREADS);
+  cfg.blockDim = dim3(S::THREADS);
   cfg.dynamicSmemBytes = S::DYN_SMEM;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  static int max_pairs[64] = {0};  // a device: pairs that can be resident at once
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  static int walkers[64] = {0};  // a device: CTAs or pairs that can be resident at once
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!max_pairs[dev]) {
+  if (!walkers[dev]) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::DYN_SMEM);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(num_sms() & ~1);
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;  // the occupancy query takes the cluster shape alone
-    int n = 0;
-    e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
-    if (e != cudaSuccess) return e;
-    max_pairs[dev] = std::max(1, std::min(n, W4_MAX_PAIRS));
+    int n = num_sms();
+    if (S::PAIR) {
+      cfg.gridDim = dim3(num_sms() & ~1);
+      cfg.attrs = attr + 1;
+      cfg.numAttrs = 1;  // the occupancy query takes the cluster shape alone
+      e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+      if (e != cudaSuccess) return e;
+    }
+    walkers[dev] = std::max(1, std::min(n, W4_MAX_CTAS / (S::PAIR ? 2 : 1)));
   }
-  cfg.gridDim = dim3(2 * max_pairs[dev]);
+  cfg.gridDim = dim3(walkers[dev] * (S::PAIR ? 2 : 1));
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = S::PAIR ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, kern, maps, p);
   count_launch();
   return e;
@@ -950,10 +966,10 @@ cudaError_t launch_impl(const W4Params& p, cudaStream_t s) {
 // segment expands the expert's weights again), no more than that (a stage's bytes).
 int w4_pick_bn(long long T, double avg_rows) {
   const double want = std::min((double)T, 2.5 * avg_rows);
-  return want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : want <= 128 ? 128 : 256;
+  return want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : want <= 128 ? 128 : 192;
 }
 
-size_t w4_partial_bytes(int bn) { return (size_t)W4_MAX_PAIRS * 2 * 2 * bn * 128 * sizeof(float); }
+size_t w4_partial_bytes(int bn) { return (size_t)W4_MAX_CTAS * 2 * bn * 128 * sizeof(float); }
 
 cudaError_t launch_w4_gemm(int epi, int bn, const W4Params& p, cudaStream_t s) {
 #define MOE_W4_CASE(BN_)                                                  \
@@ -966,7 +982,7 @@ cudaError_t launch_w4_gemm(int epi, int bn, const W4Params& p, cudaStream_t s) {
   MOE_W4_CASE(32)
   MOE_W4_CASE(64)
   MOE_W4_CASE(128)
-  MOE_W4_CASE(256)
+  MOE_W4_CASE(192)
 #undef MOE_W4_CASE
   return cudaErrorInvalidValue;
 }

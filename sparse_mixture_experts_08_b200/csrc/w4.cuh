@@ -36,21 +36,21 @@ struct W4Class {
   const int* perm;
 };
 
-constexpr int W4_MAX_PAIRS = 80;                 // CTA pairs of a launch
-constexpr int W4_COUNTERS = W4_MAX_PAIRS * 2 * 4;  // [pair][CTA][lane quarter]
+constexpr int W4_MAX_CTAS = 160;              // CTAs of a launch
+constexpr int W4_COUNTERS = W4_MAX_CTAS * 8;  // one an epilogue warp
 
 struct W4Params {
   W4Class cls[2];
   int n_classes;
   int group;    // 32, 64 or 128
-  float* partial;            // w4_partial_bytes(): sums of tiles that pairs of CTAs share
+  float* partial;            // w4_partial_bytes(): sums of tiles that CTAs share
   unsigned* counters;        // [W4_COUNTERS], zero: warps that have left their sums of a tile
   unsigned* counters_next;   // [W4_COUNTERS]: zeroed here, used by the next launch
   int* status;
   unsigned long long wait_limit_ns;
 };
 
-// Input rows of a tile (16 .. 256) for segments of at most T and on average avg_rows rows.
+// Input rows of a tile (16 .. 192) for segments of at most T and on average avg_rows rows.
 int w4_pick_bn(long long T, double avg_rows);
 size_t w4_partial_bytes(int bn);
 cudaError_t launch_w4_gemm(int epi, int bn, const W4Params& p, cudaStream_t s);
