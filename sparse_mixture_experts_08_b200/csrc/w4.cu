@@ -178,7 +178,7 @@ struct WtShape {
   static constexpr int EPI_WARP = WT_EXPAND_WARP + 4 * NG;
   static constexpr int THREADS = 32 * (EPI_WARP + EW);
   static constexpr int B_ROWS = PAIR ? BN / 2 : BN;    // input rows a CTA
-  static constexpr int BOX = BN / 8 < 8 ? 8 : BN / 8;  // input rows of a TMA box
+  static constexpr int HALF = B_ROWS / 2;               // staged rows where half of a CTA's suffice
   static constexpr int X_SUB = B_ROWS * 128;           // 64 columns of K: 128-byte rows
   static constexpr int X_BYTES = BK / 64 * X_SUB;
   static constexpr int CODE_BYTES = 128 * BK / 2;
@@ -191,13 +191,14 @@ struct WtShape {
   static constexpr int A_SLOTS_RAW = (512 - NUM_ACC * BN) / A_COLS;
   static constexpr int A_SLOTS = A_SLOTS_RAW > 8 ? 8 : A_SLOTS_RAW;
   static constexpr int DYN_SMEM = STAGES * STAGE_BYTES + 1024;
-  static_assert(BN % 16 == 0 && BN >= 16 && BN <= 256 && B_ROWS % BOX == 0 && BOX % 8 == 0, "tile");
+  static_assert(BN % 16 == 0 && BN >= 16 && BN <= 256 && HALF % 8 == 0, "tile");
   static_assert(STAGE_BYTES % 1024 == 0 && A_SLOTS >= 2 && STAGES >= A_SLOTS, "ring");
 };
 
 struct WtMaps {
   CUtensorMap codes[2][2], scales[2][2];  // [class][matrix]
-  CUtensorMap x[2];
+  CUtensorMap x[2][2];  // [class][half]: 64 columns x B_ROWS (HALF) rows x BK / 64
+  CUtensorMap xt[2];    // 64 columns x HALF rows, columns behind K as zero
 };
 
 struct WtSched {
@@ -347,6 +348,23 @@ __device__ __forceinline__ uint32_t lds16(uint32_t a) {
   return v;
 }
 
+// Tile copy over three dimensions; PAIR: counted on a barrier of the leader CTA.
+template <bool PAIR>
+__device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint32_t bar, void* dst, int x, int y, int z) {
+  if (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+        "%4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+        "[%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
 template <int BN, int EPI>
 __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
     w4_gemm_kernel(const __grid_constant__ WtMaps maps, const __grid_constant__ W4Params p) {
@@ -392,7 +410,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
     abort_s = 0;
     fence_mbar_init();
     tma_prefetch_desc(&maps.codes[0][0]);
-    tma_prefetch_desc(&maps.x[0]);
+    tma_prefetch_desc(&maps.x[0][0]);
   }
   if (warp == 1) {
     tmem_alloc_g<PAIR>(&tmem_base_s, 512);
@@ -546,7 +564,8 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
       const int K = c.K, f0 = it.mt * TILE_F + (int)rank * CTA_F;
       const bool live = f0 < c.R;  // a CTA whose rows lie behind the matrix loads no weights
       const int y = it.g * c.R + f0, ys = it.g * ((K + p.group - 1) / p.group);
-      const int cta_rows = it.n_inst / CTAS, nbox = (cta_rows + S::BOX - 1) / S::BOX;
+      const int cta_rows = it.n_inst / CTAS;
+      const bool half = cta_rows <= S::HALF;
       const int x_row = it.b_row + (int)rank * cta_rows;
       for (int ch = it.c0; ch < it.c1; ++ch) {
         if (!mbar_wait_warp(&stage_free[st], ph ^ 1u, lim, abort_flag)) {
@@ -570,20 +589,24 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
               mbar_arrive(&code_full[st]);
             }
           } else {
-            // (columns behind K read as zero)
-            if (leader) mbar_arrive_expect_tx(&x_full[st], CTAS * nbox * S::BOX * BK * 2);
-            const uint32_t xb = PAIR ? mapa_shared(smem_u32(&x_full[st]), 0) : 0u;
-#pragma unroll
-            for (int h = 0; h < BK / 64; ++h)
-#pragma unroll
-              for (int b = 0; b < S::B_ROWS / S::BOX; ++b)
-                if (b < nbox) {
-                  uint8_t* dst = xs + h * S::X_SUB + b * S::BOX * 128;
+            if (leader)
+              mbar_arrive_expect_tx(&x_full[st], CTAS * (half ? S::HALF : S::B_ROWS) * BK * 2);
+            const uint32_t xb = PAIR ? mapa_shared(smem_u32(&x_full[st]), 0) : smem_u32(&x_full[st]);
+            if ((K & 63) == 0 || (ch + 1) * BK <= K) {  // one copy (each costs the issuing lane some 85 cycles)
+              tma_load_3d<PAIR>(&maps.x[it.cls][half], xb, xs, 0, x_row, ch * (BK / 64));
+            } else {  // the last chunk of a K that ends inside 64 columns
+#pragma unroll 1
+              for (int h = 0; h < BK / 64; ++h) {
+                uint8_t* dst = xs + h * (half ? S::X_SUB / 2 : S::X_SUB);
+                for (int b = 0; b < (half ? 1 : 2); ++b)
                   if (PAIR)
-                    tma_load_2d_pair(&maps.x[it.cls], xb, dst, ch * BK + h * 64, x_row + b * S::BOX);
+                    tma_load_2d_pair(&maps.xt[it.cls], xb, dst + b * S::HALF * 128, ch * BK + h * 64,
+                                     x_row + b * S::HALF);
                   else
-                    tma_load_2d(&maps.x[it.cls], &x_full[st], dst, ch * BK + h * 64, x_row + b * S::BOX);
-                }
+                    tma_load_2d(&maps.xt[it.cls], &x_full[st], dst + b * S::HALF * 128, ch * BK + h * 64,
+                                x_row + b * S::HALF);
+              }
+            }
           }
         }
         __syncwarp();
@@ -621,6 +644,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(acc * BN);
         const uint32_t idesc = idesc_bf16(128 * CTAS, it.n_inst);
+        const uint32_t sub = (it.n_inst / CTAS <= S::HALF ? S::X_SUB / 2 : S::X_SUB) >> 4;  // 64 columns further
 #pragma unroll 1
         for (int ch = it.c0; ch < it.c1; ++ch) {
           if (!mbar_wait_warp(&x_full[st], ph, lim, abort_flag) || !mbar_wait_warp(&a_full[st], ph, lim, abort_flag)) {
@@ -633,7 +657,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
             const uint32_t a = tmem + (uint32_t)(S::NUM_ACC * BN + as * S::A_COLS);
 #pragma unroll
             for (int kk = 0; kk < BK / 16; ++kk)
-              umma_ts<PAIR>(d, a + 8 * kk, bd + (kk >> 2) * (S::X_SUB >> 4) + 2 * (kk & 3), idesc,
+              umma_ts<PAIR>(d, a + 8 * kk, bd + (kk >> 2) * sub + 2 * (kk & 3), idesc,
                             kk > 0 ? 1u : (uint32_t)(ch > it.c0));
             umma_commit_all<PAIR>(&stage_free[st]);
             if (ch + 1 == it.c1) umma_commit_all<PAIR>(&acc_full[acc]);
@@ -901,6 +925,19 @@ bool make_map_2d(CUtensorMap* m, const void* ptr, CUtensorMapDataType type, long
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// bf16 rows [rows, K] as [K / 64][rows][64]: one copy brings `subs` groups of 64 columns
+// of box_rows rows, each group with the 128-byte swizzle of a K-major operand.
+bool make_map_rows(CUtensorMap* m, const void* ptr, long long K, long long rows, int box_rows, int subs) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc || !ptr || K <= 0 || rows <= 0 || K % 8) return false;
+  const cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)std::max(1LL, K / 64)};
+  const cuuint64_t strides[2] = {(cuuint64_t)K * 2, 128};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)subs}, es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int BN, int EPI>
 cudaError_t launch_impl(const W4Params& p, cudaStream_t s) {
   using S = WtShape<BN>;
@@ -918,8 +955,10 @@ cudaError_t launch_impl(const W4Params& p, cudaStream_t s) {
                        2LL * c.R, ROWS, S::BK / p.group, CU_TENSOR_MAP_SWIZZLE_NONE))
         return cudaErrorInvalidValue;
     }
-    if (!make_map_2d(&maps.x[i], c.b, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, c.K, c.b_rows, 2LL * c.K, 64, S::BOX,
-                     CU_TENSOR_MAP_SWIZZLE_128B))
+    if (!make_map_2d(&maps.xt[i], c.b, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, c.K, c.b_rows, 2LL * c.K, 64, S::HALF,
+                     CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map_rows(&maps.x[i][0], c.b, c.K, c.b_rows, S::B_ROWS, S::BK / 64) ||
+        !make_map_rows(&maps.x[i][1], c.b, c.K, c.b_rows, S::HALF, S::BK / 64))
       return cudaErrorInvalidValue;
   }
   auto kern = w4_gemm_kernel<BN, EPI>;
