@@ -988,9 +988,9 @@ static moe_status_t check_w4_cfg(const moe_config_t* cfg) {
   const moe_config_t& c = *cfg;
   if (c.dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
   if (c.d % 32 || c.f % 32 || (c.n_shared && c.f_shared % 32)) return MOE_ERR_UNSUPPORTED;  // 16-byte code rows
-  // weight rows and groups are 32-bit coordinates
+  // weight rows and groups, and costs in the tile schedule, are 32-bit numbers
   const long long n = std::max(c.m, c.n_shared), r = std::max(c.d, std::max(c.f, c.n_shared ? c.f_shared : 0));
-  if (n * r >= (1LL << 31)) return MOE_ERR_UNSUPPORTED;
+  if (n * r >= (1LL << 31) || r > (1 << 23)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

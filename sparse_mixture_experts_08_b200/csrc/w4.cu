@@ -97,6 +97,21 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
+// The same times a scale s, in one rounding and one instruction less: bf16 with exponent
+// bits 0x4180 and the code at mantissa bit 3 is 16 + code, and (16 + code) s - 24 s is
+// rounded once. This needs 24 s to be a bf16 number: w4_scale_is_short says that s has at
+// most 6 significant bits (the quantizer's have 5) and is not so large that 24 s overflows.
+__device__ __forceinline__ uint32_t w4_pair_scaled(uint32_t w, int e, uint32_t ss, uint32_t ms) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;"
+      : "=r"(r)
+      : "r"(e == 0 ? w << 3 : w >> (4 * e - 3)), "r"(0x00780078u), "r"(0x41804180u));  // (w & a) | b
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(r), "r"(ss), "r"(ms));
+  return d;
+}
+__device__ __forceinline__ bool w4_scale_is_short(uint32_t s) { return (s & 3u) == 0u && (s & 0x7FFFu) < 0x7C00u; }
+
 // The inverse: bf16(code * scale) (exact for the quantizer's scales). A lane turns one
 // word (8 columns) of 4 neighbouring rows into 16 bytes each.
 template <int G>
@@ -201,12 +216,22 @@ struct WtMaps {
   CUtensorMap xt[2];    // 64 columns x HALF rows, columns behind K as zero
 };
 
+// A piece of work: chunks [c0, c1) of K of one tile.
+struct WtItem {
+  int cls, g, mt, rows, b_row, out_row, c0, c1;
+  int wa, wb;  // walkers that share the tile
+};
+
+constexpr int WT_ITEMS = 128;  // pieces of a walker that are worked out before it starts
+
 struct WtSched {
-  long long cost_start[WT_MAX_GROUPS + 1];
-  int tile_start[WT_MAX_GROUPS + 1];
+  int tile_start[WT_MAX_GROUPS + 1];  // groups in walk order: first tile
+  int cost[WT_MAX_GROUPS + 1];        // and cost of the cut tiles before
   int gid[WT_MAX_GROUPS], rows[WT_MAX_GROUPS], brow[WT_MAX_GROUPS];
-  int total, rounds, t0;   // tiles; rounds of whole tiles; first cut tile
-  long long base, cut, per;  // cost before t0, of the cut tiles, of a walker's share
+  int rounds, t0;   // rounds of whole tiles; first cut tile
+  int cut, per;     // cost of the cut tiles, of a walker's share
+  int t_first, n;   // this walker's first cut tile, all its pieces
+  WtItem items[WT_ITEMS];
 };
 
 template <int BN>
@@ -218,78 +243,67 @@ __device__ __forceinline__ int wt_height(int rows) {
 // that of expanding the codes (as long as 64 rows take).
 __device__ __forceinline__ int wt_weight(int height) { return max(height >> 4, 4); }
 
-struct WtItem {
-  int cls, g, mt, rows, n_inst, b_row, out_row, nc, c0, c1;
-  int wa, wb;  // walkers that share the tile
-};
+template <int BN>
+__device__ __forceinline__ int wt_chunks(const W4Class& c) {
+  return (c.K + WtShape<BN>::BK - 1) / WtShape<BN>::BK;
+}
+
+// Largest position whose entry is at most v (entries ascend, the first is at most v).
+__device__ __forceinline__ int wt_find(const int* e, int n, int v) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (e[mid] <= v) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Piece i of a walker (i < s.n); a cut tile may leave it an empty one.
+template <int BN>
+__device__ __forceinline__ WtItem wt_item(const W4Params& p, const WtSched& s, int G, int walker, int walkers, int i) {
+  WtItem it;
+  const bool whole = i < s.rounds;
+  const int tile = whole ? i * walkers + ((i & 1) ? walkers - 1 - walker : walker) : s.t_first + i - s.rounds;
+  const int pos = wt_find(s.tile_start, G, tile);
+  const int gi = s.gid[pos], G0 = p.cls[0].n_groups;
+  it.cls = gi < G0 ? 0 : 1;
+  it.g = gi - (it.cls ? G0 : 0);
+  const W4Class& c = p.cls[it.cls];
+  const int rows = s.rows[gi], NT = (rows + BN - 1) / BN, h = wt_height<BN>(rows);
+  const int local = tile - s.tile_start[pos], nt = local % NT, nc = wt_chunks<BN>(c);
+  it.mt = local / NT;
+  it.rows = min(h, rows - nt * h);
+  it.b_row = s.brow[gi] + nt * h;
+  it.out_row = (c.seg_off ? s.brow[gi] : it.g * c.out_group_stride) + nt * h;
+  it.c0 = 0;
+  it.c1 = nc;
+  it.wa = it.wb = walker;
+  if (!whole) {
+    // chunk j of the tile costs w and starts at `at` + j w: it is walker (that / per)'s
+    const int w = wt_weight(h), at = s.cost[pos] + (tile - max(s.tile_start[pos], s.t0)) * nc * w;
+    const int lo = walker * s.per, hi = min(lo + s.per, s.cut);
+    it.c0 = lo > at ? (lo - at + w - 1) / w : 0;
+    it.c1 = min(nc, (hi - at + w - 1) / w);
+    it.wa = at / s.per;
+    it.wb = (at + (nc - 1) * w) / s.per;
+  }
+  return it;
+}
 
 // The list of a walker's pieces of work, walked alike by every role.
 template <int BN>
 struct WtWalk {
   const W4Params& p;
   const WtSched& s;
-  int G, walker, walkers;
-  int r;
-  int t;            // next cut tile (-1: not looked up yet)
-  long long at;     // its cost, from the first cut tile on
+  int G, walker, walkers, i;
 
   __device__ __forceinline__ WtWalk(const W4Params& p_, const WtSched& s_, int G_, int w, int ws)
-      : p(p_), s(s_), G(G_), walker(w), walkers(ws), r(0), t(-1), at(0) {}
-
-  __device__ __forceinline__ int decode(int tile, WtItem& it) const {
-    int lo = 0, hi = G - 1;  // largest position with tile_start[pos] <= tile
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (s.tile_start[mid] <= tile) lo = mid; else hi = mid - 1;
-    }
-    const int gi = s.gid[lo], G0 = p.cls[0].n_groups;
-    it.cls = gi < G0 ? 0 : 1;
-    it.g = gi - (it.cls ? G0 : 0);
-    const W4Class& c = p.cls[it.cls];
-    const int rows = s.rows[gi], NT = (rows + BN - 1) / BN, h = wt_height<BN>(rows);
-    const int local = tile - s.tile_start[lo], nt = local % NT;
-    it.mt = local / NT;
-    it.rows = min(h, rows - nt * h);
-    it.n_inst = (it.rows + 15) & ~15;
-    it.b_row = s.brow[gi] + nt * h;
-    it.out_row = (c.seg_off ? s.brow[gi] : it.g * c.out_group_stride) + nt * h;
-    it.nc = (c.K + WtShape<BN>::BK - 1) / WtShape<BN>::BK;
-    return wt_weight(h);
-  }
+      : p(p_), s(s_), G(G_), walker(w), walkers(ws), i(0) {}
 
   __device__ __forceinline__ bool next(WtItem& it) {
-    if (r < s.rounds) {
-      decode(r * walkers + ((r & 1) ? walkers - 1 - walker : walker), it);
-      ++r;
-      it.c0 = 0;
-      it.c1 = it.nc;
-      it.wa = it.wb = walker;
-      return true;
-    }
-    const long long lo = walker * s.per, hi = min(lo + s.per, s.cut);
-    if (t < 0) {
-      if (lo >= hi) return false;
-      int a = 0, b = G - 1;  // largest position with cost_start[pos] <= base + lo
-      while (a < b) {
-        const int mid = (a + b + 1) >> 1;
-        if (s.cost_start[mid] <= s.base + lo) a = mid; else b = mid - 1;
-      }
-      const int h = wt_height<BN>(s.rows[s.gid[a]]);
-      const W4Class& c = p.cls[s.gid[a] < p.cls[0].n_groups ? 0 : 1];
-      const long long tc = (long long)((c.K + WtShape<BN>::BK - 1) / WtShape<BN>::BK) * wt_weight(h);
-      const long long k = (s.base + lo - s.cost_start[a]) / tc;
-      t = s.tile_start[a] + (int)k;
-      at = s.cost_start[a] + k * tc - s.base;
-    }
-    while (at < hi) {
-      const int w = decode(t, it);
-      const long long c0 = lo > at ? (lo - at + w - 1) / w : 0, c1 = (hi - at + w - 1) / w;
-      it.c0 = (int)c0;
-      it.c1 = (int)min(c1, (long long)it.nc);
-      it.wa = (int)(at / s.per);
-      it.wb = (int)((at + (long long)(it.nc - 1) * w) / s.per);
-      at += (long long)it.nc * w;
-      ++t;
+    while (i < s.n) {
+      it = i < WT_ITEMS ? s.items[i] : wt_item<BN>(p, s, G, walker, walkers, i);
+      ++i;
       if (it.c0 < it.c1) return true;
     }
     return false;
@@ -490,56 +504,58 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
           tl[b] += tiles;
         }
     }
+    // whole rounds and cut tiles; an earlier kernel of the call that flagged a device
+    // error leaves tables that are not used
+    const int prior = p.status ? *reinterpret_cast<volatile int*>(p.status) : 0;
+    const int total = __any_sync(0xffffffffu, prior != 0) ? 0 : base_t;
     if (lane == 0) sched.tile_start[G] = base_t;
     __syncwarp();
-    // cost before each position, and the split into whole and cut tiles
-    auto tile_cost = [&](const int gi) {
-      const int K = p.cls[gi < G0 ? 0 : 1].K;
-      return (long long)((K + S::BK - 1) / S::BK) * wt_weight(wt_height<BN>(sched.rows[gi]));
+    const int rounds = total / walkers - (total >= walkers && total % walkers ? 1 : 0), t0 = rounds * walkers;
+    auto cut_cost = [&](const int pos) {
+      const int gi = sched.gid[pos], n = sched.tile_start[pos + 1] - max(sched.tile_start[pos], t0);
+      return n > 0 && total ? n * wt_chunks<BN>(p.cls[gi < G0 ? 0 : 1]) * wt_weight(wt_height<BN>(sched.rows[gi])) : 0;
     };
-    long long sum = 0;
-    for (int i = lo; i < hi; ++i)
-      sum += (sched.tile_start[i + 1] - sched.tile_start[i]) * tile_cost(sched.gid[i]);
-    long long inc = sum;
+    int sum = 0;
+    for (int i = lo; i < hi; ++i) sum += cut_cost(i);
+    int inc = sum;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, inc, off);
+      const int v = __shfl_up_sync(0xffffffffu, inc, off);
       if (lane >= off) inc += v;
     }
-    long long run = inc - sum;
+    int run = inc - sum;
     for (int i = lo; i < hi; ++i) {
-      sched.cost_start[i] = run;
-      run += (sched.tile_start[i + 1] - sched.tile_start[i]) * tile_cost(sched.gid[i]);
+      sched.cost[i] = run;
+      run += cut_cost(i);
     }
-    if (lane == 31) sched.cost_start[G] = inc;
+    const int cut = __shfl_sync(0xffffffffu, inc, 31);
     __syncwarp();
     if (lane == 0) {
-      // an earlier kernel of the call flagged a device error: its tables are not used
-      const int prior = p.status ? *reinterpret_cast<volatile int*>(p.status) : 0;
-      const int total = prior ? 0 : base_t;
-      int rounds = total / walkers;
-      if (rounds > 0 && total % walkers) --rounds;
-      const int t0 = rounds * walkers;
-      long long base = 0, cut = 0;
-      if (t0 < total) {
-        int a = 0, b = G - 1;
-        while (a < b) {
-          const int mid = (a + b + 1) >> 1;
-          if (sched.tile_start[mid] <= t0) a = mid; else b = mid - 1;
-        }
-        base = sched.cost_start[a] + (t0 - sched.tile_start[a]) * tile_cost(sched.gid[a]);
-        cut = sched.cost_start[G] - base;
-      }
-      sched.total = total;
-      sched.rounds = rounds;
-      sched.t0 = t0;
-      sched.base = base;
-      sched.cut = cut;
       // (at least 512 columns of the heaviest tile, so that every walker between a tile's
       // first and last one has a part of it)
-      sched.per = max((cut + walkers - 1) / walkers, (long long)(512 / BK * max(BN / 16, 4)));
+      const int share = max((cut + walkers - 1) / walkers, 512 / BK * max(BN / 16, 4));
+      const int from = walker * share, to = min(from + share, cut);
+      auto tile_at = [&](const int x) {
+        const int pos = wt_find(sched.cost, G, x), gi = sched.gid[pos];
+        const int tc = wt_chunks<BN>(p.cls[gi < G0 ? 0 : 1]) * wt_weight(wt_height<BN>(sched.rows[gi]));
+        return max(sched.tile_start[pos], t0) + (x - sched.cost[pos]) / tc;
+      };
+      int n = 0, first = 0;
+      if (from < to) {
+        first = tile_at(from);
+        n = tile_at(to - 1) - first + 1;
+      }
+      sched.rounds = rounds;
+      sched.t0 = t0;
+      sched.cut = cut;
+      sched.per = share;
+      sched.t_first = first;
+      sched.n = rounds + n;
     }
   }
+  __syncthreads();
+  if (threadIdx.x < min(sched.n, WT_ITEMS))
+    sched.items[threadIdx.x] = wt_item<BN>(p, sched, G, walker, walkers, threadIdx.x);
   __syncwarp();
   tc_fence_before();
   __syncthreads();
@@ -564,7 +580,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
       const int K = c.K, f0 = it.mt * TILE_F + (int)rank * CTA_F;
       const bool live = f0 < c.R;  // a CTA whose rows lie behind the matrix loads no weights
       const int y = it.g * c.R + f0, ys = it.g * ((K + p.group - 1) / p.group);
-      const int cta_rows = it.n_inst / CTAS;
+      const int cta_rows = ((it.rows + 15) & ~15) / CTAS;
       const bool half = cta_rows <= S::HALF;
       const int x_row = it.b_row + (int)rank * cta_rows;
       for (int ch = it.c0; ch < it.c1; ++ch) {
@@ -643,8 +659,9 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
         }
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(acc * BN);
-        const uint32_t idesc = idesc_bf16(128 * CTAS, it.n_inst);
-        const uint32_t sub = (it.n_inst / CTAS <= S::HALF ? S::X_SUB / 2 : S::X_SUB) >> 4;  // 64 columns further
+        const int n_inst = (it.rows + 15) & ~15;
+        const uint32_t idesc = idesc_bf16(128 * CTAS, n_inst);
+        const uint32_t sub = (n_inst / CTAS <= S::HALF ? S::X_SUB / 2 : S::X_SUB) >> 4;  // 64 columns further
 #pragma unroll 1
         for (int ch = it.c0; ch < it.c1; ++ch) {
           if (!mbar_wait_warp(&x_full[st], ph, lim, abort_flag) || !mbar_wait_warp(&a_full[st], ph, lim, abort_flag)) {
@@ -714,22 +731,38 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
           }
           tc_fence_after();
           const uint32_t base = smem_base + st * S::STAGE_BYTES;
+          uint32_t sc[BK / 32];
+          bool few = true;
 #pragma unroll
-          for (int h = 0; h < BK / 64; ++h) {  // 64 columns at a time
+          for (int i = 0; i < BK / 32; ++i) {
+            const int gi = (i * 32) >> gl2;
+            sc[i] = lds16(base + scale_off + gi * SCALE_PITCH);
+            if (ch * (BK >> gl2) + gi >= ng) sc[i] = 0u;  // behind K: x is zero there, the scale not this row's
+            few = few && w4_scale_is_short(sc[i]);
+          }
+          const uint32_t t_slot = t_lane + as * S::A_COLS;
+          auto columns64 = [&](const int h, auto pair) {
             uint32_t v[32];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const uint4 c4 = lds128(base + code_off + (((2 * h + i) ^ sw) << 4));
-              const int gi = (h * 64 + i * 32) >> gl2;
-              uint32_t ss = lds16(base + scale_off + gi * SCALE_PITCH) * 0x10001u;
-              if (ch * (BK >> gl2) + gi >= ng) ss = 0u;  // behind K: x is zero there, the scale not this row's
               const uint32_t w[4] = {c4.x, c4.y, c4.z, c4.w};
+              const uint32_t ss = sc[2 * h + i] * 0x10001u, ms = mul_bf16x2(ss, 0xC1C0C1C0u);  // s, -24 s
 #pragma unroll
               for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[i * 16 + j * 4 + e] = mul_bf16x2(w4_pair(w[j] >> (4 * e)), ss);
+                for (int e = 0; e < 4; ++e) v[i * 16 + j * 4 + e] = pair(w[j], e, ss, ms);
             }
-            tmem_st_x32(t_lane + as * S::A_COLS + h * 32, v);
+            tmem_st_x32(t_slot + h * 32, v);
+          };
+          if (__all_sync(0xffffffffu, few)) {
+#pragma unroll
+            for (int h = 0; h < BK / 64; ++h)
+              columns64(h, [](uint32_t w, int e, uint32_t ss, uint32_t ms) { return w4_pair_scaled(w, e, ss, ms); });
+          } else {  // scales of another origin
+#pragma unroll
+            for (int h = 0; h < BK / 64; ++h)
+              columns64(h, [](uint32_t w, int e, uint32_t ss, uint32_t) { return mul_bf16x2(w4_pair(w >> (4 * e)), ss); });
           }
           tmem_st_wait();
           tc_fence_before();
