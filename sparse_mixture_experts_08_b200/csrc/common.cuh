@@ -78,6 +78,23 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, u
   }
 }
 
+// Waits for two barriers at the same parity, their polls overlapped.
+__device__ __forceinline__ bool mbar_wait_warp2(uint64_t* bar0, uint64_t* bar1, uint32_t parity,
+                                                unsigned long long limit_ns, const volatile int* abort_flag) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %3;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 q, [%2], %3;\n\t"
+      "and.pred p, p, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar0)), "r"(smem_u32(bar1)), "r"(parity)
+      : "memory");
+  if (__all_sync(0xffffffffu, ok)) return true;
+  return mbar_wait_warp(bar0, parity, limit_ns, abort_flag) && mbar_wait_warp(bar1, parity, limit_ns, abort_flag);
+}
+
 // Bulk copy global -> shared (the copy engine, no tensor map): bytes % 16 == 0, both
 // addresses 16-byte aligned; completion counted on `bar`.
 __device__ __forceinline__ void bulk_copy_g2s(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {

@@ -176,9 +176,9 @@ __global__ void __launch_bounds__(QW_WARPS * 32)
 // commit 46, and some hundred a turn of a long loop), so it commits once a chunk.
 // Barriers of a stage of the ring: codes (local) -> expanders; input rows (PAIR: of both
 // CTAs, at the leader) -> issuer; expanded (PAIR: at the leader) -> issuer; free: the
-// issuer's commit. A chunk's slot in tensor memory is free once the chunk A_SLOTS before
-// it is done, which that chunk's stage barrier tells (STAGES >= A_SLOTS: it cannot be a
-// phase further yet). Every wait is bounded in time as in tc_gemm.cu.
+// issuer's commit. A slot in tensor memory is free once an earlier chunk is done, which
+// that chunk's stage barrier tells (no more than STAGES chunks earlier: the barrier cannot
+// be a phase further yet). Every wait is bounded in time as in tc_gemm.cu.
 constexpr int WT_EXPAND_WARP = 4;
 constexpr int WT_SMEM_BUDGET = 196 * 1024;
 constexpr int WT_MAX_GROUPS = 1040;
@@ -202,12 +202,16 @@ struct WtShape {
   static constexpr int STAGES_RAW = WT_SMEM_BUDGET / STAGE_BYTES;
   static constexpr int STAGES = STAGES_RAW > 12 ? 12 : STAGES_RAW;
   static constexpr int NUM_ACC = 2;
-  static constexpr int A_COLS = BK / 2;  // tensor-memory columns of an A slot (two bf16 each)
+  // Expanded weights in tensor memory: a ring of slots of 128 columns of K (64 columns of
+  // two bf16 each), BK / 128 of them a chunk. A slot is free once the chunk that used it
+  // last is done: OLD0 chunks before this one for a chunk's first slot, OLD1 for its last.
+  static constexpr int A_COLS = 64, UNITS = BK / 128;
   static constexpr int A_SLOTS_RAW = (512 - NUM_ACC * BN) / A_COLS;
   static constexpr int A_SLOTS = A_SLOTS_RAW > 8 ? 8 : A_SLOTS_RAW;
+  static constexpr int OLD0 = (A_SLOTS + UNITS - 1) / UNITS, OLD1 = A_SLOTS / UNITS;
   static constexpr int DYN_SMEM = STAGES * STAGE_BYTES + 1024;
   static_assert(BN % 16 == 0 && BN >= 16 && BN <= 256 && HALF % 8 == 0, "tile");
-  static_assert(STAGE_BYTES % 1024 == 0 && A_SLOTS >= 2 && STAGES >= A_SLOTS, "ring");
+  static_assert(STAGE_BYTES % 1024 == 0 && A_SLOTS >= 2 * UNITS && STAGES >= OLD0, "ring");
 };
 
 struct WtMaps {
@@ -217,9 +221,10 @@ struct WtMaps {
 };
 
 // A piece of work: chunks [c0, c1) of K of one tile.
-struct WtItem {
+struct alignas(16) WtItem {
   int cls, g, mt, rows, b_row, out_row, c0, c1;
   int wa, wb;  // walkers that share the tile
+  int pad[2];
 };
 
 constexpr int WT_ITEMS = 128;  // pieces of a walker that are worked out before it starts
@@ -664,23 +669,27 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
         const uint32_t sub = (n_inst / CTAS <= S::HALF ? S::X_SUB / 2 : S::X_SUB) >> 4;  // 64 columns further
 #pragma unroll 1
         for (int ch = it.c0; ch < it.c1; ++ch) {
-          if (!mbar_wait_warp(&x_full[st], ph, lim, abort_flag) || !mbar_wait_warp(&a_full[st], ph, lim, abort_flag)) {
+          if (!mbar_wait_warp2(&x_full[st], &a_full[st], ph, lim, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
           if (elect_one()) {
             const uint64_t bd = sdesc_sw128(smem_base + st * S::STAGE_BYTES);
-            const uint32_t a = tmem + (uint32_t)(S::NUM_ACC * BN + as * S::A_COLS);
+            uint32_t a[S::UNITS];
+#pragma unroll
+            for (int u = 0; u < S::UNITS; ++u)
+              a[u] = tmem + (uint32_t)(S::NUM_ACC * BN + (as + u >= A_SLOTS ? as + u - A_SLOTS : as + u) * S::A_COLS);
 #pragma unroll
             for (int kk = 0; kk < BK / 16; ++kk)
-              umma_ts<PAIR>(d, a + 8 * kk, bd + (kk >> 2) * sub + 2 * (kk & 3), idesc,
+              umma_ts<PAIR>(d, a[kk >> 3] + 8 * (kk & 7), bd + (kk >> 2) * sub + 2 * (kk & 3), idesc,
                             kk > 0 ? 1u : (uint32_t)(ch > it.c0));
             umma_commit_all<PAIR>(&stage_free[st]);
             if (ch + 1 == it.c1) umma_commit_all<PAIR>(&acc_full[acc]);
           }
           __syncwarp();
-          if (++as == A_SLOTS) as = 0;
+          as += S::UNITS;
+          if (as >= A_SLOTS) as -= A_SLOTS;
           if (++st == STAGES) {
             st = 0;
             ph ^= 1u;
@@ -717,53 +726,74 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
     constexpr int SCALE_PITCH = MATS == 2 ? 128 : 256;
     const int gl2 = 31 - __clz(p.group);
     const uint32_t t_lane = tmem + ((uint32_t)(q * 32) << 16) + S::NUM_ACC * BN;
-    int st = 0, as = 0, turn = 0, old = STAGES - A_SLOTS;  // old: the stage A_SLOTS chunks ago
-    uint32_t ph = 0, old_ph = 1;                            // (before the first such chunk: passes at once)
+    int st = 0, as = 0, turn = 0;
+    uint32_t ph = 0;
+    // stage and parity of the chunk `back` chunks ago (before the first such chunk: passes at once)
+    auto done = [&](const int back) {
+      const bool wrap = st < back;
+      return mbar_wait_warp(&stage_free[wrap ? st - back + STAGES : st - back], ph ^ (wrap ? 1u : 0u), lim, abort_flag);
+    };
     while (ok && walk.next(it)) {
       const int K = p.cls[it.cls].K, ng = (K + p.group - 1) >> gl2;
 #pragma unroll 1
       for (int ch = it.c0; ch < it.c1; ++ch) {
         if (turn == grp) {
-          if (!mbar_wait_warp(&code_full[st], ph, lim, abort_flag) ||
-              !mbar_wait_warp(&stage_free[old], old_ph, lim, abort_flag)) {
+          if (!mbar_wait_warp(&code_full[st], ph, lim, abort_flag)) {
             ok = false;
             break;
           }
-          tc_fence_after();
           const uint32_t base = smem_base + st * S::STAGE_BYTES;
+          uint4 cw[BK / 32];
           uint32_t sc[BK / 32];
           bool few = true;
 #pragma unroll
           for (int i = 0; i < BK / 32; ++i) {
             const int gi = (i * 32) >> gl2;
+            cw[i] = lds128(base + code_off + ((i ^ sw) << 4));
             sc[i] = lds16(base + scale_off + gi * SCALE_PITCH);
             if (ch * (BK >> gl2) + gi >= ng) sc[i] = 0u;  // behind K: x is zero there, the scale not this row's
             few = few && w4_scale_is_short(sc[i]);
           }
-          const uint32_t t_slot = t_lane + as * S::A_COLS;
+          few = __all_sync(0xffffffffu, few);
+          if (!done(S::OLD0)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
           auto columns64 = [&](const int h, auto pair) {
             uint32_t v[32];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const uint4 c4 = lds128(base + code_off + (((2 * h + i) ^ sw) << 4));
-              const uint32_t w[4] = {c4.x, c4.y, c4.z, c4.w};
+              const uint32_t w[4] = {cw[2 * h + i].x, cw[2 * h + i].y, cw[2 * h + i].z, cw[2 * h + i].w};
               const uint32_t ss = sc[2 * h + i] * 0x10001u, ms = mul_bf16x2(ss, 0xC1C0C1C0u);  // s, -24 s
 #pragma unroll
               for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[i * 16 + j * 4 + e] = pair(w[j], e, ss, ms);
             }
-            tmem_st_x32(t_slot + h * 32, v);
+            const int slot = as + (h >> 1) >= A_SLOTS ? as + (h >> 1) - A_SLOTS : as + (h >> 1);
+            tmem_st_x32(t_lane + slot * S::A_COLS + (h & 1) * 32, v);
           };
-          if (__all_sync(0xffffffffu, few)) {
+          auto short_scale = [](uint32_t w, int e, uint32_t ss, uint32_t ms) { return w4_pair_scaled(w, e, ss, ms); };
+          auto any_scale = [](uint32_t w, int e, uint32_t ss, uint32_t) { return mul_bf16x2(w4_pair(w >> (4 * e)), ss); };
 #pragma unroll
-            for (int h = 0; h < BK / 64; ++h)
-              columns64(h, [](uint32_t w, int e, uint32_t ss, uint32_t ms) { return w4_pair_scaled(w, e, ss, ms); });
-          } else {  // scales of another origin
-#pragma unroll
-            for (int h = 0; h < BK / 64; ++h)
-              columns64(h, [](uint32_t w, int e, uint32_t ss, uint32_t) { return mul_bf16x2(w4_pair(w >> (4 * e)), ss); });
+          for (int u = 0; u < S::UNITS; ++u) {
+            if (u > 0 && S::OLD1 != S::OLD0) {
+              if (!done(S::OLD1)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+            }
+            if (few) {
+              columns64(2 * u, short_scale);
+              columns64(2 * u + 1, short_scale);
+            } else {
+              columns64(2 * u, any_scale);
+              columns64(2 * u + 1, any_scale);
+            }
           }
+          if (!ok) break;
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
@@ -777,11 +807,8 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
           }
         }
         if (++turn == S::NG) turn = 0;
-        if (++as == A_SLOTS) as = 0;
-        if (++old == STAGES) {
-          old = 0;
-          old_ph ^= 1u;
-        }
+        as += S::UNITS;
+        if (as >= A_SLOTS) as -= A_SLOTS;
         if (++st == STAGES) {
           st = 0;
           ph ^= 1u;
