@@ -202,16 +202,14 @@ struct WtShape {
   static constexpr int STAGES_RAW = WT_SMEM_BUDGET / STAGE_BYTES;
   static constexpr int STAGES = STAGES_RAW > 12 ? 12 : STAGES_RAW;
   static constexpr int NUM_ACC = 2;
-  // Expanded weights in tensor memory: a ring of slots of 128 columns of K (64 columns of
-  // two bf16 each), BK / 128 of them a chunk. A slot is free once the chunk that used it
-  // last is done: OLD0 chunks before this one for a chunk's first slot, OLD1 for its last.
-  static constexpr int A_COLS = 64, UNITS = BK / 128;
+  // Expanded weights in tensor memory: a ring of slots of a chunk (two bf16 a column). A
+  // slot is free once the chunk A_SLOTS before is done.
+  static constexpr int A_COLS = BK / 2;
   static constexpr int A_SLOTS_RAW = (512 - NUM_ACC * BN) / A_COLS;
-  static constexpr int A_SLOTS = A_SLOTS_RAW > 8 ? 8 : A_SLOTS_RAW;
-  static constexpr int OLD0 = (A_SLOTS + UNITS - 1) / UNITS, OLD1 = A_SLOTS / UNITS;
+  static constexpr int A_SLOTS = A_SLOTS_RAW > 6 ? 6 : A_SLOTS_RAW;
   static constexpr int DYN_SMEM = STAGES * STAGE_BYTES + 1024;
   static_assert(BN % 16 == 0 && BN >= 16 && BN <= 256 && HALF % 8 == 0, "tile");
-  static_assert(STAGE_BYTES % 1024 == 0 && A_SLOTS >= 2 * UNITS && STAGES >= OLD0, "ring");
+  static_assert(STAGE_BYTES % 1024 == 0 && A_SLOTS >= 2 && STAGES >= A_SLOTS, "ring");
 };
 
 struct WtMaps {
@@ -589,7 +587,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
       const bool half = cta_rows <= S::HALF;
       const int x_row = it.b_row + (int)rank * cta_rows;
       for (int ch = it.c0; ch < it.c1; ++ch) {
-        if (!mbar_wait_warp(&stage_free[st], ph ^ 1u, lim, abort_flag)) {
+        if (!mbar_wait_warp<true>(&stage_free[st], ph ^ 1u, lim, abort_flag)) {
           ok = false;
           break;
         }
@@ -676,20 +674,16 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
           tc_fence_after();
           if (elect_one()) {
             const uint64_t bd = sdesc_sw128(smem_base + st * S::STAGE_BYTES);
-            uint32_t a[S::UNITS];
-#pragma unroll
-            for (int u = 0; u < S::UNITS; ++u)
-              a[u] = tmem + (uint32_t)(S::NUM_ACC * BN + (as + u >= A_SLOTS ? as + u - A_SLOTS : as + u) * S::A_COLS);
+            const uint32_t a = tmem + (uint32_t)(S::NUM_ACC * BN + as * S::A_COLS);
 #pragma unroll
             for (int kk = 0; kk < BK / 16; ++kk)
-              umma_ts<PAIR>(d, a[kk >> 3] + 8 * (kk & 7), bd + (kk >> 2) * sub + 2 * (kk & 3), idesc,
+              umma_ts<PAIR>(d, a + 8 * kk, bd + (kk >> 2) * sub + 2 * (kk & 3), idesc,
                             kk > 0 ? 1u : (uint32_t)(ch > it.c0));
             umma_commit_all<PAIR>(&stage_free[st]);
             if (ch + 1 == it.c1) umma_commit_all<PAIR>(&acc_full[acc]);
           }
           __syncwarp();
-          as += S::UNITS;
-          if (as >= A_SLOTS) as -= A_SLOTS;
+          if (++as == A_SLOTS) as = 0;
           if (++st == STAGES) {
             st = 0;
             ph ^= 1u;
@@ -728,11 +722,15 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
     const uint32_t t_lane = tmem + ((uint32_t)(q * 32) << 16) + S::NUM_ACC * BN;
     int st = 0, as = 0, turn = 0;
     uint32_t ph = 0;
-    // stage and parity of the chunk `back` chunks ago (before the first such chunk: passes at once)
-    auto done = [&](const int back) {
-      const bool wrap = st < back;
-      return mbar_wait_warp(&stage_free[wrap ? st - back + STAGES : st - back], ph ^ (wrap ? 1u : 0u), lim, abort_flag);
+    // (before the first such chunk the wait passes at once)
+    auto slot_free = [&]() {
+      const bool wrap = st < A_SLOTS;
+      return mbar_wait_warp(&stage_free[wrap ? st - A_SLOTS + STAGES : st - A_SLOTS], ph ^ (wrap ? 1u : 0u), lim,
+                            abort_flag);
     };
+    // The codes of a short chunk are fetched before the wait for its slot; those of a long
+    // one 64 columns at a time (all of them held at once slowed the unpacking).
+    constexpr bool EARLY = BK == 128;
     while (ok && walk.next(it)) {
       const int K = p.cls[it.cls].K, ng = (K + p.group - 1) >> gl2;
 #pragma unroll 1
@@ -749,51 +747,41 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
 #pragma unroll
           for (int i = 0; i < BK / 32; ++i) {
             const int gi = (i * 32) >> gl2;
-            cw[i] = lds128(base + code_off + ((i ^ sw) << 4));
+            if (EARLY) cw[i] = lds128(base + code_off + ((i ^ sw) << 4));
             sc[i] = lds16(base + scale_off + gi * SCALE_PITCH);
             if (ch * (BK >> gl2) + gi >= ng) sc[i] = 0u;  // behind K: x is zero there, the scale not this row's
             few = few && w4_scale_is_short(sc[i]);
           }
           few = __all_sync(0xffffffffu, few);
-          if (!done(S::OLD0)) {
+          if (!slot_free()) {
             ok = false;
             break;
           }
           tc_fence_after();
+          const uint32_t t_slot = t_lane + as * S::A_COLS;
           auto columns64 = [&](const int h, auto pair) {
             uint32_t v[32];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const uint32_t w[4] = {cw[2 * h + i].x, cw[2 * h + i].y, cw[2 * h + i].z, cw[2 * h + i].w};
+              const uint4 c4 = EARLY ? cw[2 * h + i] : lds128(base + code_off + (((2 * h + i) ^ sw) << 4));
+              const uint32_t w[4] = {c4.x, c4.y, c4.z, c4.w};
               const uint32_t ss = sc[2 * h + i] * 0x10001u, ms = mul_bf16x2(ss, 0xC1C0C1C0u);  // s, -24 s
 #pragma unroll
               for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[i * 16 + j * 4 + e] = pair(w[j], e, ss, ms);
             }
-            const int slot = as + (h >> 1) >= A_SLOTS ? as + (h >> 1) - A_SLOTS : as + (h >> 1);
-            tmem_st_x32(t_lane + slot * S::A_COLS + (h & 1) * 32, v);
+            tmem_st_x32(t_slot + h * 32, v);
           };
-          auto short_scale = [](uint32_t w, int e, uint32_t ss, uint32_t ms) { return w4_pair_scaled(w, e, ss, ms); };
-          auto any_scale = [](uint32_t w, int e, uint32_t ss, uint32_t) { return mul_bf16x2(w4_pair(w >> (4 * e)), ss); };
+          if (few) {
 #pragma unroll
-          for (int u = 0; u < S::UNITS; ++u) {
-            if (u > 0 && S::OLD1 != S::OLD0) {
-              if (!done(S::OLD1)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-            }
-            if (few) {
-              columns64(2 * u, short_scale);
-              columns64(2 * u + 1, short_scale);
-            } else {
-              columns64(2 * u, any_scale);
-              columns64(2 * u + 1, any_scale);
-            }
+            for (int h = 0; h < BK / 64; ++h)
+              columns64(h, [](uint32_t w, int e, uint32_t ss, uint32_t ms) { return w4_pair_scaled(w, e, ss, ms); });
+          } else {  // scales of another origin
+#pragma unroll
+            for (int h = 0; h < BK / 64; ++h)
+              columns64(h, [](uint32_t w, int e, uint32_t ss, uint32_t) { return mul_bf16x2(w4_pair(w >> (4 * e)), ss); });
           }
-          if (!ok) break;
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
@@ -807,8 +795,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
           }
         }
         if (++turn == S::NG) turn = 0;
-        as += S::UNITS;
-        if (as >= A_SLOTS) as -= A_SLOTS;
+        if (++as == A_SLOTS) as = 0;
         if (++st == STAGES) {
           st = 0;
           ph ^= 1u;
