@@ -64,15 +64,15 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, unsign
 
 // The same wait by a whole converged warp, which stays converged: all lanes poll (one lane
 // polling for the others costs more: 200 cycles against 84 for a barrier that is ready,
-// measured alone) and vote. NAP: sleep between polls, for waits of microseconds whose
+// measured alone) and vote. NAP_NS: sleep between polls, for waits of microseconds whose
 // polls would slow the other warps' (a ready barrier took 160 cycles beside 20 pollers).
-template <bool NAP = false>
+template <int NAP_NS = 0>
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, unsigned long long limit_ns,
                                                const volatile int* abort_flag) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   const uint64_t t0 = globaltimer_ns();
   while (true) {
-    if (NAP) __nanosleep(100);
+    if (NAP_NS) __nanosleep(NAP_NS);
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     if (__any_sync(0xffffffffu, *abort_flag != 0 || globaltimer_ns() - t0 > limit_ns)) return false;
   }

@@ -169,9 +169,9 @@ __global__ void __launch_bounds__(QW_WARPS * 32)
 // fp32 partial sums in the workspace: whichever warp finishes last adds them in the order
 // of K, so the result does not depend on who that is, and no one waits.
 //
-// Warps: 0 and 2 TMA producers (codes and scales; input rows), 1 matrix issuer (PAIR: in
-// the leader CTA) and owner of the tensor memory, then NG groups of four that expand
-// alternate chunks, then the epilogue's. The issuer's instruction stream is what bounded
+// Warps: 0 and 2 TMA producers (codes and scales; input rows), 1 (and 3) matrix issuers
+// (PAIR: in the leader CTA), 1 also owner of the tensor memory, then two teams that expand alternate
+// chunks (four warps for each 128 columns), then the epilogue's. The issuer's instruction stream is what bounded
 // the first forms of this kernel (a ready barrier costs it 84 cycles, a product 20, a
 // commit 46, and some hundred a turn of a long loop), so it commits once a chunk.
 // Barriers of a stage of the ring: codes (local) -> expanders; input rows (PAIR: of both
@@ -188,9 +188,9 @@ template <int BN>
 struct WtShape {
   static constexpr bool PAIR = BN >= 64;
   static constexpr int BK = PAIR ? 128 : 256;          // columns of K a stage
-  static constexpr int NG = PAIR ? 2 : 3;              // groups of expanding warps
+  static constexpr int TEAMS = 2, UNITS = BK / 128;    // teams of expanding warps: four for each 128 columns
   static constexpr int EW = PAIR ? 8 : 4;              // epilogue warps
-  static constexpr int EPI_WARP = WT_EXPAND_WARP + 4 * NG;
+  static constexpr int EPI_WARP = WT_EXPAND_WARP + 4 * TEAMS * UNITS;
   static constexpr int THREADS = 32 * (EPI_WARP + EW);
   static constexpr int B_ROWS = PAIR ? BN / 2 : BN;    // input rows a CTA
   static constexpr int HALF = B_ROWS / 2;               // staged rows where half of a CTA's suffice
@@ -201,11 +201,14 @@ struct WtShape {
   static constexpr int STAGE_BYTES = X_BYTES + CODE_BYTES + SCALE_BYTES;
   static constexpr int STAGES_RAW = WT_SMEM_BUDGET / STAGE_BYTES;
   static constexpr int STAGES = STAGES_RAW > 12 ? 12 : STAGES_RAW;
-  static constexpr int NUM_ACC = 2;
+  // Issuers: short segments have two (in warps 1 and 3) that take alternate chunks, each
+  // with a sum of its own, since one's instruction stream would set the pace.
+  static constexpr int ISSUERS = PAIR ? 1 : 2;
+  static constexpr int NUM_ACC = 2, ACC_COLS = ISSUERS * BN;
   // Expanded weights in tensor memory: a ring of slots of a chunk (two bf16 a column). A
   // slot is free once the chunk A_SLOTS before is done.
   static constexpr int A_COLS = BK / 2;
-  static constexpr int A_SLOTS_RAW = (512 - NUM_ACC * BN) / A_COLS;
+  static constexpr int A_SLOTS_RAW = (512 - NUM_ACC * ACC_COLS) / A_COLS;
   static constexpr int A_SLOTS = A_SLOTS_RAW > 6 ? 6 : A_SLOTS_RAW;
   static constexpr int DYN_SMEM = STAGES * STAGE_BYTES + 1024;
   static_assert(BN % 16 == 0 && BN >= 16 && BN <= 256 && HALF % 8 == 0, "tile");
@@ -416,14 +419,14 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(&code_full[i], 1);
       mbar_init(&x_full[i], 1);
-      mbar_init(&a_full[i], 4 * CTAS);  // four expanding warps of each CTA
+      mbar_init(&a_full[i], 4 * S::UNITS * CTAS);  // a team of each CTA
       mbar_init(&stage_free[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_full[i], S::ISSUERS);
       mbar_init(&acc_free[i], EW * CTAS);  // the epilogue warps of each CTA
     }
-    mbar_init(&drain_bar, 1);
+    mbar_init(&drain_bar, S::ISSUERS);
     abort_s = 0;
     fence_mbar_init();
     tma_prefetch_desc(&maps.codes[0][0]);
@@ -587,7 +590,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
       const bool half = cta_rows <= S::HALF;
       const int x_row = it.b_row + (int)rank * cta_rows;
       for (int ch = it.c0; ch < it.c1; ++ch) {
-        if (!mbar_wait_warp<true>(&stage_free[st], ph ^ 1u, lim, abort_flag)) {
+        if (!mbar_wait_warp<100>(&stage_free[st], ph ^ 1u, lim, abort_flag)) {
           ok = false;
           break;
         }
@@ -650,10 +653,12 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
                        WT_DRAIN_LIMIT_NS, &never))
           set_status(p.status, MOE_ERR_TIMEOUT);
       }
-  } else if (warp == 1) {
-    // ---------------------------------------------------------------- matrix issuer
-    if (leader) {
-      int st = 0, as = 0, acc = 0;
+  } else if (warp == 1 || warp == 3) {
+    // ---------------------------------------------------------------- matrix issuers
+    constexpr int IS = S::ISSUERS;
+    const int me = warp >> 1;  // the chunks n (counted over all pieces) with n % IS == me are this issuer's
+    if (leader && me < IS) {
+      int st = me, as = me, acc = 0, n0 = 0;
       uint32_t ph = 0, accph = 0;
       while (ok && walk.next(it)) {
         if (!mbar_wait_warp(&acc_free[acc], accph ^ 1u, lim, abort_flag)) {
@@ -661,12 +666,14 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
           break;
         }
         tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)(acc * BN);
+        const uint32_t d = tmem + (uint32_t)(acc * S::ACC_COLS + me * BN);
         const int n_inst = (it.rows + 15) & ~15;
         const uint32_t idesc = idesc_bf16(128 * CTAS, n_inst);
         const uint32_t sub = (n_inst / CTAS <= S::HALF ? S::X_SUB / 2 : S::X_SUB) >> 4;  // 64 columns further
+        const int first = it.c0 + (IS == 2 && (n0 & 1) != me ? 1 : 0);
+        n0 += it.c1 - it.c0;
 #pragma unroll 1
-        for (int ch = it.c0; ch < it.c1; ++ch) {
+        for (int ch = first; ch < it.c1; ch += IS) {
           if (!mbar_wait_warp2(&x_full[st], &a_full[st], ph, lim, abort_flag)) {
             ok = false;
             break;
@@ -674,22 +681,25 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
           tc_fence_after();
           if (elect_one()) {
             const uint64_t bd = sdesc_sw128(smem_base + st * S::STAGE_BYTES);
-            const uint32_t a = tmem + (uint32_t)(S::NUM_ACC * BN + as * S::A_COLS);
+            const uint32_t a = tmem + (uint32_t)(S::NUM_ACC * S::ACC_COLS + as * S::A_COLS);
 #pragma unroll
             for (int kk = 0; kk < BK / 16; ++kk)
               umma_ts<PAIR>(d, a + 8 * kk, bd + (kk >> 2) * sub + 2 * (kk & 3), idesc,
-                            kk > 0 ? 1u : (uint32_t)(ch > it.c0));
+                            kk > 0 ? 1u : (uint32_t)(ch > first));
             umma_commit_all<PAIR>(&stage_free[st]);
-            if (ch + 1 == it.c1) umma_commit_all<PAIR>(&acc_full[acc]);
           }
           __syncwarp();
-          if (++as == A_SLOTS) as = 0;
-          if (++st == STAGES) {
-            st = 0;
+          as += IS;
+          if (as >= A_SLOTS) as -= A_SLOTS;
+          st += IS;
+          if (st >= STAGES) {
+            st -= STAGES;
             ph ^= 1u;
           }
         }
         if (!ok) break;
+        if (elect_one()) umma_commit_all<PAIR>(&acc_full[acc]);
+        __syncwarp();
         if (++acc == S::NUM_ACC) {
           acc = 0;
           accph ^= 1u;
@@ -711,6 +721,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
   } else if (warp >= WT_EXPAND_WARP && warp < S::EPI_WARP) {
     // ---------------------------------------------------------------- expanders
     const int grp = (warp - WT_EXPAND_WARP) >> 2, q = warp & 3;
+    const int team = grp / S::UNITS, unit = grp % S::UNITS;  // its turn, its 128 columns of the chunk
     const int row = MATS == 2 ? (lane >> 4) * 64 + q * 16 + (lane & 15) : q * 32 + lane;  // of the staged codes
     const uint32_t code_off = S::X_BYTES + row * (BK / 2);
     const uint32_t sw = BK == 256 ? row & 7 : (row >> 1) & 3;  // the TMA's 128- or 64-byte swizzle
@@ -719,7 +730,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
                                (MATS == 2 ? (lane >> 4) * (S::SCALE_BYTES / 2) + (q * 16 + (lane & 15)) * 2 : row * 2);
     constexpr int SCALE_PITCH = MATS == 2 ? 128 : 256;
     const int gl2 = 31 - __clz(p.group);
-    const uint32_t t_lane = tmem + ((uint32_t)(q * 32) << 16) + S::NUM_ACC * BN;
+    const uint32_t t_lane = tmem + ((uint32_t)(q * 32) << 16) + S::NUM_ACC * S::ACC_COLS;
     int st = 0, as = 0, turn = 0;
     uint32_t ph = 0;
     // (before the first such chunk the wait passes at once)
@@ -728,26 +739,24 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
       return mbar_wait_warp(&stage_free[wrap ? st - A_SLOTS + STAGES : st - A_SLOTS], ph ^ (wrap ? 1u : 0u), lim,
                             abort_flag);
     };
-    // The codes of a short chunk are fetched before the wait for its slot; those of a long
-    // one 64 columns at a time (all of them held at once slowed the unpacking).
-    constexpr bool EARLY = BK == 128;
     while (ok && walk.next(it)) {
       const int K = p.cls[it.cls].K, ng = (K + p.group - 1) >> gl2;
 #pragma unroll 1
       for (int ch = it.c0; ch < it.c1; ++ch) {
-        if (turn == grp) {
+        if (turn == team) {
           if (!mbar_wait_warp(&code_full[st], ph, lim, abort_flag)) {
             ok = false;
             break;
           }
           const uint32_t base = smem_base + st * S::STAGE_BYTES;
-          uint4 cw[BK / 32];
-          uint32_t sc[BK / 32];
+          // codes and scales are fetched while the slot is waited for
+          uint4 cw[4];
+          uint32_t sc[4];
           bool few = true;
 #pragma unroll
-          for (int i = 0; i < BK / 32; ++i) {
-            const int gi = (i * 32) >> gl2;
-            if (EARLY) cw[i] = lds128(base + code_off + ((i ^ sw) << 4));
+          for (int i = 0; i < 4; ++i) {
+            const int gi = (unit * 128 + i * 32) >> gl2;
+            cw[i] = lds128(base + code_off + (((4 * unit + i) ^ sw) << 4));
             sc[i] = lds16(base + scale_off + gi * SCALE_PITCH);
             if (ch * (BK >> gl2) + gi >= ng) sc[i] = 0u;  // behind K: x is zero there, the scale not this row's
             few = few && w4_scale_is_short(sc[i]);
@@ -758,29 +767,23 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t t_slot = t_lane + as * S::A_COLS;
-          auto columns64 = [&](const int h, auto pair) {
+          const uint32_t t_slot = t_lane + as * S::A_COLS + unit * 64;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // 64 columns at a time
             uint32_t v[32];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const uint4 c4 = EARLY ? cw[2 * h + i] : lds128(base + code_off + (((2 * h + i) ^ sw) << 4));
-              const uint32_t w[4] = {c4.x, c4.y, c4.z, c4.w};
-              const uint32_t ss = sc[2 * h + i] * 0x10001u, ms = mul_bf16x2(ss, 0xC1C0C1C0u);  // s, -24 s
+              const uint32_t w[4] = {cw[2 * h + i].x, cw[2 * h + i].y, cw[2 * h + i].z, cw[2 * h + i].w};
+              const uint32_t ss = few ? sc[2 * h + i] * 0x10001u : 0x3F803F80u, ms = mul_bf16x2(ss, 0xC1C0C1C0u);
 #pragma unroll
               for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[i * 16 + j * 4 + e] = pair(w[j], e, ss, ms);
+                for (int e = 0; e < 4; ++e) v[i * 16 + j * 4 + e] = w4_pair_scaled(w[j], e, ss, ms);
             }
+            if (!few)  // a scale of another origin: code - 8 (exact) came out above
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[k] = mul_bf16x2(v[k], sc[2 * h + (k >> 4)] * 0x10001u);
             tmem_st_x32(t_slot + h * 32, v);
-          };
-          if (few) {
-#pragma unroll
-            for (int h = 0; h < BK / 64; ++h)
-              columns64(h, [](uint32_t w, int e, uint32_t ss, uint32_t ms) { return w4_pair_scaled(w, e, ss, ms); });
-          } else {  // scales of another origin
-#pragma unroll
-            for (int h = 0; h < BK / 64; ++h)
-              columns64(h, [](uint32_t w, int e, uint32_t ss, uint32_t) { return mul_bf16x2(w4_pair(w >> (4 * e)), ss); });
           }
           tmem_st_wait();
           tc_fence_before();
@@ -794,7 +797,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
               mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&a_full[st]), 0));
           }
         }
-        if (++turn == S::NG) turn = 0;
+        if (++turn == S::TEAMS) turn = 0;
         if (++as == A_SLOTS) as = 0;
         if (++st == STAGES) {
           st = 0;
@@ -812,7 +815,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
     const int q = warp & 3, ew = warp - S::EPI_WARP;
     const int cfirst = 16 * (ew >> 2);
     constexpr int CSTEP = 16 * (EW / 4);
-    int acc = 0;
+    int acc = 0, n0 = 0;
     uint32_t accph = 0;
     while (ok && walk.next(it)) {
       const W4Class& c = p.cls[it.cls];
@@ -877,13 +880,12 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
         return p.partial + ((((size_t)w * 2 + slot) * CTAS + rank) * BN) * 128 + q * 32 + lane;
       };
       float* mine = whole ? nullptr : part_of(walker, it.wa < walker ? 0 : 1);
-      if (!mbar_wait_warp<true>(&acc_full[acc], accph, lim, abort_flag)) {
+      if (!mbar_wait_warp<100>(&acc_full[acc], accph, lim, abort_flag)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
-      uint32_t ra[16], rb[16];
+      const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * S::ACC_COLS);
       auto use = [&](const int c0, const uint32_t (&r)[16]) {
         float v[16];
 #pragma unroll
@@ -906,17 +908,41 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
             mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&acc_free[acc]), 0));
         }
       };
-      // the loads of one 16-column chunk are in flight while the one before is used
-      if (cfirst < rows) tmem_ld_x16(t_row + cfirst, ra); else release();
+      uint32_t ra[16], rb[16];
+      if (S::ISSUERS == 2) {
+        // the sum of the issuers' sums; one of them has none when the piece is one chunk
+        const int chunks = it.c1 - it.c0;
+        const bool both = chunks > 1;
+        const uint32_t t_one = t_row + (!both && (n0 & 1) ? BN : 0);
+        n0 += chunks;
 #pragma unroll 1
-      for (int c0 = cfirst; c0 < rows; c0 += 2 * CSTEP) {
-        tmem_ld_wait_keep(ra);
-        if (c0 + CSTEP < rows) tmem_ld_x16(t_row + c0 + CSTEP, rb); else release();
-        use(c0, ra);
-        if (c0 + CSTEP >= rows) break;
-        tmem_ld_wait_keep(rb);
-        if (c0 + 2 * CSTEP < rows) tmem_ld_x16(t_row + c0 + 2 * CSTEP, ra); else release();
-        use(c0 + CSTEP, rb);
+        for (int c0 = cfirst; c0 < rows; c0 += CSTEP) {
+          tmem_ld_x16(t_one + c0, ra);
+          if (both) {
+            tmem_ld_x16(t_row + BN + c0, rb);
+            tmem_ld_wait_keep(ra, rb);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) ra[j] = __float_as_uint(__uint_as_float(ra[j]) + __uint_as_float(rb[j]));
+          } else {
+            tmem_ld_wait_keep(ra);
+          }
+          if (c0 + CSTEP >= rows) release();
+          use(c0, ra);
+        }
+        if (cfirst >= rows) release();
+      } else {
+        // the loads of one 16-column chunk are in flight while the one before is used
+        if (cfirst < rows) tmem_ld_x16(t_row + cfirst, ra); else release();
+#pragma unroll 1
+        for (int c0 = cfirst; c0 < rows; c0 += 2 * CSTEP) {
+          tmem_ld_wait_keep(ra);
+          if (c0 + CSTEP < rows) tmem_ld_x16(t_row + c0 + CSTEP, rb); else release();
+          use(c0, ra);
+          if (c0 + CSTEP >= rows) break;
+          tmem_ld_wait_keep(rb);
+          if (c0 + 2 * CSTEP < rows) tmem_ld_x16(t_row + c0 + 2 * CSTEP, ra); else release();
+          use(c0 + CSTEP, rb);
+        }
       }
       if (++acc == S::NUM_ACC) {
         acc = 0;
