@@ -170,8 +170,8 @@ __global__ void __launch_bounds__(QW_WARPS * 32)
 // of K, so the result does not depend on who that is, and no one waits.
 //
 // Warps: 0 and 2 TMA producers (codes and scales; input rows), 1 (and 3) matrix issuers
-// (PAIR: in the leader CTA), 1 also owner of the tensor memory, then two teams that expand alternate
-// chunks (four warps for each 128 columns), then the epilogue's. The issuer's instruction stream is what bounded
+// (PAIR: in the leader CTA), 1 also owner of the tensor memory, then teams of four that take
+// turns to expand chunks, then the epilogue's. The issuer's instruction stream is what bounded
 // the first forms of this kernel (a ready barrier costs it 84 cycles, a product 20, a
 // commit 46, and some hundred a turn of a long loop), so it commits once a chunk.
 // Barriers of a stage of the ring: codes (local) -> expanders; input rows (PAIR: of both
@@ -188,9 +188,9 @@ template <int BN>
 struct WtShape {
   static constexpr bool PAIR = BN >= 64;
   static constexpr int BK = PAIR ? 128 : 256;          // columns of K a stage
-  static constexpr int TEAMS = 2, UNITS = BK / 128;    // teams of expanding warps: four for each 128 columns
+  static constexpr int TEAMS = PAIR ? 2 : 3;    // teams of four expanding warps
   static constexpr int EW = PAIR ? 8 : 4;              // epilogue warps
-  static constexpr int EPI_WARP = WT_EXPAND_WARP + 4 * TEAMS * UNITS;
+  static constexpr int EPI_WARP = WT_EXPAND_WARP + 4 * TEAMS;
   static constexpr int THREADS = 32 * (EPI_WARP + EW);
   static constexpr int B_ROWS = PAIR ? BN / 2 : BN;    // input rows a CTA
   static constexpr int HALF = B_ROWS / 2;               // staged rows where half of a CTA's suffice
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(&code_full[i], 1);
       mbar_init(&x_full[i], 1);
-      mbar_init(&a_full[i], 4 * S::UNITS * CTAS);  // a team of each CTA
+      mbar_init(&a_full[i], 4 * CTAS);  // a team of each CTA
       mbar_init(&stage_free[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -720,8 +720,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
     }
   } else if (warp >= WT_EXPAND_WARP && warp < S::EPI_WARP) {
     // ---------------------------------------------------------------- expanders
-    const int grp = (warp - WT_EXPAND_WARP) >> 2, q = warp & 3;
-    const int team = grp / S::UNITS, unit = grp % S::UNITS;  // its turn, its 128 columns of the chunk
+    const int team = (warp - WT_EXPAND_WARP) >> 2, q = warp & 3;
     const int row = MATS == 2 ? (lane >> 4) * 64 + q * 16 + (lane & 15) : q * 32 + lane;  // of the staged codes
     const uint32_t code_off = S::X_BYTES + row * (BK / 2);
     const uint32_t sw = BK == 256 ? row & 7 : (row >> 1) & 3;  // the TMA's 128- or 64-byte swizzle
@@ -749,14 +748,16 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
             break;
           }
           const uint32_t base = smem_base + st * S::STAGE_BYTES;
-          // codes and scales are fetched while the slot is waited for
-          uint4 cw[4];
-          uint32_t sc[4];
+          // the codes of a short chunk are fetched before the wait for its slot, those of a
+          // long one 64 columns at a time (all of them held at once slowed the unpacking)
+          constexpr bool EARLY = BK == 128;
+          uint4 cw[BK / 32];
+          uint32_t sc[BK / 32];
           bool few = true;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int gi = (unit * 128 + i * 32) >> gl2;
-            cw[i] = lds128(base + code_off + (((4 * unit + i) ^ sw) << 4));
+          for (int i = 0; i < BK / 32; ++i) {
+            const int gi = (i * 32) >> gl2;
+            if (EARLY) cw[i] = lds128(base + code_off + ((i ^ sw) << 4));
             sc[i] = lds16(base + scale_off + gi * SCALE_PITCH);
             if (ch * (BK >> gl2) + gi >= ng) sc[i] = 0u;  // behind K: x is zero there, the scale not this row's
             few = few && w4_scale_is_short(sc[i]);
@@ -767,13 +768,14 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t t_slot = t_lane + as * S::A_COLS + unit * 64;
+          const uint32_t t_slot = t_lane + as * S::A_COLS;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {  // 64 columns at a time
+          for (int h = 0; h < BK / 64; ++h) {  // 64 columns at a time
             uint32_t v[32];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const uint32_t w[4] = {cw[2 * h + i].x, cw[2 * h + i].y, cw[2 * h + i].z, cw[2 * h + i].w};
+              const uint4 c4 = EARLY ? cw[2 * h + i] : lds128(base + code_off + (((2 * h + i) ^ sw) << 4));
+              const uint32_t w[4] = {c4.x, c4.y, c4.z, c4.w};
               const uint32_t ss = few ? sc[2 * h + i] * 0x10001u : 0x3F803F80u, ms = mul_bf16x2(ss, 0xC1C0C1C0u);
 #pragma unroll
               for (int j = 0; j < 4; ++j)
