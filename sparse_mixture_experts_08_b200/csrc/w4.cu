@@ -233,7 +233,10 @@ constexpr int WT_ITEMS = 128;  // pieces of a walker that are worked out before 
 struct WtSched {
   int tile_start[WT_MAX_GROUPS + 1];  // groups in walk order: first tile
   int cost[WT_MAX_GROUPS + 1];        // and cost of the cut tiles before
-  int gid[WT_MAX_GROUPS], rows[WT_MAX_GROUPS], brow[WT_MAX_GROUPS];
+  int gid[WT_MAX_GROUPS];
+  int rows[WT_MAX_GROUPS], brow[WT_MAX_GROUPS];  // by group
+  short height[WT_MAX_GROUPS];
+  int hist[32];
   int rounds, t0;   // rounds of whole tiles; first cut tile
   int cut, per;     // cost of the cut tiles, of a walker's share
   int t_first, n;   // this walker's first cut tile, all its pieces
@@ -275,7 +278,7 @@ __device__ __forceinline__ WtItem wt_item(const W4Params& p, const WtSched& s, i
   it.cls = gi < G0 ? 0 : 1;
   it.g = gi - (it.cls ? G0 : 0);
   const W4Class& c = p.cls[it.cls];
-  const int rows = s.rows[gi], NT = (rows + BN - 1) / BN, h = wt_height<BN>(rows);
+  const int rows = s.rows[gi], NT = (rows + BN - 1) / BN, h = s.height[gi];
   const int local = tile - s.tile_start[pos], nt = local % NT, nc = wt_chunks<BN>(c);
   it.mt = local / NT;
   it.rows = min(h, rows - nt * h);
@@ -294,6 +297,129 @@ __device__ __forceinline__ WtItem wt_item(const W4Params& p, const WtSched& s, i
     it.wb = (at + (nc - 1) * w) / s.per;
   }
   return it;
+}
+
+// The schedule, by one warp: groups ordered by tile height, tallest first (a counting
+// sort over the heights, stable in group order), tiles and costs added up in that order.
+template <int BN, int TILE_F>
+__device__ __forceinline__ void wt_schedule(const W4Params& p, WtSched& s, int G, int walker, int walkers, int lane) {
+  constexpr int BK = WtShape<BN>::BK;
+  constexpr int NB = BN / 16 + 1;  // bucket = tile height / 16 (0: a group without rows)
+  static_assert(NB <= 32, "a bucket a lane");
+  const int G0 = p.cls[0].n_groups;
+  // an earlier kernel of the call that flagged a device error leaves tables that are not used
+  const int prior = p.status ? *reinterpret_cast<volatile int*>(p.status) : 0;
+  s.hist[lane] = 0;
+  __syncwarp();
+  for (int g0 = 0; g0 < G; g0 += 32) {
+    const int gi = g0 + lane;
+    int key = -1;
+    if (gi < G) {
+      const int cl = gi < G0 ? 0 : 1, g = gi - (cl ? G0 : 0);
+      const W4Class& c = p.cls[cl];
+      int rows, brow;
+      if (c.seg_off) {
+        const int a = c.seg_off[g], b = c.seg_off[g + 1];
+        rows = b - a;
+        brow = a;
+        if (a < 0 || b < a || b > c.max_row) {
+          set_status(p.status, MOE_ERR_DEVICE_INDEX);
+          rows = brow = 0;
+        }
+      } else {
+        rows = c.const_rows;
+        brow = g * c.b_group_stride;
+      }
+      const int h = wt_height<BN>(rows);
+      key = h >> 4;
+      s.rows[gi] = rows;
+      s.brow[gi] = brow;
+      s.height[gi] = (short)h;
+    }
+    // rank among the groups of this height so far
+    const unsigned same = __match_any_sync(0xffffffffu, key);
+    const int rank = __popc(same & ((1u << lane) - 1u));
+    int before = 0;
+    if (key >= 0) before = s.hist[key];
+    __syncwarp();
+    if (key >= 0 && rank == 0) s.hist[key] = before + __popc(same);
+    if (gi < G) s.cost[gi] = before + rank;
+    __syncwarp();
+  }
+  {  // first position of each height, tallest first
+    const int n = lane < NB ? s.hist[NB - 1 - lane] : 0;
+    int inc = n;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += v;
+    }
+    __syncwarp();
+    if (lane < NB) s.hist[NB - 1 - lane] = inc - n;
+    __syncwarp();
+  }
+  for (int gi = lane; gi < G; gi += 32) s.gid[s.hist[s.height[gi] >> 4] + s.cost[gi]] = gi;
+  __syncwarp();
+  int total = 0;
+  for (int p0 = 0; p0 < G; p0 += 32) {
+    const int pos = p0 + lane;
+    int n = 0;
+    if (pos < G) {
+      const int gi = s.gid[pos];
+      n = ((p.cls[gi < G0 ? 0 : 1].R + TILE_F - 1) / TILE_F) * ((s.rows[gi] + BN - 1) / BN);
+    }
+    int inc = n;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += v;
+    }
+    if (pos < G) s.tile_start[pos] = total + inc - n;
+    total += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  if (lane == 0) s.tile_start[G] = total;
+  __syncwarp();
+  if (__any_sync(0xffffffffu, prior != 0)) total = 0;
+  // whole rounds, and the tiles that are cut
+  const int rounds = total / walkers - (total >= walkers && total % walkers ? 1 : 0), t0 = rounds * walkers;
+  int cut = 0;
+  for (int p0 = 0; p0 < G; p0 += 32) {
+    const int pos = p0 + lane;
+    int c = 0;
+    if (pos < G && total) {
+      const int gi = s.gid[pos], n = s.tile_start[pos + 1] - max(s.tile_start[pos], t0);
+      if (n > 0) c = n * wt_chunks<BN>(p.cls[gi < G0 ? 0 : 1]) * wt_weight(s.height[gi]);
+    }
+    int inc = c;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += v;
+    }
+    if (pos < G) s.cost[pos] = cut + inc - c;
+    cut += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  __syncwarp();
+  // (at least 512 columns of the heaviest tile, so that every walker between a tile's
+  // first and last one has a part of it)
+  const int share = max((cut + walkers - 1) / walkers, 512 / BK * max(BN / 16, 4));
+  const int from = walker * share, to = min(from + share, cut);
+  int tile = 0;
+  if (lane < 2 && from < to) {  // the tiles that hold the first and the last of its cost
+    const int x = lane == 0 ? from : to - 1;
+    const int pos = wt_find(s.cost, G, x), gi = s.gid[pos];
+    const int tc = wt_chunks<BN>(p.cls[gi < G0 ? 0 : 1]) * wt_weight(s.height[gi]);
+    tile = max(s.tile_start[pos], t0) + (x - s.cost[pos]) / tc;
+  }
+  const int last = __shfl_sync(0xffffffffu, tile, 1);
+  if (lane == 0) {
+    s.rounds = rounds;
+    s.t0 = t0;
+    s.cut = cut;
+    s.per = share;
+    s.t_first = tile;
+    s.n = rounds + (from < to ? last - tile + 1 : 0);
+  }
 }
 
 // The list of a walker's pieces of work, walked alike by every role.
@@ -429,144 +555,41 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
     mbar_init(&drain_bar, S::ISSUERS);
     abort_s = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&maps.codes[0][0]);
-    tma_prefetch_desc(&maps.x[0][0]);
   }
+  if (warp == 2 && lane < (int)(sizeof(WtMaps) / sizeof(CUtensorMap)))
+    tma_prefetch_desc(reinterpret_cast<const CUtensorMap*>(&maps) + lane);
   if (warp == 1) {
     tmem_alloc_g<PAIR>(&tmem_base_s, 512);
     tmem_relinquish_g<PAIR>();
   }
   __syncwarp();
-  if (PAIR) cluster_sync_all();  // the peer's barriers are initialised before either CTA signals them
   pdl_launch_dependents();
-  pdl_wait();
-  // the counters of the next launch on this workspace (two sets, used in turn): zero
-  // whatever this launch, or one that was cut short, leaves in its own
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < W4_COUNTERS; i += S::THREADS) p.counters_next[i] = 0u;
-  if (warp == 0) {
-    constexpr int NB = BN / 16 + 1;  // bucket = tile height / 16 (0: a group without rows)
-    const int per = (G + 31) / 32;
-    const int lo = min(G, lane * per), hi = min(G, lo + per);
-    auto group_tiles = [&](const int gi, const int rows) {
-      return ((p.cls[gi < G0 ? 0 : 1].R + TILE_F - 1) / TILE_F) * ((rows + BN - 1) / BN);
-    };
-    int cnt[NB], tl[NB];
-#pragma unroll
-    for (int b = 0; b < NB; ++b) cnt[b] = tl[b] = 0;
-    for (int gi = lo; gi < hi; ++gi) {
-      const int cl = gi < G0 ? 0 : 1, g = gi - (cl ? G0 : 0);
-      const W4Class& c = p.cls[cl];
-      int rows, brow;
-      if (c.seg_off) {
-        const int a = c.seg_off[g], b = c.seg_off[g + 1];
-        rows = b - a;
-        brow = a;
-        if (a < 0 || b < a || b > c.max_row) {
-          set_status(p.status, MOE_ERR_DEVICE_INDEX);
-          rows = brow = 0;
-        }
-      } else {
-        rows = c.const_rows;
-        brow = g * c.b_group_stride;
-      }
-      sched.rows[gi] = rows;
-      sched.brow[gi] = brow;
-      const int key = wt_height<BN>(rows) / 16, tiles = group_tiles(gi, rows);
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-        if (b == key) {
-          ++cnt[b];
-          tl[b] += tiles;
-        }
-    }
-    int base_c = 0, base_t = 0;
-#pragma unroll
-    for (int b = NB - 1; b >= 0; --b) {
-      int ic = cnt[b], itl = tl[b];
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int vc = __shfl_up_sync(0xffffffffu, ic, off), vt = __shfl_up_sync(0xffffffffu, itl, off);
-        if (lane >= off) {
-          ic += vc;
-          itl += vt;
-        }
-      }
-      const int sum_c = __shfl_sync(0xffffffffu, ic, 31), sum_t = __shfl_sync(0xffffffffu, itl, 31);
-      cnt[b] = base_c + ic - cnt[b];
-      tl[b] = base_t + itl - tl[b];
-      base_c += sum_c;
-      base_t += sum_t;
-    }
-    for (int gi = lo; gi < hi; ++gi) {
-      const int rows = sched.rows[gi];
-      const int key = wt_height<BN>(rows) / 16, tiles = group_tiles(gi, rows);
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-        if (b == key) {
-          sched.gid[cnt[b]] = gi;
-          sched.tile_start[cnt[b]] = tl[b];
-          ++cnt[b];
-          tl[b] += tiles;
-        }
-    }
-    // whole rounds and cut tiles; an earlier kernel of the call that flagged a device
-    // error leaves tables that are not used
-    const int prior = p.status ? *reinterpret_cast<volatile int*>(p.status) : 0;
-    const int total = __any_sync(0xffffffffu, prior != 0) ? 0 : base_t;
-    if (lane == 0) sched.tile_start[G] = base_t;
-    __syncwarp();
-    const int rounds = total / walkers - (total >= walkers && total % walkers ? 1 : 0), t0 = rounds * walkers;
-    auto cut_cost = [&](const int pos) {
-      const int gi = sched.gid[pos], n = sched.tile_start[pos + 1] - max(sched.tile_start[pos], t0);
-      return n > 0 && total ? n * wt_chunks<BN>(p.cls[gi < G0 ? 0 : 1]) * wt_weight(wt_height<BN>(sched.rows[gi])) : 0;
-    };
-    int sum = 0;
-    for (int i = lo; i < hi; ++i) sum += cut_cost(i);
-    int inc = sum;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, inc, off);
-      if (lane >= off) inc += v;
-    }
-    int run = inc - sum;
-    for (int i = lo; i < hi; ++i) {
-      sched.cost[i] = run;
-      run += cut_cost(i);
-    }
-    const int cut = __shfl_sync(0xffffffffu, inc, 31);
-    __syncwarp();
-    if (lane == 0) {
-      // (at least 512 columns of the heaviest tile, so that every walker between a tile's
-      // first and last one has a part of it)
-      const int share = max((cut + walkers - 1) / walkers, 512 / BK * max(BN / 16, 4));
-      const int from = walker * share, to = min(from + share, cut);
-      auto tile_at = [&](const int x) {
-        const int pos = wt_find(sched.cost, G, x), gi = sched.gid[pos];
-        const int tc = wt_chunks<BN>(p.cls[gi < G0 ? 0 : 1]) * wt_weight(wt_height<BN>(sched.rows[gi]));
-        return max(sched.tile_start[pos], t0) + (x - sched.cost[pos]) / tc;
-      };
-      int n = 0, first = 0;
-      if (from < to) {
-        first = tile_at(from);
-        n = tile_at(to - 1) - first + 1;
-      }
-      sched.rounds = rounds;
-      sched.t0 = t0;
-      sched.cut = cut;
-      sched.per = share;
-      sched.t_first = first;
-      sched.n = rounds + n;
-    }
-  }
-  __syncthreads();
-  if (threadIdx.x < min(sched.n, WT_ITEMS))
-    sched.items[threadIdx.x] = wt_item<BN>(p, sched, G, walker, walkers, threadIdx.x);
-  __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  if (PAIR)
+    cluster_sync_all();  // the peer's barriers are initialised before either CTA signals them
+  else
+    __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base_s;
+  // Barriers and tensor memory are ready. Warp 0 waits for the kernels before this one and
+  // lays out the schedule, warp 3 zeroes the counters; the expanders run their loop body
+  // once on whatever the shared memory holds, which fetches its instructions meanwhile.
+  if (warp == 0) {
+    pdl_wait();
+    wt_schedule<BN, TILE_F>(p, sched, G, walker, walkers, lane);
+  } else if (warp == 3 && blockIdx.x == 0) {
+    pdl_wait();
+    // the counters of the next launch on this workspace (two sets, used in turn): zero
+    // whatever this launch, or one that was cut short, leaves in its own
+    for (int i = lane; i < W4_COUNTERS; i += 32) p.counters_next[i] = 0u;
+  }
+  auto scheduled = [&]() {  // every warp passes here once before it walks
+    __syncthreads();
+    if (threadIdx.x < min(sched.n, WT_ITEMS))
+      sched.items[threadIdx.x] = wt_item<BN>(p, sched, G, walker, walkers, threadIdx.x);
+    __syncthreads();
+  };
+  if (warp < WT_EXPAND_WARP || warp >= S::EPI_WARP) scheduled();
   const unsigned long long lim = p.wait_limit_ns;
   WtWalk<BN> walk(p, sched, G, walker, walkers);
   WtItem it;
@@ -738,12 +761,15 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
       return mbar_wait_warp(&stage_free[wrap ? st - A_SLOTS + STAGES : st - A_SLOTS], ph ^ (wrap ? 1u : 0u), lim,
                             abort_flag);
     };
-    while (ok && walk.next(it)) {
-      const int K = p.cls[it.cls].K, ng = (K + p.group - 1) >> gl2;
+    bool dry = true;  // the first turn, before there is work
+    it.c0 = 0;
+    it.c1 = 1;
+    int ng = 0;
+    do {
 #pragma unroll 1
       for (int ch = it.c0; ch < it.c1; ++ch) {
-        if (turn == team) {
-          if (!mbar_wait_warp(&code_full[st], ph, lim, abort_flag)) {
+        if (dry || turn == team) {
+          if (!dry && !mbar_wait_warp(&code_full[st], ph, lim, abort_flag)) {
             ok = false;
             break;
           }
@@ -763,7 +789,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
             few = few && w4_scale_is_short(sc[i]);
           }
           few = __all_sync(0xffffffffu, few);
-          if (!slot_free()) {
+          if (!dry && !slot_free()) {
             ok = false;
             break;
           }
@@ -792,13 +818,14 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
           __syncwarp();
           // (relaxed: the stores to tensor memory have completed, and a release at
           // cluster scope would wait for much more)
-          if (lane == 0) {
+          if (lane == 0 && !dry) {
             if (leader)
               mbar_arrive_relaxed(&a_full[st]);
             else
               mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&a_full[st]), 0));
           }
         }
+        if (dry) break;
         if (++turn == S::TEAMS) turn = 0;
         if (++as == A_SLOTS) as = 0;
         if (++st == STAGES) {
@@ -806,7 +833,13 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
           ph ^= 1u;
         }
       }
-    }
+      if (dry) {
+        dry = false;
+        scheduled();
+      }
+      if (!ok || !walk.next(it)) break;
+      ng = (p.cls[it.cls].K + p.group - 1) >> gl2;
+    } while (true);
     if (!ok) {
       set_status(p.status, MOE_ERR_TIMEOUT);
       abort_s = 1;
