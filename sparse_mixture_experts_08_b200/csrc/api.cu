@@ -762,12 +762,18 @@ static moe_status_t layer_forward_impl(const moe_config_t& c, const void* x, con
                                   inv_perm, w_perm, at<void>(ws, L.x_perm), status, s));
   } else {
     MOE_CUDA(launch_route(c, x, w_router, bias, nullptr, logits_out, logits, idx, w, status, s, true));
-    int32_t* start = at<int32_t>(ws, L.start);
-    MOE_CUDA(launch_route_index(1, c.T, c.k, c.m, idx, counts, offsets, lis, start, status, s));
-    MOE_CUDA(launch_rank(c.T, c.k, c.m, idx, offsets, start, w, perm, inv_perm, w_perm, status, s));
-    MOE_TRY(mark_stage(3, s));
-    if (!x_codes)  // (given codes are moved instead, in run_ffn)
-      MOE_CUDA(launch_permute_rows(c.dtype, (int)Tk, c.k, c.d, x, inv_perm, at<void>(ws, L.x_perm), s));
+    if (w4 && small_dispatch_ok(Tk, c.m)) {  // (bf16 rows; stage 3 has no launch of its own)
+      MOE_TRY(mark_stage(3, s));
+      MOE_CUDA(launch_small_dispatch(c.T, c.k, c.m, c.d, idx, w, x, counts, offsets, lis, perm, inv_perm, w_perm,
+                                     at<void>(ws, L.x_perm), status, s));
+    } else {
+      int32_t* start = at<int32_t>(ws, L.start);
+      MOE_CUDA(launch_route_index(1, c.T, c.k, c.m, idx, counts, offsets, lis, start, status, s));
+      MOE_CUDA(launch_rank(c.T, c.k, c.m, idx, offsets, start, w, perm, inv_perm, w_perm, status, s));
+      MOE_TRY(mark_stage(3, s));
+      if (!x_codes)  // (given codes are moved instead, in run_ffn)
+        MOE_CUDA(launch_permute_rows(c.dtype, (int)Tk, c.k, c.d, x, inv_perm, at<void>(ws, L.x_perm), s));
+    }
   }
   MOE_TRY(mark_stage(4, s));
   FfnIo io;

@@ -288,6 +288,12 @@ cudaError_t launch_rank(int T, int k, int m, const int32_t* idx, const int32_t* 
                         cudaStream_t s);
 cudaError_t launch_permute_rows(int dtype, int Tk, int k, int d, const void* x, const int32_t* inv_perm, void* x_perm,
                                 cudaStream_t s);
+// Histogram, offsets, LIS, permutation and bf16 row copy of a small batch in one launch:
+// the tables of route_index, rank and permute_rows.
+bool small_dispatch_ok(long long tasks, int m);
+cudaError_t launch_small_dispatch(int T, int k, int m, int d, const int32_t* idx, const float* task_w, const void* x,
+                                  int32_t* counts, int32_t* offsets, moe_lis_t* lis, int32_t* perm, int32_t* inv_perm,
+                                  float* w_perm, void* x_perm, int* status, cudaStream_t s);
 cudaError_t launch_combine(int dtype, int T, int d, int k, int ksplit, const float* y_perm, long long y_split_stride,
                            const int32_t* inv_perm, int n_shared, const float* y_shared, long long ysh_split_stride,
                            void* out, cudaStream_t s, const int32_t* row_splits = nullptr);

@@ -860,6 +860,154 @@ cudaError_t launch_permute_rows(int dtype, int Tk, int k, int d, const void* x, 
   return cudaGetLastError();
 }
 
+// ------------------------------------------------ the whole dispatch of a small batch
+// route_index, rank and permute_rows in one launch, for batches whose tables are a few
+// hundred entries: what those launches cost there is their latency (three of them 15 us,
+// this one 5, at 16 tokens). Every block builds the tables for itself from the ids and
+// copies its share of the rows; block 0 writes the tables. The order is the stable
+// counting sort's: task q goes to offsets[e] + the number of earlier tasks of expert e.
+// Any id outside [0, m) sets MOE_ERR_DEVICE_INDEX and nothing else is written.
+constexpr int SD_THREADS = 256, SD_MAX_TASKS = 512;
+__global__ void __launch_bounds__(SD_THREADS)
+    small_dispatch_kernel(int T, int k, int m, int chunks, int parts, const int32_t* __restrict__ idx,
+                          const float* __restrict__ task_w, const uint4* __restrict__ x, int32_t* __restrict__ counts,
+                          int32_t* __restrict__ offsets, moe_lis_t* __restrict__ lis, int32_t* __restrict__ perm,
+                          int32_t* __restrict__ inv_perm, float* __restrict__ w_perm, uint4* __restrict__ x_perm,
+                          int* status) {
+  __shared__ int cnt[1024], off[1024], pos_s[SD_MAX_TASKS], e_s[SD_MAX_TASKS];
+  __shared__ int bad, wsum[8], wmax[8], warg[8];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, Tk = T * k;
+  for (int e = tid; e < m; e += SD_THREADS) cnt[e] = 0;
+  if (tid == 0) bad = 0;
+  pdl_launch_dependents();
+  pdl_wait();
+  for (int q = tid; q < Tk; q += SD_THREADS) e_s[q] = idx[q];
+  __syncthreads();
+  if (warp == 0) {  // rank of each task within its expert, 32 tasks at a time
+    for (int q0 = 0; q0 < Tk; q0 += 32) {
+      const int q = q0 + lane;
+      int e = q < Tk ? e_s[q] : -1;
+      if (q < Tk && (e < 0 || e >= m)) {
+        bad = 1;
+        e = -1;
+      }
+      const unsigned same = __match_any_sync(FULL, e);
+      const int rank = __popc(same & ((1u << lane) - 1u)), before = e >= 0 ? cnt[e] : 0;
+      __syncwarp();
+      if (e >= 0 && rank == 0) cnt[e] = before + __popc(same);
+      if (q < Tk) pos_s[q] = before + rank;
+      __syncwarp();
+    }
+  }
+  __syncthreads();
+  if (bad) {
+    if (tid == 0) set_status(status, MOE_ERR_DEVICE_INDEX);
+    return;
+  }
+  // offsets: four experts a thread, scanned over the block; the largest count, lowest expert first
+  int n[4], sum = 0, mv = -1, ma = 0x7fffffff;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = 4 * tid + i;
+    n[i] = e < m ? cnt[e] : 0;
+    sum += n[i];
+    if (e < m && n[i] > mv) {
+      mv = n[i];
+      ma = e;
+    }
+  }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(FULL, incl, o);
+    if (lane >= o) incl += v;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const int ov = __shfl_xor_sync(FULL, mv, o), oa = __shfl_xor_sync(FULL, ma, o);
+    if (ov > mv || (ov == mv && oa < ma)) {
+      mv = ov;
+      ma = oa;
+    }
+  }
+  if (lane == 31) wsum[warp] = incl;
+  if (lane == 0) {
+    wmax[warp] = mv;
+    warg[warp] = ma;
+  }
+  __syncthreads();
+  int ex = incl - sum;
+  for (int w = 0; w < warp; ++w) ex += wsum[w];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = 4 * tid + i;
+    if (e < m) {
+      off[e] = ex;
+      if (blockIdx.x == 0) {
+        counts[e] = n[i];
+        offsets[e] = ex;
+        if (e == m - 1) offsets[m] = ex + n[i];
+      }
+    }
+    ex += n[i];
+  }
+  __syncthreads();
+  for (int q = tid; q < Tk; q += SD_THREADS) {
+    const int pos = off[e_s[q]] + pos_s[q];
+    pos_s[q] = pos;
+    if (blockIdx.x == 0) {
+      inv_perm[q] = pos;
+      perm[pos] = q;
+      w_perm[pos] = task_w[q];
+    }
+  }
+  if (blockIdx.x == 0 && tid == 0) {
+    for (int w = 1; w < 8; ++w)
+      if (wmax[w] > wmax[0]) {  // (later warps hold higher experts)
+        wmax[0] = wmax[w];
+        warg[0] = warg[w];
+      }
+    lis->max_count = wmax[0];
+    lis->argmax_expert = warg[0];
+    lis->lis = (double)((long long)m * wmax[0]) / (double)((long long)T * k);
+  }
+  __syncthreads();
+  // rows: a warp per (token, part of its row), as in permute_rows
+  const int cpp = (chunks + parts - 1) / parts;
+  for (int un = blockIdx.x * (SD_THREADS / 32) + warp; un < T * parts; un += gridDim.x * (SD_THREADS / 32)) {
+    const int t = un / parts, c_lo = un % parts * cpp, c_hi = min(chunks, c_lo + cpp);
+    const uint4* src = x + (long long)t * chunks;
+    for (int c0 = c_lo + lane; c0 < c_hi; c0 += 32 * PR_BATCH) {
+      uint4 v[PR_BATCH];
+#pragma unroll
+      for (int u = 0; u < PR_BATCH; ++u)
+        if (c0 + 32 * u < c_hi) v[u] = src[c0 + 32 * u];
+      for (int sl = 0; sl < k; ++sl) {
+        uint4* o = x_perm + (long long)pos_s[t * k + sl] * chunks;
+#pragma unroll
+        for (int u = 0; u < PR_BATCH; ++u)
+          if (c0 + 32 * u < c_hi) o[c0 + 32 * u] = v[u];
+      }
+    }
+  }
+}
+
+bool small_dispatch_ok(long long tasks, int m) { return tasks <= SD_MAX_TASKS && m <= 1024; }
+
+cudaError_t launch_small_dispatch(int T, int k, int m, int d, const int32_t* idx, const float* task_w, const void* x,
+                                  int32_t* counts, int32_t* offsets, moe_lis_t* lis, int32_t* perm, int32_t* inv_perm,
+                                  float* w_perm, void* x_perm, int* status, cudaStream_t s) {
+  const int chunks = d / 8;
+  // parts of a row: until there is a warp for each SM, keeping a chunk per lane
+  int parts = 1;
+  while ((long long)T * parts < num_sms() && chunks / (2 * parts) >= 32) parts *= 2;
+  const int blocks = std::min(num_sms(), (T * parts + SD_THREADS / 32 - 1) / (SD_THREADS / 32));
+  launch_k(small_dispatch_kernel, blocks, SD_THREADS, 0, s, T, k, m, chunks, parts, idx, task_w, (const uint4*)x,
+           counts, offsets, lis, perm, inv_perm, w_perm, (uint4*)x_perm, status);
+  count_launch();
+  return cudaGetLastError();
+}
+
 // ------------------------------------------------ offsets, LIS and the permutation from tile ranks
 // The router's epilogue left, per 128-token tile, the tasks of each expert
 // (tile_cnt[tile][e]) and each task's rank among its tile's tasks of that expert
