@@ -116,9 +116,9 @@ static Layout make_layout(const moe_config_t& c, const Plan& p) {
   };
   const size_t Tk = (size_t)c.T * c.k;
   const size_t T = (size_t)c.T;
-  // the status word, then (offset 256, in every layer's workspace alike) the counters of
-  // the 4-bit products: two sets that the two products of a call use in turn
-  L.status = take(256 + 2 * W4_COUNTERS * sizeof(unsigned));
+  // the status word, then (in every layer's workspace alike) the grid count (offset 128)
+  // and the counters (offset 256) of the 4-bit products
+  L.status = take(256 + W4_COUNTER_WORDS * sizeof(unsigned));
   L.logits = take(T * c.m * 4);
   L.idx = take(Tk * 4);
   L.w = take(Tk * 4);
@@ -310,8 +310,8 @@ static void fill_common(GemmParams& p, int* status) {
   p.wait_limit_ns = g_wait_limit_ns;
 }
 
-// The two products with 4-bit expert weights (routed and shared classes in one launch
-// each); the down projection is not split over K.
+// The two products with 4-bit expert weights, routed and shared classes together: one
+// launch for both where the segments are short, else one each.
 static int w4_bn(const moe_config_t& c) { return w4_pick_bn(c.T, (double)c.T * c.k / c.m); }
 
 static moe_status_t run_ffn_w4(const moe_config_t& c, const FfnIo& io, int* status, cudaStream_t s,
@@ -325,13 +325,15 @@ static moe_status_t run_ffn_w4(const moe_config_t& c, const FfnIo& io, int* stat
   p.status = status;
   p.wait_limit_ns = g_wait_limit_ns;
   p.partial = io.w4_partial;
+  p.grid_count = reinterpret_cast<unsigned long long*>(status + 32);
+  unsigned* const counters = reinterpret_cast<unsigned*>(status + 64);
   const int bn = w4_bn(c);
+  const bool both = w4_both_products(bn);
   for (int down = 0; down < 2; ++down) {
-    p.counters = reinterpret_cast<unsigned*>(status) + 64 + down * W4_COUNTERS;
-    p.counters_next = reinterpret_cast<unsigned*>(status) + 64 + (1 - down) * W4_COUNTERS;
+    W4Class* const cls = p.cls + (both && down ? 2 : 0);
     int n = 0;
     if (io.n_routed > 0) {
-      W4Class& g = p.cls[n++];
+      W4Class& g = cls[n++];
       g.n_groups = io.n_routed;
       g.R = down ? c.d : c.f;
       g.K = down ? c.f : c.d;
@@ -347,7 +349,7 @@ static moe_status_t run_ffn_w4(const moe_config_t& c, const FfnIo& io, int* stat
       g.perm = io.perm;
     }
     if (io.n_shared > 0) {
-      W4Class& g = p.cls[n++];
+      W4Class& g = cls[n++];
       std::memset(&g, 0, sizeof(g));
       g.n_groups = io.n_shared;
       g.R = down ? c.d : c.f_shared;
@@ -362,9 +364,19 @@ static moe_status_t run_ffn_w4(const moe_config_t& c, const FfnIo& io, int* stat
       g.a1 = W4Matrix{w.sh_up, (const bf*)w.sh_up_scale};
     }
     p.n_classes = n;
-    const int epi = down ? EPI_DOWN : swiglu ? EPI_SWIGLU : EPI_RELU;
-    MOE_CUDA(launch_w4_gemm(epi, bn, p, s));
-    if (!down && stage_marks) MOE_TRY(mark_stage(5, s));
+    const int epi = down && !both ? EPI_DOWN : swiglu ? EPI_SWIGLU : EPI_RELU;
+    if (both) {  // one launch (its stages coincide)
+      if (down) {
+        p.counters = counters + 2 * W4_COUNTERS;
+        MOE_CUDA(launch_w4_gemm(epi, bn, p, s));
+        if (stage_marks) MOE_TRY(mark_stage(5, s));
+      }
+    } else {
+      p.counters = counters + down * W4_COUNTERS;
+      p.counters_next = counters + (1 - down) * W4_COUNTERS;
+      MOE_CUDA(launch_w4_gemm(epi, bn, p, s));
+      if (!down && stage_marks) MOE_TRY(mark_stage(5, s));
+    }
   }
   return MOE_OK;
 }

@@ -180,13 +180,14 @@ __global__ void __launch_bounds__(QW_WARPS * 32)
 // that chunk's stage barrier tells (no more than STAGES chunks earlier: the barrier cannot
 // be a phase further yet). Every wait is bounded in time as in tc_gemm.cu.
 constexpr int WT_EXPAND_WARP = 4;
-constexpr int WT_SMEM_BUDGET = 196 * 1024;
 constexpr int WT_MAX_GROUPS = 1040;
 constexpr unsigned long long WT_DRAIN_LIMIT_NS = 200ull * 1000 * 1000;
 
 template <int BN>
 struct WtShape {
   static constexpr bool PAIR = BN >= 64;
+  static constexpr int PHASES = PAIR ? 1 : 2;          // both products in one launch (short segments)
+  static constexpr int SMEM_BUDGET = (PHASES == 2 ? 180 : 196) * 1024;
   static constexpr int BK = PAIR ? 128 : 256;          // columns of K a stage
   static constexpr int TEAMS = PAIR ? 2 : 3;    // teams of four expanding warps
   static constexpr int EW = PAIR ? 8 : 4;              // epilogue warps
@@ -199,7 +200,7 @@ struct WtShape {
   static constexpr int CODE_BYTES = 128 * BK / 2;
   static constexpr int SCALE_BYTES = 128 * 2 * BK / 32;  // at most, groups of 32
   static constexpr int STAGE_BYTES = X_BYTES + CODE_BYTES + SCALE_BYTES;
-  static constexpr int STAGES_RAW = WT_SMEM_BUDGET / STAGE_BYTES;
+  static constexpr int STAGES_RAW = SMEM_BUDGET / STAGE_BYTES;
   static constexpr int STAGES = STAGES_RAW > 12 ? 12 : STAGES_RAW;
   // Issuers: short segments have two (in warps 1 and 3) that take alternate chunks, each
   // with a sum of its own, since one's instruction stream would set the pace.
@@ -215,31 +216,37 @@ struct WtShape {
   static_assert(STAGE_BYTES % 1024 == 0 && A_SLOTS >= 2 && STAGES >= A_SLOTS, "ring");
 };
 
+template <int PHASES>
 struct WtMaps {
-  CUtensorMap codes[2][2], scales[2][2];  // [class][matrix]
-  CUtensorMap x[2][2];  // [class][half]: 64 columns x B_ROWS (HALF) rows x BK / 64
-  CUtensorMap xt[2];    // 64 columns x HALF rows, columns behind K as zero
+  CUtensorMap codes[2 * PHASES][2], scales[2 * PHASES][2];  // [phase, class][matrix]
+  CUtensorMap x[2 * PHASES][2];  // [class][half]: 64 columns x B_ROWS (HALF) rows x BK / 64
+  CUtensorMap xt[2 * PHASES];    // 64 columns x HALF rows, columns behind K as zero
 };
 
-// A piece of work: chunks [c0, c1) of K of one tile.
+// A piece of work: chunks [c0, c1) of K of one tile. cls: 2 phase + class.
 struct alignas(16) WtItem {
   int cls, g, mt, rows, b_row, out_row, c0, c1;
   int wa, wb;  // walkers that share the tile
   int pad[2];
 };
 
-constexpr int WT_ITEMS = 128;  // pieces of a walker that are worked out before it starts
+constexpr int WT_ITEMS = 96;  // pieces of a walker that are worked out before it starts
 
-struct WtSched {
+struct WtPhase {
   int tile_start[WT_MAX_GROUPS + 1];  // groups in walk order: first tile
   int cost[WT_MAX_GROUPS + 1];        // and cost of the cut tiles before
-  int gid[WT_MAX_GROUPS];
-  int rows[WT_MAX_GROUPS], brow[WT_MAX_GROUPS];  // by group
-  short height[WT_MAX_GROUPS];
-  int hist[32];
   int rounds, t0;   // rounds of whole tiles; first cut tile
   int cut, per;     // cost of the cut tiles, of a walker's share
   int t_first, n;   // this walker's first cut tile, all its pieces
+};
+
+template <int PHASES>
+struct WtSched {
+  WtPhase ph[PHASES];
+  int gid[WT_MAX_GROUPS];
+  int rows[WT_MAX_GROUPS], brow[WT_MAX_GROUPS];  // by group; first row in its segment order
+  short height[WT_MAX_GROUPS];
+  int hist[32];
   WtItem items[WT_ITEMS];
 };
 
@@ -267,42 +274,55 @@ __device__ __forceinline__ int wt_find(const int* e, int n, int v) {
   return lo;
 }
 
-// Piece i of a walker (i < s.n); a cut tile may leave it an empty one.
+// Output features of a tile in a phase: of SwiGLU's first product half a tile's rows.
+template <int BN, int EPI>
+__device__ __forceinline__ int wt_cta_f(int phase) {
+  return EPI == EPI_SWIGLU && phase == 0 ? 64 : 128;
+}
+
+// Piece i of a walker, over all phases; a cut tile may leave it an empty one.
 template <int BN>
-__device__ __forceinline__ WtItem wt_item(const W4Params& p, const WtSched& s, int G, int walker, int walkers, int i) {
+__device__ __forceinline__ WtItem wt_item(const W4Params& p, const WtSched<WtShape<BN>::PHASES>& s, int G, int walker,
+                                          int walkers, int i) {
   WtItem it;
-  const bool whole = i < s.rounds;
-  const int tile = whole ? i * walkers + ((i & 1) ? walkers - 1 - walker : walker) : s.t_first + i - s.rounds;
-  const int pos = wt_find(s.tile_start, G, tile);
-  const int gi = s.gid[pos], G0 = p.cls[0].n_groups;
-  it.cls = gi < G0 ? 0 : 1;
-  it.g = gi - (it.cls ? G0 : 0);
+  int phase = 0;
+  if (WtShape<BN>::PHASES == 2 && i >= s.ph[0].n) {
+    phase = 1;
+    i -= s.ph[0].n;
+  }
+  const WtPhase& f = s.ph[phase];
+  const bool whole = i < f.rounds;
+  const int tile = whole ? i * walkers + ((i & 1) ? walkers - 1 - walker : walker) : f.t_first + i - f.rounds;
+  const int pos = wt_find(f.tile_start, G, tile);
+  const int gi = s.gid[pos], G0 = p.cls[0].n_groups, cl = gi < G0 ? 0 : 1;
+  it.cls = 2 * phase + cl;
+  it.g = gi - (cl ? G0 : 0);
   const W4Class& c = p.cls[it.cls];
   const int rows = s.rows[gi], NT = (rows + BN - 1) / BN, h = s.height[gi];
-  const int local = tile - s.tile_start[pos], nt = local % NT, nc = wt_chunks<BN>(c);
+  const int local = tile - f.tile_start[pos], nt = local % NT, nc = wt_chunks<BN>(c);
   it.mt = local / NT;
   it.rows = min(h, rows - nt * h);
-  it.b_row = s.brow[gi] + nt * h;
+  it.b_row = (c.seg_off ? s.brow[gi] : it.g * c.b_group_stride) + nt * h;
   it.out_row = (c.seg_off ? s.brow[gi] : it.g * c.out_group_stride) + nt * h;
   it.c0 = 0;
   it.c1 = nc;
   it.wa = it.wb = walker;
   if (!whole) {
     // chunk j of the tile costs w and starts at `at` + j w: it is walker (that / per)'s
-    const int w = wt_weight(h), at = s.cost[pos] + (tile - max(s.tile_start[pos], s.t0)) * nc * w;
-    const int lo = walker * s.per, hi = min(lo + s.per, s.cut);
+    const int w = wt_weight(h), at = f.cost[pos] + (tile - max(f.tile_start[pos], f.t0)) * nc * w;
+    const int lo = walker * f.per, hi = min(lo + f.per, f.cut);
     it.c0 = lo > at ? (lo - at + w - 1) / w : 0;
     it.c1 = min(nc, (hi - at + w - 1) / w);
-    it.wa = at / s.per;
-    it.wb = (at + (nc - 1) * w) / s.per;
+    it.wa = at / f.per;
+    it.wb = (at + (nc - 1) * w) / f.per;
   }
   return it;
 }
 
 // The schedule, by one warp: groups ordered by tile height, tallest first (a counting
 // sort over the heights, stable in group order), tiles and costs added up in that order.
-template <int BN, int TILE_F>
-__device__ __forceinline__ void wt_schedule(const W4Params& p, WtSched& s, int G, int walker, int walkers, int lane) {
+template <int BN, int EPI>
+__device__ __forceinline__ void wt_schedule(const W4Params& p, WtSched<WtShape<BN>::PHASES>& s, int G, int walker, int walkers, int lane) {
   constexpr int BK = WtShape<BN>::BK;
   constexpr int NB = BN / 16 + 1;  // bucket = tile height / 16 (0: a group without rows)
   static_assert(NB <= 32, "a bucket a lane");
@@ -328,7 +348,7 @@ __device__ __forceinline__ void wt_schedule(const W4Params& p, WtSched& s, int G
         }
       } else {
         rows = c.const_rows;
-        brow = g * c.b_group_stride;
+        brow = 0;
       }
       const int h = wt_height<BN>(rows);
       key = h >> 4;
@@ -343,7 +363,7 @@ __device__ __forceinline__ void wt_schedule(const W4Params& p, WtSched& s, int G
     if (key >= 0) before = s.hist[key];
     __syncwarp();
     if (key >= 0 && rank == 0) s.hist[key] = before + __popc(same);
-    if (gi < G) s.cost[gi] = before + rank;
+    if (gi < G) s.ph[0].cost[gi] = before + rank;
     __syncwarp();
   }
   {  // first position of each height, tallest first
@@ -358,67 +378,72 @@ __device__ __forceinline__ void wt_schedule(const W4Params& p, WtSched& s, int G
     if (lane < NB) s.hist[NB - 1 - lane] = inc - n;
     __syncwarp();
   }
-  for (int gi = lane; gi < G; gi += 32) s.gid[s.hist[s.height[gi] >> 4] + s.cost[gi]] = gi;
+  for (int gi = lane; gi < G; gi += 32) s.gid[s.hist[s.height[gi] >> 4] + s.ph[0].cost[gi]] = gi;
   __syncwarp();
-  int total = 0;
-  for (int p0 = 0; p0 < G; p0 += 32) {
-    const int pos = p0 + lane;
-    int n = 0;
-    if (pos < G) {
-      const int gi = s.gid[pos];
-      n = ((p.cls[gi < G0 ? 0 : 1].R + TILE_F - 1) / TILE_F) * ((s.rows[gi] + BN - 1) / BN);
-    }
-    int inc = n;
+#pragma unroll 1
+  for (int phase = 0; phase < WtShape<BN>::PHASES; ++phase) {
+    WtPhase& f = s.ph[phase];
+    const int tile_f = wt_cta_f<BN, EPI>(phase) * (WtShape<BN>::PAIR ? 2 : 1);
+    int total = 0;
+    for (int p0 = 0; p0 < G; p0 += 32) {
+      const int pos = p0 + lane;
+      int n = 0;
+      if (pos < G) {
+        const int gi = s.gid[pos];
+        n = ((p.cls[2 * phase + (gi < G0 ? 0 : 1)].R + tile_f - 1) / tile_f) * ((s.rows[gi] + BN - 1) / BN);
+      }
+      int inc = n;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, inc, off);
-      if (lane >= off) inc += v;
+      for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += v;
+      }
+      if (pos < G) f.tile_start[pos] = total + inc - n;
+      total += __shfl_sync(0xffffffffu, inc, 31);
     }
-    if (pos < G) s.tile_start[pos] = total + inc - n;
-    total += __shfl_sync(0xffffffffu, inc, 31);
-  }
-  if (lane == 0) s.tile_start[G] = total;
-  __syncwarp();
-  if (__any_sync(0xffffffffu, prior != 0)) total = 0;
-  // whole rounds, and the tiles that are cut
-  const int rounds = total / walkers - (total >= walkers && total % walkers ? 1 : 0), t0 = rounds * walkers;
-  int cut = 0;
-  for (int p0 = 0; p0 < G; p0 += 32) {
-    const int pos = p0 + lane;
-    int c = 0;
-    if (pos < G && total) {
-      const int gi = s.gid[pos], n = s.tile_start[pos + 1] - max(s.tile_start[pos], t0);
-      if (n > 0) c = n * wt_chunks<BN>(p.cls[gi < G0 ? 0 : 1]) * wt_weight(s.height[gi]);
-    }
-    int inc = c;
+    if (lane == 0) f.tile_start[G] = total;
+    __syncwarp();
+    if (__any_sync(0xffffffffu, prior != 0)) total = 0;
+    // whole rounds, and the tiles that are cut
+    const int rounds = total / walkers - (total >= walkers && total % walkers ? 1 : 0), t0 = rounds * walkers;
+    int cut = 0;
+    for (int p0 = 0; p0 < G; p0 += 32) {
+      const int pos = p0 + lane;
+      int c = 0;
+      if (pos < G && total) {
+        const int gi = s.gid[pos], n = f.tile_start[pos + 1] - max(f.tile_start[pos], t0);
+        if (n > 0) c = n * wt_chunks<BN>(p.cls[2 * phase + (gi < G0 ? 0 : 1)]) * wt_weight(s.height[gi]);
+      }
+      int inc = c;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, inc, off);
-      if (lane >= off) inc += v;
+      for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += v;
+      }
+      if (pos < G) f.cost[pos] = cut + inc - c;
+      cut += __shfl_sync(0xffffffffu, inc, 31);
     }
-    if (pos < G) s.cost[pos] = cut + inc - c;
-    cut += __shfl_sync(0xffffffffu, inc, 31);
-  }
-  __syncwarp();
-  // (at least 512 columns of the heaviest tile, so that every walker between a tile's
-  // first and last one has a part of it)
-  const int share = max((cut + walkers - 1) / walkers, 512 / BK * max(BN / 16, 4));
-  const int from = walker * share, to = min(from + share, cut);
-  int tile = 0;
-  if (lane < 2 && from < to) {  // the tiles that hold the first and the last of its cost
-    const int x = lane == 0 ? from : to - 1;
-    const int pos = wt_find(s.cost, G, x), gi = s.gid[pos];
-    const int tc = wt_chunks<BN>(p.cls[gi < G0 ? 0 : 1]) * wt_weight(s.height[gi]);
-    tile = max(s.tile_start[pos], t0) + (x - s.cost[pos]) / tc;
-  }
-  const int last = __shfl_sync(0xffffffffu, tile, 1);
-  if (lane == 0) {
-    s.rounds = rounds;
-    s.t0 = t0;
-    s.cut = cut;
-    s.per = share;
-    s.t_first = tile;
-    s.n = rounds + (from < to ? last - tile + 1 : 0);
+    __syncwarp();
+    // (at least 512 columns of the heaviest tile, so that every walker between a tile's
+    // first and last one has a part of it)
+    const int share = max((cut + walkers - 1) / walkers, 512 / BK * max(BN / 16, 4));
+    const int from = walker * share, to = min(from + share, cut);
+    int tile = 0;
+    if (lane < 2 && from < to) {  // the tiles that hold the first and the last of its cost
+      const int x = lane == 0 ? from : to - 1;
+      const int pos = wt_find(f.cost, G, x), gi = s.gid[pos];
+      const int tc = wt_chunks<BN>(p.cls[2 * phase + (gi < G0 ? 0 : 1)]) * wt_weight(s.height[gi]);
+      tile = max(f.tile_start[pos], t0) + (x - f.cost[pos]) / tc;
+    }
+    const int last = __shfl_sync(0xffffffffu, tile, 1);
+    if (lane == 0) {
+      f.rounds = rounds;
+      f.t0 = t0;
+      f.cut = cut;
+      f.per = share;
+      f.t_first = tile;
+      f.n = rounds + (from < to ? last - tile + 1 : 0);
+    }
   }
 }
 
@@ -426,14 +451,15 @@ __device__ __forceinline__ void wt_schedule(const W4Params& p, WtSched& s, int G
 template <int BN>
 struct WtWalk {
   const W4Params& p;
-  const WtSched& s;
-  int G, walker, walkers, i;
+  const WtSched<WtShape<BN>::PHASES>& s;
+  int G, walker, walkers, i, n;
 
-  __device__ __forceinline__ WtWalk(const W4Params& p_, const WtSched& s_, int G_, int w, int ws)
-      : p(p_), s(s_), G(G_), walker(w), walkers(ws), i(0) {}
+  __device__ __forceinline__ WtWalk(const W4Params& p_, const WtSched<WtShape<BN>::PHASES>& s_, int G_, int w, int ws)
+      : p(p_), s(s_), G(G_), walker(w), walkers(ws), i(0), n(-1) {}
 
   __device__ __forceinline__ bool next(WtItem& it) {
-    while (i < s.n) {
+    if (n < 0) n = s.ph[0].n + (WtShape<BN>::PHASES == 2 ? s.ph[WtShape<BN>::PHASES - 1].n : 0);
+    while (i < n) {
       it = i < WT_ITEMS ? s.items[i] : wt_item<BN>(p, s, G, walker, walkers, i);
       ++i;
       if (it.c0 < it.c1) return true;
@@ -441,6 +467,27 @@ struct WtWalk {
     return false;
   }
 };
+
+// Waits (bounded) until the grid's count has reached `target`, then orders what the counted
+// warps stored before the copies that this warp issues next.
+__device__ __forceinline__ bool w4_grid_wait(unsigned long long* count, unsigned long long target,
+                                             unsigned long long limit_ns, const volatile int* abort_flag) {
+  const uint64_t t0 = globaltimer_ns();
+  bool ok = true;
+  while (true) {
+    unsigned long long v;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(count) : "memory");
+    if (__all_sync(0xffffffffu, v >= target)) break;
+    if (__any_sync(0xffffffffu, *abort_flag != 0 || globaltimer_ns() - t0 > limit_ns)) {
+      ok = false;
+      break;
+    }
+  }
+  __threadfence();
+  asm volatile("fence.proxy.async.global;" ::: "memory");
+  __syncwarp();
+  return ok;
+}
 
 // D (+)= A . B^T, A in tensor memory (PAIR: over both CTAs).
 template <bool PAIR>
@@ -513,20 +560,18 @@ __device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint32_t bar
 
 template <int BN, int EPI>
 __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
-    w4_gemm_kernel(const __grid_constant__ WtMaps maps, const __grid_constant__ W4Params p) {
+    w4_gemm_kernel(const __grid_constant__ WtMaps<WtShape<BN>::PHASES> maps, const __grid_constant__ W4Params p) {
   using S = WtShape<BN>;
-  constexpr int MATS = EPI == EPI_SWIGLU ? 2 : 1;
-  constexpr bool PAIR = S::PAIR;
+  constexpr bool PAIR = S::PAIR, TWO = S::PHASES == 2;
   constexpr int CTAS = PAIR ? 2 : 1;
   constexpr int STAGES = S::STAGES, A_SLOTS = S::A_SLOTS, BK = S::BK, EW = S::EW;
-  constexpr int CTA_F = MATS == 2 ? 64 : 128;  // output features of a CTA's rows
-  constexpr int TILE_F = CTAS * CTA_F;
-  __shared__ WtSched sched;
+  __shared__ WtSched<S::PHASES> sched;
   __shared__ __align__(8) uint64_t code_full[STAGES], x_full[STAGES], a_full[STAGES], stage_free[STAGES],
       acc_full[2], acc_free[2], drain_bar;
   __shared__ __align__(16) __nv_bfloat16 stg[EPI == EPI_DOWN ? 1 : EW][16][32];  // epilogue warp: 16 output rows
   __shared__ uint32_t tmem_base_s;
   __shared__ int abort_s;
+  __shared__ unsigned long long launch_s;  // TWO: the launch's number on this workspace
   extern __shared__ uint8_t dyn_smem[];
 
   // (the shuffle tells the compiler that the role is the whole warp's: loop state and
@@ -556,7 +601,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
     abort_s = 0;
     fence_mbar_init();
   }
-  if (warp == 2 && lane < (int)(sizeof(WtMaps) / sizeof(CUtensorMap)))
+  if (warp == 2 && lane < (int)(sizeof(maps) / sizeof(CUtensorMap)))
     tma_prefetch_desc(reinterpret_cast<const CUtensorMap*>(&maps) + lane);
   if (warp == 1) {
     tmem_alloc_g<PAIR>(&tmem_base_s, 512);
@@ -572,20 +617,35 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_base_s;
   // Barriers and tensor memory are ready. Warp 0 waits for the kernels before this one and
-  // lays out the schedule, warp 3 zeroes the counters; the expanders run their loop body
+  // lays out the schedule, warp 3 sees to the counters; the expanders run their loop body
   // once on whatever the shared memory holds, which fetches its instructions meanwhile.
   if (warp == 0) {
     pdl_wait();
-    wt_schedule<BN, TILE_F>(p, sched, G, walker, walkers, lane);
-  } else if (warp == 3 && blockIdx.x == 0) {
+    wt_schedule<BN, EPI>(p, sched, G, walker, walkers, lane);
+  } else if (warp == 3) {
+    // TWO: the second product's input rows are the first one's output, so they wait for a
+    // grid-wide count of the epilogue warps that have left the first product (all CTAs are
+    // resident: a cooperative launch). The count only grows, by the same number a launch
+    // whatever happens in it, so launches are numbered by it. (The weights do not wait: the
+    // ring holds the second product's first chunks before the last CTA leaves the first.)
+    // The counters of cut tiles: this launch zeroes the set that the next one uses,
+    // whatever it, or one that was cut short, leaves in its own.
     pdl_wait();
-    // the counters of the next launch on this workspace (two sets, used in turn): zero
-    // whatever this launch, or one that was cut short, leaves in its own
-    for (int i = lane; i < W4_COUNTERS; i += 32) p.counters_next[i] = 0u;
+    if (TWO) {
+      unsigned long long v;
+      asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p.grid_count) : "memory");
+      const unsigned long long number = v / (gridDim.x * EW);
+      if (lane == 0) launch_s = number;
+      if (blockIdx.x == 0)
+        for (int i = lane; i < 2 * W4_COUNTERS2; i += 32)
+          p.counters[(number & 1 ? 0 : 2 * W4_COUNTERS2) + i] = 0u;
+    } else if (blockIdx.x == 0) {
+      for (int i = lane; i < W4_COUNTERS; i += 32) p.counters_next[i] = 0u;
+    }
   }
   auto scheduled = [&]() {  // every warp passes here once before it walks
     __syncthreads();
-    if (threadIdx.x < min(sched.n, WT_ITEMS))
+    if (threadIdx.x < min(sched.ph[0].n + (TWO ? sched.ph[S::PHASES - 1].n : 0), WT_ITEMS))
       sched.items[threadIdx.x] = wt_item<BN>(p, sched, G, walker, walkers, threadIdx.x);
     __syncthreads();
   };
@@ -601,16 +661,26 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
     // would bound the short tiles). As in the issuer, the whole warp walks and waits and
     // one lane issues.
     const bool codes = warp == 0;
+    bool second = false;
     int st = 0, used = 0;
     uint32_t ph = 0;
     const int gpc = BK / p.group;
     while (ok && walk.next(it)) {
       const W4Class& c = p.cls[it.cls];
-      const int K = c.K, f0 = it.mt * TILE_F + (int)rank * CTA_F;
+      const int cta_f = wt_cta_f<BN, EPI>(it.cls >> 1);
+      const bool mats2 = cta_f == 64;
+      const int K = c.K, f0 = (it.mt * CTAS + (int)rank) * cta_f;
       const bool live = f0 < c.R;  // a CTA whose rows lie behind the matrix loads no weights
       const int y = it.g * c.R + f0, ys = it.g * ((K + p.group - 1) / p.group);
       const int cta_rows = ((it.rows + 15) & ~15) / CTAS;
       const bool half = cta_rows <= S::HALF;
+      if (TWO && !codes && it.cls >= 2 && !second) {
+        second = true;
+        if (!w4_grid_wait(p.grid_count, (launch_s + 1) * (gridDim.x * EW), lim, abort_flag)) {
+          ok = false;
+          break;
+        }
+      }
       const int x_row = it.b_row + (int)rank * cta_rows;
       for (int ch = it.c0; ch < it.c1; ++ch) {
         if (!mbar_wait_warp<100>(&stage_free[st], ph ^ 1u, lim, abort_flag)) {
@@ -625,10 +695,10 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
             if (live) {
               mbar_arrive_expect_tx(&code_full[st], S::CODE_BYTES + gpc * 256);
               tma_load_2d(&maps.codes[it.cls][0], &code_full[st], cs, ch * (BK / 2), y);
-              if (MATS == 2)
+              if (mats2)
                 tma_load_2d(&maps.codes[it.cls][1], &code_full[st], cs + S::CODE_BYTES / 2, ch * (BK / 2), y);
               tma_load_2d(&maps.scales[it.cls][0], &code_full[st], ss, f0, ys + ch * gpc);
-              if (MATS == 2)
+              if (mats2)
                 tma_load_2d(&maps.scales[it.cls][1], &code_full[st], ss + S::SCALE_BYTES / 2, f0, ys + ch * gpc);
             } else {
               mbar_arrive(&code_full[st]);
@@ -744,14 +814,19 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
   } else if (warp >= WT_EXPAND_WARP && warp < S::EPI_WARP) {
     // ---------------------------------------------------------------- expanders
     const int team = (warp - WT_EXPAND_WARP) >> 2, q = warp & 3;
-    const int row = MATS == 2 ? (lane >> 4) * 64 + q * 16 + (lane & 15) : q * 32 + lane;  // of the staged codes
-    const uint32_t code_off = S::X_BYTES + row * (BK / 2);
-    const uint32_t sw = BK == 256 ? row & 7 : (row >> 1) & 3;  // the TMA's 128- or 64-byte swizzle
-    // scales: [matrix][group][64 rows] or [group][128 rows]
-    const uint32_t scale_off = S::X_BYTES + S::CODE_BYTES +
-                               (MATS == 2 ? (lane >> 4) * (S::SCALE_BYTES / 2) + (q * 16 + (lane & 15)) * 2 : row * 2);
-    constexpr int SCALE_PITCH = MATS == 2 ? 128 : 256;
+    // (set for each piece: SwiGLU's first product stages two matrices)
+    uint32_t code_off, sw, scale_off, scale_pitch;
     const int gl2 = 31 - __clz(p.group);
+    auto layout = [&](const bool mats2) {
+      const int row = mats2 ? (lane >> 4) * 64 + q * 16 + (lane & 15) : q * 32 + lane;  // of the staged codes
+      code_off = S::X_BYTES + row * (BK / 2);
+      sw = BK == 256 ? row & 7 : (row >> 1) & 3;  // the TMA's 128- or 64-byte swizzle
+      // scales: [matrix][group][64 rows] or [group][128 rows]
+      scale_off = S::X_BYTES + S::CODE_BYTES +
+                  (mats2 ? (lane >> 4) * (S::SCALE_BYTES / 2) + (q * 16 + (lane & 15)) * 2 : row * 2);
+      scale_pitch = mats2 ? 128 : 256;
+    };
+    layout(wt_cta_f<BN, EPI>(0) == 64);
     const uint32_t t_lane = tmem + ((uint32_t)(q * 32) << 16) + S::NUM_ACC * S::ACC_COLS;
     int st = 0, as = 0, turn = 0;
     uint32_t ph = 0;
@@ -784,7 +859,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
           for (int i = 0; i < BK / 32; ++i) {
             const int gi = (i * 32) >> gl2;
             if (EARLY) cw[i] = lds128(base + code_off + ((i ^ sw) << 4));
-            sc[i] = lds16(base + scale_off + gi * SCALE_PITCH);
+            sc[i] = lds16(base + scale_off + gi * scale_pitch);
             if (ch * (BK >> gl2) + gi >= ng) sc[i] = 0u;  // behind K: x is zero there, the scale not this row's
             few = few && w4_scale_is_short(sc[i]);
           }
@@ -838,6 +913,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
         scheduled();
       }
       if (!ok || !walk.next(it)) break;
+      if (TWO) layout(wt_cta_f<BN, EPI>(it.cls >> 1) == 64);
       ng = (p.cls[it.cls].K + p.group - 1) >> gl2;
     } while (true);
     if (!ok) {
@@ -852,14 +928,24 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
     constexpr int CSTEP = 16 * (EW / 4);
     int acc = 0, n0 = 0;
     uint32_t accph = 0;
+    bool left_first = !TWO;
+    auto leave_first = [&]() {  // once a launch, by every epilogue warp, whatever happened before
+      left_first = true;
+      __threadfence();
+      asm volatile("fence.proxy.async.global;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) atomicAdd(p.grid_count, 1ull);
+    };
     while (ok && walk.next(it)) {
       const W4Class& c = p.cls[it.cls];
-      const int f0 = it.mt * TILE_F + (int)rank * CTA_F;
+      const int phase = EPI == EPI_DOWN ? 1 : it.cls >> 1;
+      if (TWO && phase == 1 && !left_first) leave_first();
+      const int f0 = (it.mt * CTAS + (int)rank) * (EPI == EPI_DOWN ? 128 : wt_cta_f<BN, EPI>(phase));
       const int rows = it.rows;
       // 16 rows' sums of this lane's weight row -> output rows [c0, c0 + 16)
       auto emit = [&](const int c0, const float (&v)[16]) {
         const int jn = min(16, rows - c0);
-        if (EPI == EPI_DOWN) {
+        if (EPI == EPI_DOWN || (TWO && phase == 1)) {
           const int feat = f0 + q * 32 + lane;
           const long long r0 = it.out_row + c0;
           float wv = 1.f;
@@ -912,7 +998,8 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
       const bool whole = it.wa == it.wb;
       // this warp's part of a walker's partial sums: [row][128 lanes]
       auto part_of = [&](const int w, const int slot) {
-        return p.partial + ((((size_t)w * 2 + slot) * CTAS + rank) * BN) * 128 + q * 32 + lane;
+        return p.partial + (TWO && phase == 1 ? w4_partial_floats(BN) : 0) +
+               ((((size_t)w * 2 + slot) * CTAS + rank) * BN) * 128 + q * 32 + lane;
       };
       float* mine = whole ? nullptr : part_of(walker, it.wa < walker ? 0 : 1);
       if (!mbar_wait_warp<100>(&acc_full[acc], accph, lim, abort_flag)) {
@@ -987,8 +1074,10 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
         // the last of the tile's walkers to get here adds the parts, in the order of K
         __threadfence();
         __syncwarp();
+        unsigned* const counters =
+            p.counters + (TWO ? (2 * (int)(launch_s & 1) + phase) * W4_COUNTERS2 : 0);
         unsigned n = 0;
-        if (lane == 0) n = atomicAdd(&p.counters[(it.wa * CTAS + (int)rank) * EW + ew], 1u);
+        if (lane == 0) n = atomicAdd(&counters[(it.wa * CTAS + (int)rank) * EW + ew], 1u);
         n = __shfl_sync(0xffffffffu, n, 0);
         if (n == (unsigned)(it.wb - it.wa)) {
           __threadfence();
@@ -1008,6 +1097,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
         }
       }
     }
+    if (!left_first) leave_first();
     if (!ok) {
       set_status(p.status, MOE_ERR_TIMEOUT);
       abort_s = 1;
@@ -1049,18 +1139,18 @@ bool make_map_rows(CUtensorMap* m, const void* ptr, long long K, long long rows,
 template <int BN, int EPI>
 cudaError_t launch_impl(const W4Params& p, cudaStream_t s) {
   using S = WtShape<BN>;
-  constexpr int MATS = EPI == EPI_SWIGLU ? 2 : 1, ROWS = MATS == 2 ? 64 : 128;
-  WtMaps maps;
-  for (int i = 0; i < 2; ++i) {
-    const W4Class& c = p.cls[i < p.n_classes ? i : 0];
-    const int ng = (c.K + p.group - 1) / p.group;
+  WtMaps<S::PHASES> maps;
+  for (int i = 0; i < 2 * S::PHASES; ++i) {
+    const W4Class& c = p.cls[i % 2 < p.n_classes ? i : i & ~1];
+    const bool mats2 = EPI == EPI_SWIGLU && i < 2;
+    const int ng = (c.K + p.group - 1) / p.group, rows = mats2 ? 64 : 128;
     for (int j = 0; j < 2; ++j) {
-      const W4Matrix& a = MATS == 2 && j ? c.a1 : c.a0;
+      const W4Matrix& a = mats2 && j ? c.a1 : c.a0;
       if (!make_map_2d(&maps.codes[i][j], a.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.K / 2, (long long)c.n_groups * c.R,
-                       c.K / 2, S::BK / 2, ROWS,
+                       c.K / 2, S::BK / 2, rows,
                        S::BK == 256 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) ||
           !make_map_2d(&maps.scales[i][j], a.scales, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, c.R, (long long)c.n_groups * ng,
-                       2LL * c.R, ROWS, S::BK / p.group, CU_TENSOR_MAP_SWIZZLE_NONE))
+                       2LL * c.R, rows, S::BK / p.group, CU_TENSOR_MAP_SWIZZLE_NONE))
         return cudaErrorInvalidValue;
     }
     if (!make_map_2d(&maps.xt[i], c.b, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, c.K, c.b_rows, 2LL * c.K, 64, S::HALF,
@@ -1077,10 +1167,15 @@ cudaError_t launch_impl(const W4Params& p, cudaStream_t s) {
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
+  if (S::PAIR) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+  } else {
+    attr[1].id = cudaLaunchAttributeCooperative;
+    attr[1].val.cooperative = 1;
+  }
   static int walkers[64] = {0};  // a device: CTAs or pairs that can be resident at once
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1101,7 +1196,7 @@ cudaError_t launch_impl(const W4Params& p, cudaStream_t s) {
   }
   cfg.gridDim = dim3(walkers[dev] * (S::PAIR ? 2 : 1));
   cfg.attrs = attr;
-  cfg.numAttrs = S::PAIR ? 2 : 1;
+  cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, kern, maps, p);
   count_launch();
   return e;
@@ -1116,14 +1211,16 @@ int w4_pick_bn(long long T, double avg_rows) {
   return want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : want <= 128 ? 128 : 192;
 }
 
-size_t w4_partial_bytes(int bn) { return (size_t)W4_MAX_CTAS * 2 * bn * 128 * sizeof(float); }
+bool w4_both_products(int bn) { return bn <= 32; }
+
+size_t w4_partial_bytes(int bn) { return w4_partial_floats(bn) * sizeof(float) * (w4_both_products(bn) ? 2 : 1); }
 
 cudaError_t launch_w4_gemm(int epi, int bn, const W4Params& p, cudaStream_t s) {
 #define MOE_W4_CASE(BN_)                                                  \
   if (bn == BN_) {                                                        \
+    static_assert(WtShape<BN_>::PHASES == (BN_ <= 32 ? 2 : 1), "phases"); \
     if (epi == EPI_SWIGLU) return launch_impl<BN_, EPI_SWIGLU>(p, s);     \
     if (epi == EPI_RELU) return launch_impl<BN_, EPI_RELU>(p, s);         \
-    if (epi == EPI_DOWN) return launch_impl<BN_, EPI_DOWN>(p, s);         \
   }
   MOE_W4_CASE(16)
   MOE_W4_CASE(32)
@@ -1131,6 +1228,9 @@ cudaError_t launch_w4_gemm(int epi, int bn, const W4Params& p, cudaStream_t s) {
   MOE_W4_CASE(128)
   MOE_W4_CASE(192)
 #undef MOE_W4_CASE
+  if (epi == EPI_DOWN && bn == 64) return launch_impl<64, EPI_DOWN>(p, s);
+  if (epi == EPI_DOWN && bn == 128) return launch_impl<128, EPI_DOWN>(p, s);
+  if (epi == EPI_DOWN && bn == 192) return launch_impl<192, EPI_DOWN>(p, s);
   return cudaErrorInvalidValue;
 }
 
