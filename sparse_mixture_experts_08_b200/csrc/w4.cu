@@ -320,15 +320,13 @@ __device__ __forceinline__ WtItem wt_item(const W4Params& p, const WtSched<WtSha
 }
 
 // The schedule, by one warp: groups ordered by tile height, tallest first (a counting
-// sort over the heights, stable in group order), tiles and costs added up in that order.
-template <int BN, int EPI>
-__device__ __forceinline__ void wt_schedule(const W4Params& p, WtSched<WtShape<BN>::PHASES>& s, int G, int walker, int walkers, int lane) {
-  constexpr int BK = WtShape<BN>::BK;
+// sort over the heights, stable in group order), tiles and costs added up in that order,
+// and this walker's first pieces of work. First the order, then a warp for each phase.
+template <int BN>
+__device__ __forceinline__ void wt_order(const W4Params& p, WtSched<WtShape<BN>::PHASES>& s, int G, int lane) {
   constexpr int NB = BN / 16 + 1;  // bucket = tile height / 16 (0: a group without rows)
   static_assert(NB <= 32, "a bucket a lane");
   const int G0 = p.cls[0].n_groups;
-  // an earlier kernel of the call that flagged a device error leaves tables that are not used
-  const int prior = p.status ? *reinterpret_cast<volatile int*>(p.status) : 0;
   s.hist[lane] = 0;
   __syncwarp();
   for (int g0 = 0; g0 < G; g0 += 32) {
@@ -380,71 +378,80 @@ __device__ __forceinline__ void wt_schedule(const W4Params& p, WtSched<WtShape<B
   }
   for (int gi = lane; gi < G; gi += 32) s.gid[s.hist[s.height[gi] >> 4] + s.ph[0].cost[gi]] = gi;
   __syncwarp();
-#pragma unroll 1
-  for (int phase = 0; phase < WtShape<BN>::PHASES; ++phase) {
-    WtPhase& f = s.ph[phase];
-    const int tile_f = wt_cta_f<BN, EPI>(phase) * (WtShape<BN>::PAIR ? 2 : 1);
-    int total = 0;
-    for (int p0 = 0; p0 < G; p0 += 32) {
-      const int pos = p0 + lane;
-      int n = 0;
-      if (pos < G) {
-        const int gi = s.gid[pos];
-        n = ((p.cls[2 * phase + (gi < G0 ? 0 : 1)].R + tile_f - 1) / tile_f) * ((s.rows[gi] + BN - 1) / BN);
-      }
-      int inc = n;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, off);
-        if (lane >= off) inc += v;
-      }
-      if (pos < G) f.tile_start[pos] = total + inc - n;
-      total += __shfl_sync(0xffffffffu, inc, 31);
-    }
-    if (lane == 0) f.tile_start[G] = total;
-    __syncwarp();
-    if (__any_sync(0xffffffffu, prior != 0)) total = 0;
-    // whole rounds, and the tiles that are cut
-    const int rounds = total / walkers - (total >= walkers && total % walkers ? 1 : 0), t0 = rounds * walkers;
-    int cut = 0;
-    for (int p0 = 0; p0 < G; p0 += 32) {
-      const int pos = p0 + lane;
-      int c = 0;
-      if (pos < G && total) {
-        const int gi = s.gid[pos], n = f.tile_start[pos + 1] - max(f.tile_start[pos], t0);
-        if (n > 0) c = n * wt_chunks<BN>(p.cls[2 * phase + (gi < G0 ? 0 : 1)]) * wt_weight(s.height[gi]);
-      }
-      int inc = c;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, off);
-        if (lane >= off) inc += v;
-      }
-      if (pos < G) f.cost[pos] = cut + inc - c;
-      cut += __shfl_sync(0xffffffffu, inc, 31);
-    }
-    __syncwarp();
-    // (at least 512 columns of the heaviest tile, so that every walker between a tile's
-    // first and last one has a part of it)
-    const int share = max((cut + walkers - 1) / walkers, 512 / BK * max(BN / 16, 4));
-    const int from = walker * share, to = min(from + share, cut);
-    int tile = 0;
-    if (lane < 2 && from < to) {  // the tiles that hold the first and the last of its cost
-      const int x = lane == 0 ? from : to - 1;
-      const int pos = wt_find(f.cost, G, x), gi = s.gid[pos];
-      const int tc = wt_chunks<BN>(p.cls[2 * phase + (gi < G0 ? 0 : 1)]) * wt_weight(s.height[gi]);
-      tile = max(f.tile_start[pos], t0) + (x - f.cost[pos]) / tc;
-    }
-    const int last = __shfl_sync(0xffffffffu, tile, 1);
-    if (lane == 0) {
-      f.rounds = rounds;
-      f.t0 = t0;
-      f.cut = cut;
-      f.per = share;
-      f.t_first = tile;
-      f.n = rounds + (from < to ? last - tile + 1 : 0);
-    }
+}
+
+template <int BN, int EPI>
+__device__ __forceinline__ void wt_phase(const W4Params& p, WtSched<WtShape<BN>::PHASES>& s, int G, int walker,
+                                         int walkers, int lane, int phase, bool none) {
+  using S = WtShape<BN>;
+  WtPhase& f = s.ph[phase];
+  const int G0 = p.cls[0].n_groups;
+  const int log2_f = (EPI == EPI_SWIGLU && phase == 0 ? 6 : 7) + (S::PAIR ? 1 : 0);
+  const int tiles0 = (p.cls[2 * phase].R + (1 << log2_f) - 1) >> log2_f;
+  const int tiles1 = (p.cls[2 * phase + 1].R + (1 << log2_f) - 1) >> log2_f;
+  const int nc0 = wt_chunks<BN>(p.cls[2 * phase]), nc1 = wt_chunks<BN>(p.cls[2 * phase + 1]);
+  const int per = (G + 31) / 32, lo = min(G, lane * per), hi = min(G, lo + per);
+  int sum = 0;
+  for (int pos = lo; pos < hi; ++pos) {
+    const int gi = s.gid[pos], n = (gi < G0 ? tiles0 : tiles1) * ((s.rows[gi] + BN - 1) / BN);
+    f.tile_start[pos] = sum;  // (this lane's part)
+    sum += n;
   }
+  int inc = sum;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, inc, off);
+    if (lane >= off) inc += v;
+  }
+  for (int pos = lo; pos < hi; ++pos) f.tile_start[pos] += inc - sum;
+  int total = __shfl_sync(0xffffffffu, inc, 31);
+  if (lane == 0) f.tile_start[G] = total;
+  __syncwarp();
+  if (none) total = 0;
+  // whole rounds, and the tiles that are cut
+  int rounds = 0;
+  if (total >= walkers) {
+    rounds = total / walkers;
+    if (rounds * walkers != total) --rounds;
+  }
+  const int t0 = rounds * walkers;
+  sum = 0;
+  for (int pos = lo; pos < hi; ++pos) {
+    const int gi = s.gid[pos], n = f.tile_start[pos + 1] - max(f.tile_start[pos], t0);
+    f.cost[pos] = sum;
+    if (n > 0 && total) sum += n * (gi < G0 ? nc0 : nc1) * wt_weight(s.height[gi]);
+  }
+  inc = sum;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, inc, off);
+    if (lane >= off) inc += v;
+  }
+  for (int pos = lo; pos < hi; ++pos) f.cost[pos] += inc - sum;
+  const int cut = __shfl_sync(0xffffffffu, inc, 31);
+  __syncwarp();
+  // (at least 512 columns of the heaviest tile, so that every walker between a tile's
+  // first and last one has a part of it)
+  const int share = max((cut + walkers - 1) / walkers, 512 / S::BK * max(BN / 16, 4));
+  const int from = walker * share, to = min(from + share, cut);
+  int tile = 0;
+  if (lane < 2 && from < to) {  // the tiles that hold the first and the last of its cost
+    const int x = lane == 0 ? from : to - 1;
+    const int pos = wt_find(f.cost, G, x), gi = s.gid[pos];
+    tile = max(f.tile_start[pos], t0) + (x - f.cost[pos]) / ((gi < G0 ? nc0 : nc1) * wt_weight(s.height[gi]));
+  }
+  const int last = __shfl_sync(0xffffffffu, tile, 1);
+  if (lane == 0) {
+    f.rounds = rounds;
+    f.t0 = t0;
+    f.cut = cut;
+    f.per = share;
+    f.t_first = tile;
+    f.n = rounds + (from < to ? last - tile + 1 : 0);
+  }
+  __syncwarp();
+  if (S::PHASES == 1)
+    for (int i = lane; i < min(f.n, WT_ITEMS); i += 32) s.items[i] = wt_item<BN>(p, s, G, walker, walkers, i);
 }
 
 // The list of a walker's pieces of work, walked alike by every role.
@@ -541,6 +548,9 @@ __device__ __forceinline__ uint32_t lds16(uint32_t a) {
   return v;
 }
 
+// Barrier of the two warps that lay out the schedule of two products (named barrier 1).
+__device__ __forceinline__ void schedule_bar() { asm volatile("barrier.sync 1, 64;" ::: "memory"); }
+
 // Tile copy over three dimensions; PAIR: counted on a barrier of the leader CTA.
 template <bool PAIR>
 __device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint32_t bar, void* dst, int x, int y, int z) {
@@ -616,12 +626,24 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
     __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base_s;
-  // Barriers and tensor memory are ready. Warp 0 waits for the kernels before this one and
-  // lays out the schedule, warp 3 sees to the counters; the expanders run their loop body
+  // Barriers and tensor memory are ready. Warp 0 (and 2) waits for the kernels before this
+  // one and lays out the schedule, warp 3 sees to the counters; the expanders run their loop body
   // once on whatever the shared memory holds, which fetches its instructions meanwhile.
-  if (warp == 0) {
+  if (warp == 0 || (TWO && warp == 2)) {
     pdl_wait();
-    wt_schedule<BN, EPI>(p, sched, G, walker, walkers, lane);
+    // an earlier kernel of the call that flagged a device error leaves tables that are not used
+    const int prior = p.status ? *reinterpret_cast<volatile int*>(p.status) : 0;
+    if (warp == 0) wt_order<BN>(p, sched, G, lane);
+    __syncwarp();
+    if (TWO) schedule_bar();
+    wt_phase<BN, EPI>(p, sched, G, walker, walkers, lane, warp >> 1, __any_sync(0xffffffffu, prior != 0));
+    if (TWO) {
+      schedule_bar();
+      const int n0 = sched.ph[0].n, n = n0 + sched.ph[S::PHASES - 1].n;
+      for (int i = (warp ? n0 : 0) + lane; i < min(warp ? n : n0, WT_ITEMS); i += 32)
+        sched.items[i] = wt_item<BN>(p, sched, G, walker, walkers, i);
+    }
+    __syncwarp();
   } else if (warp == 3) {
     // TWO: the second product's input rows are the first one's output, so they wait for a
     // grid-wide count of the epilogue warps that have left the first product (all CTAs are
@@ -643,13 +665,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
       for (int i = lane; i < W4_COUNTERS; i += 32) p.counters_next[i] = 0u;
     }
   }
-  auto scheduled = [&]() {  // every warp passes here once before it walks
-    __syncthreads();
-    if (threadIdx.x < min(sched.ph[0].n + (TWO ? sched.ph[S::PHASES - 1].n : 0), WT_ITEMS))
-      sched.items[threadIdx.x] = wt_item<BN>(p, sched, G, walker, walkers, threadIdx.x);
-    __syncthreads();
-  };
-  if (warp < WT_EXPAND_WARP || warp >= S::EPI_WARP) scheduled();
+  if (warp < WT_EXPAND_WARP || warp >= S::EPI_WARP) __syncthreads();  // the schedule is there
   const unsigned long long lim = p.wait_limit_ns;
   WtWalk<BN> walk(p, sched, G, walker, walkers);
   WtItem it;
@@ -910,7 +926,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
       }
       if (dry) {
         dry = false;
-        scheduled();
+        __syncthreads();  // the schedule is there
       }
       if (!ok || !walk.next(it)) break;
       if (TWO) layout(wt_cta_f<BN, EPI>(it.cls >> 1) == 64);
@@ -1086,7 +1102,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
             float v[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] = 0.f;
-#pragma unroll 1
+#pragma unroll 2
             for (int w = it.wa; w <= it.wb; ++w) {
               const float* o = part_of(w, w == it.wa ? 1 : 0) + c0 * 128;
 #pragma unroll
