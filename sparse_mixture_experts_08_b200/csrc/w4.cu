@@ -18,8 +18,11 @@ namespace moe {
 namespace {
 
 // ------------------------------------------------------------------ quantizer
+// Both directions are bound by HBM when few instructions are spent an element: two bytes
+// of weights and half a byte of codes each way.
 constexpr int QW_WARPS = 8;    // warps a block
-constexpr int QW_ROWS = 32;    // rows a block, 4 a warp
+constexpr int QW_ROWS = 32;    // rows a turn of a block, 4 a warp
+constexpr int QW_TURNS = 4;    // turns a block, at most
 constexpr int QW_COLS = 256;   // columns a block: 8 a lane
 
 __device__ __forceinline__ float scale_5bits(float amax) {
@@ -28,56 +31,92 @@ __device__ __forceinline__ float scale_5bits(float amax) {
   return u >= 0x00800000u ? __uint_as_float(u) : 1.f;
 }
 
-// Code + 8 of v: a saturating integer conversion, so any input gives a code.
-__device__ __forceinline__ uint32_t code4(float v, float sc) {
-  return (uint32_t)(min(7, max(-8, __float2int_rn(__fdiv_rn(v, sc)))) + 8);
+// The bits of 1.5 2^23 + 8 + (v / scale to the nearest whole number, ties to even), with
+// r = 1 / scale rounded: two instructions in place of a division. v has 8 significant bits
+// and the scale 5, so v / scale is either exactly half-way between two whole numbers or at
+// least 1 / 1280 from it. v r is off by at most 2^-21, so rounding it to multiples of
+// 2^-12 first (the addition of 1.5 2^11) gives the half-way number exactly or stays on its
+// side; the second addition rounds to whole numbers as the division would have.
+__device__ __forceinline__ uint32_t code_bits(float v, float r) {
+  return __float_as_uint(__fadd_rn(__fmaf_rn(v, r, 3072.f), 12582920.f - 3072.f));
 }
 
-// A block takes QW_ROWS rows x QW_COLS columns: a lane 8 columns of 4 rows. The group's
-// maximum comes from the G / 8 lanes that share it; the scales meet in shared memory so
-// that each group's QW_ROWS scales leave as one 64-byte run of the group-major layout.
+__device__ __forceinline__ uint32_t abs_max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b & 0x7FFF7FFFu));
+  return d;
+}
+
+// A block takes QW_COLS columns of QW_TURNS x QW_ROWS rows: a lane 8 columns of 4 rows a
+// turn, the next turn's loads in flight meanwhile. The group's maximum comes from the
+// G / 8 lanes that share it (two rows in one register); the scales meet in shared memory
+// so that each group's scales leave as one run of the group-major layout.
 template <int G>
 __global__ void __launch_bounds__(QW_WARPS * 32)
-    quantize_w4_kernel(int rows, int cols, const uint4* __restrict__ src, uint32_t* __restrict__ codes,
+    quantize_w4_kernel(int rows, int cols, int turns, const uint4* __restrict__ src, uint32_t* __restrict__ codes,
                        __nv_bfloat16* __restrict__ scales) {
-  constexpr int GPB = QW_COLS / G;
-  __shared__ __nv_bfloat16 sc_s[GPB][QW_ROWS];
+  constexpr int GPB = QW_COLS / G, ROWS = QW_ROWS * QW_TURNS;
+  __shared__ __nv_bfloat16 sc_s[GPB][ROWS];
   pdl_launch_dependents();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long mat = blockIdx.z;
   const int ng = (cols + G - 1) / G;
   const int c8 = blockIdx.x * (QW_COLS / 8) + lane, n8 = cols >> 3;
-  const int row0 = blockIdx.y * QW_ROWS + warp * 4;
-  uint4 v[4];
+  const int row_b = blockIdx.y * turns * QW_ROWS;
+  const bool cok = c8 < n8;
+  auto fetch = [&](uint4 (&v)[4], const int turn) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (c8 < n8 && row0 + i < rows) v[i] = src[(mat * rows + row0 + i) * n8 + c8];
-  }
+    for (int i = 0; i < 4; ++i) {
+      const int row = row_b + turn * QW_ROWS + warp * 4 + i;
+      v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (cok && row < rows) v[i] = __ldcs(src + (mat * rows + row) * n8 + c8);
+    }
+  };
+  uint4 v[4], nx[4];
+  fetch(v, 0);
+#pragma unroll 1
+  for (int turn = 0; turn < turns; ++turn) {
+    const int row0 = row_b + turn * QW_ROWS + warp * 4;
+    if (row_b + turn * QW_ROWS >= rows) break;
+    if (turn + 1 < turns) fetch(nx, turn + 1);
+    uint32_t m[2];  // the maxima of rows 0, 1 and 2, 3
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-    float f[8], amax = 0.f;
+    for (int i = 0; i < 2; ++i) {
+      uint32_t a = 0u, b = 0u;
+      a = abs_max_bf16x2(abs_max_bf16x2(abs_max_bf16x2(abs_max_bf16x2(a, v[2 * i].x), v[2 * i].y), v[2 * i].z),
+                         v[2 * i].w);
+      b = abs_max_bf16x2(
+          abs_max_bf16x2(abs_max_bf16x2(abs_max_bf16x2(b, v[2 * i + 1].x), v[2 * i + 1].y), v[2 * i + 1].z),
+          v[2 * i + 1].w);
+      m[i] = abs_max_bf16x2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      f[2 * j] = __uint_as_float(w[j] << 16);
-      f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-      amax = fmaxf(amax, fmaxf(fabsf(f[2 * j]), fabsf(f[2 * j + 1])));
+      for (int off = G / 16; off > 0; off >>= 1) m[i] = abs_max_bf16x2(m[i], __shfl_xor_sync(0xffffffffu, m[i], off));
+    }
+    // lane i of a group's lanes works out row i % 4's scale for all of them
+    const uint32_t mine = lane & 2 ? m[1] : m[0];
+    const float sc = scale_5bits(__uint_as_float(lane & 1 ? mine & 0xFFFF0000u : mine << 16)), rc = __frcp_rn(sc);
+    if (lane % (G / 8) < 4) sc_s[lane / (G / 8)][turn * QW_ROWS + warp * 4 + (lane & 3)] = __float2bfloat16_rn(sc);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float r = __shfl_sync(0xffffffffu, rc, (lane & ~3) + i);
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      // each term is 0x4B400000 + code + 8: the sum of the shifted terms less the shifted constants
+      uint32_t word = 0u - 0x4B400000u * 0x11111111u;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        word += (code_bits(__uint_as_float(w[j] << 16), r) << (4 * j)) +
+                (code_bits(__uint_as_float(w[j] & 0xFFFF0000u), r) << (16 + 4 * j));
+      if (cok && row0 + i < rows) codes[(mat * rows + row0 + i) * n8 + c8] = word;
     }
 #pragma unroll
-    for (int off = G / 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-    const float sc = scale_5bits(amax);
-    uint32_t word = 0u;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) word |= (code4(f[2 * j], sc) << (4 * j)) | (code4(f[2 * j + 1], sc) << (16 + 4 * j));
-    if (c8 < n8 && row0 + i < rows) codes[(mat * rows + row0 + i) * n8 + c8] = word;
-    if (lane % (G / 8) == 0) sc_s[lane / (G / 8)][warp * 4 + i] = __float2bfloat16_rn(sc);
+    for (int i = 0; i < 4; ++i) v[i] = nx[i];
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < GPB * QW_ROWS; i += QW_WARPS * 32) {
-    const int g = blockIdx.x * GPB + i / QW_ROWS, row = blockIdx.y * QW_ROWS + i % QW_ROWS;
-    if (g < ng && row < rows) scales[(mat * ng + g) * rows + row] = sc_s[i / QW_ROWS][i % QW_ROWS];
+  const int n = turns * QW_ROWS;  // rows of this block: a power of two
+  for (int i = threadIdx.x; i < GPB * n; i += QW_WARPS * 32) {
+    const int gl = i / n, r = i % n, g = blockIdx.x * GPB + gl, row = row_b + r;
+    if (g < ng && row < rows) scales[(mat * ng + g) * rows + row] = sc_s[gl][r];
   }
 }
 
@@ -113,10 +152,11 @@ __device__ __forceinline__ uint32_t w4_pair_scaled(uint32_t w, int e, uint32_t s
 __device__ __forceinline__ bool w4_scale_is_short(uint32_t s) { return (s & 3u) == 0u && (s & 0x7FFFu) < 0x7C00u; }
 
 // The inverse: bf16(code * scale) (exact for the quantizer's scales). A lane turns one
-// word (8 columns) of 4 neighbouring rows into 16 bytes each.
+// word (8 columns) of 4 neighbouring rows a turn into 16 bytes each, the next turn's words
+// in flight meanwhile.
 template <int G>
 __global__ void __launch_bounds__(QW_WARPS * 32)
-    dequantize_w4_kernel(int rows, int cols, const uint32_t* __restrict__ codes,
+    dequantize_w4_kernel(int rows, int cols, int turns, const uint32_t* __restrict__ codes,
                          const uint16_t* __restrict__ scales, uint4* __restrict__ dst) {
   pdl_launch_dependents();
   pdl_wait();
@@ -124,21 +164,36 @@ __global__ void __launch_bounds__(QW_WARPS * 32)
   const long long mat = blockIdx.z;
   const int ng = (cols + G - 1) / G;
   const int c8 = blockIdx.x * (QW_COLS / 8) + lane, n8 = cols >> 3;
-  const int row0 = blockIdx.y * QW_ROWS + warp * 4;
-  if (c8 >= n8 || row0 >= rows) return;  // rows % 8 == 0: the 4 rows exist together
-  const uint2 s4 = *reinterpret_cast<const uint2*>(scales + (mat * ng + 8 * c8 / G) * rows + row0);
-  uint32_t w[4];
+  const int row_b = blockIdx.y * turns * QW_ROWS + warp * 4;
+  if (c8 >= n8) return;
+  uint32_t w[4], nw[4];
+  uint2 s4, ns4;
+  auto fetch = [&](uint32_t (&d)[4], uint2& s, const int turn) {
+    const int row0 = row_b + turn * QW_ROWS;
+    if (turn >= turns || row0 >= rows) return;  // rows % 8 == 0: the 4 rows exist together
+    s = *reinterpret_cast<const uint2*>(scales + (mat * ng + 8 * c8 / G) * rows + row0);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = codes[(mat * rows + row0 + i) * n8 + c8];
+    for (int i = 0; i < 4; ++i) d[i] = __ldcs(codes + (mat * rows + row0 + i) * n8 + c8);
+  };
+  fetch(w, s4, 0);
+#pragma unroll 1
+  for (int turn = 0; turn < turns; ++turn) {
+    const int row0 = row_b + turn * QW_ROWS;
+    if (row0 >= rows) break;
+    fetch(nw, ns4, turn + 1);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t h = ((i & 2) ? s4.y : s4.x) >> (16 * (i & 1)) & 0xFFFFu, ss = h | (h << 16);
-    uint4 o;
-    o.x = mul_bf16x2(w4_pair(w[i]), ss);
-    o.y = mul_bf16x2(w4_pair(w[i] >> 4), ss);
-    o.z = mul_bf16x2(w4_pair(w[i] >> 8), ss);
-    o.w = mul_bf16x2(w4_pair(w[i] >> 12), ss);
-    dst[(mat * rows + row0 + i) * n8 + c8] = o;
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t h = ((i & 2) ? s4.y : s4.x) >> (16 * (i & 1)) & 0xFFFFu, ss = h | (h << 16);
+      uint4 o;
+      o.x = mul_bf16x2(w4_pair(w[i]), ss);
+      o.y = mul_bf16x2(w4_pair(w[i] >> 4), ss);
+      o.z = mul_bf16x2(w4_pair(w[i] >> 8), ss);
+      o.w = mul_bf16x2(w4_pair(w[i] >> 12), ss);
+      __stcs(dst + (mat * rows + row0 + i) * n8 + c8, o);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = nw[i];
+    s4 = ns4;
   }
 }
 
@@ -189,8 +244,8 @@ struct WtShape {
   static constexpr int PHASES = PAIR ? 1 : 2;          // both products in one launch (short segments)
   static constexpr int SMEM_BUDGET = (PHASES == 2 ? 180 : 196) * 1024;
   static constexpr int BK = PAIR ? 128 : 256;          // columns of K a stage
-  static constexpr int TEAMS = PAIR ? 2 : 3;    // teams of four expanding warps
-  static constexpr int EW = PAIR ? 8 : 4;              // epilogue warps
+  static constexpr int TEAMS = BN > 128 ? 2 : 3;    // teams of four expanding warps
+  static constexpr int EW = BN > 128 ? 8 : 4;              // epilogue warps
   static constexpr int EPI_WARP = WT_EXPAND_WARP + 4 * TEAMS;
   static constexpr int THREADS = 32 * (EPI_WARP + EW);
   static constexpr int B_ROWS = PAIR ? BN / 2 : BN;    // input rows a CTA
@@ -1221,10 +1276,11 @@ cudaError_t launch_impl(const W4Params& p, cudaStream_t s) {
 }  // namespace
 
 // Input rows a tile: enough for most segments to be one tile (every further tile of a
-// segment expands the expert's weights again), no more than that (a stage's bytes).
+// segment expands the expert's weights again), no more than that (a stage's bytes, and
+// the tensor memory left for expanded weights).
 int w4_pick_bn(long long T, double avg_rows) {
-  const double want = std::min((double)T, 2.5 * avg_rows);
-  return want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : want <= 128 ? 128 : 192;
+  const double want = std::min((double)T, 2.0 * avg_rows);
+  return want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : std::min((double)T, avg_rows) <= 160 ? 128 : 192;
 }
 
 bool w4_both_products(int bn) { return bn <= 32; }
@@ -1250,11 +1306,19 @@ cudaError_t launch_w4_gemm(int epi, int bn, const W4Params& p, cudaStream_t s) {
   return cudaErrorInvalidValue;
 }
 
+// Turns of a block: all of them where that still gives every SM several blocks, else one
+// (a small matrix is bound by one block's latency).
+static int quantizer_turns(long long n, int rows, int cols) {
+  const long long blocks = n * ((cols + QW_COLS - 1) / QW_COLS) * ((rows + QW_ROWS - 1) / QW_ROWS);
+  return blocks >= 16LL * QW_TURNS * num_sms() ? QW_TURNS : 1;
+}
+
 cudaError_t launch_quantize_w4(long long n, int rows, int cols, int group, const void* src, uint8_t* codes,
                                void* scales, cudaStream_t s) {
-  const dim3 grid((cols + QW_COLS - 1) / QW_COLS, (rows + QW_ROWS - 1) / QW_ROWS, (unsigned)n);
+  const int turns = quantizer_turns(n, rows, cols), block_rows = QW_ROWS * turns;
+  const dim3 grid((cols + QW_COLS - 1) / QW_COLS, (rows + block_rows - 1) / block_rows, (unsigned)n);
   auto kern = group == 32 ? quantize_w4_kernel<32> : group == 64 ? quantize_w4_kernel<64> : quantize_w4_kernel<128>;
-  cudaError_t e = launch_k(kern, grid, dim3(QW_WARPS * 32), 0, s, rows, cols, (const uint4*)src, (uint32_t*)codes,
+  cudaError_t e = launch_k(kern, grid, dim3(QW_WARPS * 32), 0, s, rows, cols, turns, (const uint4*)src, (uint32_t*)codes,
                            (__nv_bfloat16*)scales);
   count_launch();
   return e;
@@ -1262,10 +1326,11 @@ cudaError_t launch_quantize_w4(long long n, int rows, int cols, int group, const
 
 cudaError_t launch_dequantize_w4(long long n, int rows, int cols, int group, const uint8_t* codes, const void* scales,
                                  void* dst, cudaStream_t s) {
-  const dim3 grid((cols + QW_COLS - 1) / QW_COLS, (rows + QW_ROWS - 1) / QW_ROWS, (unsigned)n);
+  const int turns = quantizer_turns(n, rows, cols), block_rows = QW_ROWS * turns;
+  const dim3 grid((cols + QW_COLS - 1) / QW_COLS, (rows + block_rows - 1) / block_rows, (unsigned)n);
   auto kern =
       group == 32 ? dequantize_w4_kernel<32> : group == 64 ? dequantize_w4_kernel<64> : dequantize_w4_kernel<128>;
-  cudaError_t e = launch_k(kern, grid, dim3(QW_WARPS * 32), 0, s, rows, cols, (const uint32_t*)codes,
+  cudaError_t e = launch_k(kern, grid, dim3(QW_WARPS * 32), 0, s, rows, cols, turns, (const uint32_t*)codes,
                            (const uint16_t*)scales, (uint4*)dst);
   count_launch();
   return e;
