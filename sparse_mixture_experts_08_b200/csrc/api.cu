@@ -961,9 +961,9 @@ moe_status_t moe_add_rmsnorm(int64_t rows, int32_t d, int32_t dtype, float eps, 
                              moe_stream_t stream) {
   if (rows < 0 || d < 8 || (dtype != MOE_F32 && dtype != MOE_BF16)) return MOE_ERR_INVALID_ARG;
   if (!(eps >= 0.f && eps <= 3.0e38f)) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return d % 8 || d > norm_max_d() ? MOE_ERR_UNSUPPORTED : MOE_OK;  // (empty tensors have no addresses)
   if (!codes != !scales || (!y && !codes)) return MOE_ERR_INVALID_ARG;
   if (d % (codes ? 16 : 8) || d > norm_max_d() || rows > (1LL << 40) / d) return MOE_ERR_UNSUPPORTED;
-  if (rows == 0) return MOE_OK;
   if (!x || !weight) return MOE_ERR_INVALID_ARG;
   for (const void* p : std::initializer_list<const void*>{x, residual, weight, sum_out, y, (const void*)codes})
     if (p && !aligned16(p)) return MOE_ERR_INVALID_ARG;

@@ -16,10 +16,11 @@ namespace moe {
 namespace {
 
 template <typename T>
-struct Vec8;  // 8 consecutive elements
+struct Vec;  // the N consecutive elements of 16 bytes
 
 template <>
-struct Vec8<__nv_bfloat16> {
+struct Vec<__nv_bfloat16> {
+  static constexpr int N = 8;
   uint4 v;
   __device__ __forceinline__ void load(const void* p) { v = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void store(void* p) const { *reinterpret_cast<uint4*>(p) = v; }
@@ -43,92 +44,84 @@ struct Vec8<__nv_bfloat16> {
 };
 
 template <>
-struct Vec8<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const void* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
-  }
-  __device__ __forceinline__ void store(void* p) const {
-    reinterpret_cast<float4*>(p)[0] = a;
-    reinterpret_cast<float4*>(p)[1] = b;
-  }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-  }
-  __device__ __forceinline__ void put(const float (&f)[8]) {
-    a = make_float4(f[0], f[1], f[2], f[3]);
-    b = make_float4(f[4], f[5], f[6], f[7]);
-  }
+struct Vec<float> {
+  static constexpr int N = 4;
+  float4 v;
+  __device__ __forceinline__ void load(const void* p) { v = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ void store(void* p) const { *reinterpret_cast<float4*>(p) = v; }
+  __device__ __forceinline__ void get(float (&f)[4]) const { f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w; }
+  __device__ __forceinline__ void put(const float (&f)[4]) { v = make_float4(f[0], f[1], f[2], f[3]); }
 };
 
-// Reduction over the TPR threads of a row; TPR > 32 goes through shared memory (`buf`,
-// one slot a warp; the caller passes a buffer of its own to each reduction, so one
-// barrier each is enough).
-template <int TPR, bool MAX>
+// Reduction over the threads of a row: one warp, or (WIDE) the block, through shared
+// memory (`buf`, one slot a warp; the caller passes a buffer of its own to each
+// reduction, so one barrier each is enough).
+template <bool WIDE, bool MAX>
 __device__ __forceinline__ float row_reduce(float v, float* buf) {
 #pragma unroll
-  for (int off = (TPR < 32 ? TPR : 32) / 2; off > 0; off >>= 1) {
+  for (int off = 16; off > 0; off >>= 1) {
     const float o = __shfl_xor_sync(0xffffffffu, v, off);
     v = MAX ? fmaxf(v, o) : v + o;
   }
-  if (TPR > 32) {
+  if (WIDE) {
     if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
     __syncthreads();
     v = buf[0];
-#pragma unroll
-    for (int i = 1; i < TPR / 32; ++i) v = MAX ? fmaxf(v, buf[i]) : v + buf[i];
+    const int nw = blockDim.x >> 5;
+    for (int i = 1; i < nw; ++i) v = MAX ? fmaxf(v, buf[i]) : v + buf[i];
   }
   return v;
 }
 
-// TPR threads a row (32: several rows a block, one a warp; more: one row a block), VPT
-// vectors of 8 elements a thread, vector i of thread t at 8 (i TPR + t). An element is
-// read and written by the same thread, in that order, so sum_out or y may be x or
-// residual themselves.
-template <typename T, int TPR, int VPT>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
+// A row's threads: a warp (narrow rows, several a block) or (WIDE) the block, of as many
+// warps as the row's 16-byte vectors fill, VPT a thread (with a power of two of threads,
+// half of them idle at 2056 fp32 elements, 8191 rows took 32 us, so 27).
+// Vector i of thread t starts at element N (i TPR + t). An element is read and written by the same thread, in that
+// order, so sum_out or y may be x or residual themselves.
+template <typename T, bool WIDE, int VPT, int MAX_THREADS>
+__global__ void __launch_bounds__(MAX_THREADS)
     add_rmsnorm_kernel(long long rows, int d, float eps, const T* x, const T* residual,
                        const T* __restrict__ weight, T* sum_out, T* y, uint8_t* __restrict__ codes,
                        float* __restrict__ scales) {
-  constexpr int RPB = TPR < 128 ? 128 / TPR : 1;
   __shared__ float red[2][32];
-  const int t = threadIdx.x % TPR;
-  const long long row = (long long)blockIdx.x * RPB + threadIdx.x / TPR;
-  const int nv = d >> 3;
+  const int TPR = WIDE ? blockDim.x : 32;
+  const int t = WIDE ? threadIdx.x : threadIdx.x & 31;
+  const long long row = WIDE ? blockIdx.x : (long long)blockIdx.x * (MAX_THREADS / 32) + (threadIdx.x >> 5);
+  constexpr int N = Vec<T>::N;
+  const int nv = d / N;
   pdl_launch_dependents();
   pdl_wait();
-  if (row >= rows) return;  // whole warps (TPR = 32); a block of TPR > 32 has one row
+  if (row >= rows) return;  // whole warps; a WIDE block has one row
   // the weight row is fetched with the inputs, so its latency is theirs; rows of four
   // vectors a thread fetch it where it is used (registers)
   constexpr bool EARLY = VPT < 4;
-  Vec8<T> w[EARLY ? VPT : 1];
+  Vec<T> w[EARLY ? VPT : 1];
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
-    if (EARLY && i * TPR + t < nv) w[i].load(weight + 8 * (size_t)(i * TPR + t));
+    if (EARLY && i * TPR + t < nv) w[i].load(weight + N * (size_t)(i * TPR + t));
   const size_t base = (size_t)row * d;
-  float r[VPT][8];
+  float r[VPT][N];
   {
-    Vec8<T> a[VPT], b[VPT];
+    Vec<T> a[VPT], b[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
       if (i * TPR + t < nv) {
-        a[i].load(x + base + 8 * (size_t)(i * TPR + t));
-        if (residual) b[i].load(residual + base + 8 * (size_t)(i * TPR + t));
+        a[i].load(x + base + N * (size_t)(i * TPR + t));
+        if (residual) b[i].load(residual + base + N * (size_t)(i * TPR + t));
       }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       if (i * TPR + t < nv) {
         a[i].get(r[i]);
         if (residual) {
-          float q[8];
+          float q[N];
           b[i].get(q);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) r[i][j] += q[j];
+          for (int j = 0; j < N; ++j) r[i][j] += q[j];
         }
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) r[i][j] = 0.f;
+        for (int j = 0; j < N; ++j) r[i][j] = 0.f;
       }
     }
   }
@@ -136,90 +129,116 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(r[i][j], r[i][j], ss);
+    for (int j = 0; j < N; ++j) ss = fmaf(r[i][j], r[i][j], ss);
   if (sum_out) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
       if (i * TPR + t < nv) {
-        Vec8<T> o;
+        Vec<T> o;
         o.put(r[i]);
-        o.store(sum_out + base + 8 * (size_t)(i * TPR + t));
+        o.store(sum_out + base + N * (size_t)(i * TPR + t));
       }
   }
-  ss = row_reduce<TPR, false>(ss, red[0]);
+  ss = row_reduce<WIDE, false>(ss, red[0]);
   const float inv = 1.f / sqrtf(ss / (float)d + eps);
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
     if (i * TPR + t < nv) {
-      float g[8];
-      if (!EARLY) w[0].load(weight + 8 * (size_t)(i * TPR + t));
+      float g[N];
+      if (!EARLY) w[0].load(weight + N * (size_t)(i * TPR + t));
       w[EARLY ? i : 0].get(g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < N; ++j) {
         r[i][j] = r[i][j] * inv * g[j];
         amax = fmaxf(amax, fabsf(r[i][j]));
       }
       if (y) {
-        Vec8<T> o;
+        Vec<T> o;
         o.put(r[i]);
-        o.store(y + base + 8 * (size_t)(i * TPR + t));
+        o.store(y + base + N * (size_t)(i * TPR + t));
       }
     }
   if (codes) {
-    amax = row_reduce<TPR, true>(amax, red[1]);
-    const float sc = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+    amax = row_reduce<WIDE, true>(amax, red[1]);
+    float sc = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
     if (t == 0) scales[row] = sc;
+    if (sc < 0x1p-100f) {  // the reciprocal of a tiny scale would overflow
+      sc *= 0x1p64f;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int j = 0; j < N; ++j) r[i][j] *= 0x1p64f;
+    }
+    // y times the scale's reciprocal: within 2^-23 of the quotient, which is less than
+    // what fp32 leaves open in y itself
+    const float rs = __frcp_rn(sc);
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
       if (i * TPR + t < nv) {
-        uint32_t o[2];
+        uint32_t o[N / 4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          o[h] = 0u;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            o[h] |= (uint32_t)__nv_cvt_float_to_fp8(__fdiv_rn(r[i][4 * h + j], sc), __NV_SATFINITE, __NV_E4M3)
-                    << (8 * j);
+        for (int h = 0; h < N / 4; ++h) {
+          const float* v = &r[i][4 * h];
+          o[h] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[0] * rs, v[1] * rs), __NV_SATFINITE, __NV_E4M3) |
+                 (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[2] * rs, v[3] * rs), __NV_SATFINITE, __NV_E4M3)
+                     << 16;
         }
-        *reinterpret_cast<uint2*>(codes + base + 8 * (size_t)(i * TPR + t)) = make_uint2(o[0], o[1]);
+        uint8_t* c = codes + base + N * (size_t)(i * TPR + t);
+        if constexpr (N == 8)
+          *reinterpret_cast<uint2*>(c) = make_uint2(o[0], o[1]);
+        else
+          *reinterpret_cast<uint32_t*>(c) = o[0];
       }
   }
 }
 
-template <typename T, int TPR, int VPT>
-cudaError_t launch_norm(long long rows, int d, float eps, const void* x, const void* residual, const void* weight,
-                        void* sum_out, void* y, uint8_t* codes, float* scales, cudaStream_t s) {
-  constexpr int THREADS = TPR < 128 ? 128 : TPR, RPB = THREADS / TPR;
-  const long long blocks = (rows + RPB - 1) / RPB;
+template <typename T, bool WIDE, int VPT, int MAX_THREADS>
+cudaError_t launch_norm(int threads, long long rows, int d, float eps, const void* x, const void* residual,
+                        const void* weight, void* sum_out, void* y, uint8_t* codes, float* scales, cudaStream_t s) {
+  const int per_block = WIDE ? 1 : MAX_THREADS / 32;
+  const long long blocks = (rows + per_block - 1) / per_block;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  cudaError_t e = launch_k(add_rmsnorm_kernel<T, TPR, VPT>, dim3((unsigned)blocks), dim3(THREADS), 0, s, rows, d, eps,
-                           (const T*)x, (const T*)residual, (const T*)weight, (T*)sum_out, (T*)y, codes, scales);
+  cudaError_t e = launch_k(add_rmsnorm_kernel<T, WIDE, VPT, MAX_THREADS>, dim3((unsigned)blocks), dim3(threads), 0, s,
+                           rows, d, eps, (const T*)x, (const T*)residual, (const T*)weight, (T*)sum_out, (T*)y, codes,
+                           scales);
   count_launch();
   return e;
 }
 
+// A warp a row up to two vectors a lane; then two vectors a thread (one where there are
+// too few rows to fill the SMs and latency is what counts), four or eight for rows that
+// would take more than 512 threads (2048 x 16384 bf16 rows with two of 1024 threads ran at
+// 4.3 TB/s, one block a SM).
 template <typename T>
 cudaError_t pick_norm(long long rows, int d, float eps, const void* x, const void* residual, const void* weight,
                       void* sum_out, void* y, uint8_t* codes, float* scales, cudaStream_t s) {
-  const int nv = d / 8;
-#define MOE_NORM(TPR_, VPT_) \
-  if (nv <= TPR_ * VPT_) return launch_norm<T, TPR_, VPT_>(rows, d, eps, x, residual, weight, sum_out, y, codes, scales, s);
-  MOE_NORM(32, 1)
-  MOE_NORM(32, 2)
-  MOE_NORM(128, 1)
-  MOE_NORM(128, 2)
-  MOE_NORM(256, 2)
-  MOE_NORM(512, 2)
-  MOE_NORM(1024, 2)
-  MOE_NORM(1024, 4)
+  const int nv = d / Vec<T>::N;
+  const bool few = rows < 2LL * num_sms();
+  const int vpt = nv <= 32 ? 1 : nv <= 64 ? 2 : few && nv <= 1024 ? 1 : nv <= 1024 ? 2 : nv <= 4096 ? 4 : 8;
+  const int threads = ((nv + vpt - 1) / vpt + 31) & ~31;
+#define MOE_NORM(WIDE_, VPT_, MAX_)                                                                              \
+  return launch_norm<T, WIDE_, VPT_, MAX_>(WIDE_ ? threads : MAX_, rows, d, eps, x, residual, weight, sum_out, y, \
+                                           codes, scales, s)
+  if (nv <= 32) MOE_NORM(false, 1, 128);
+  if (nv <= 64) MOE_NORM(false, 2, 128);
+  if (vpt == 1) MOE_NORM(true, 1, 1024);
+  if (vpt == 2) {
+    if (threads <= 256) MOE_NORM(true, 2, 256);
+    MOE_NORM(true, 2, 512);
+  }
+  if (vpt == 4) {
+    if (threads <= 512) MOE_NORM(true, 4, 512);
+    MOE_NORM(true, 4, 1024);
+  }
+  if constexpr (Vec<T>::N == 4) MOE_NORM(true, 8, 1024);
 #undef MOE_NORM
   return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-int norm_max_d() { return 1024 * 4 * 8; }
+int norm_max_d() { return 32768; }
 
 cudaError_t launch_add_rmsnorm(int dtype, long long rows, int d, float eps, const void* x, const void* residual,
                                const void* weight, void* sum_out, void* y, uint8_t* codes, float* scales,
