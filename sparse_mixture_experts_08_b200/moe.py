@@ -142,20 +142,23 @@ def _p(t) -> Optional[int]:
 _DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
 
 
-def _operands(fn: str, *tensors):
-    """Refuses what the library cannot see: tensors that are not contiguous, or not all on the current CUDA device."""
-    dev = -2
+def _pointers(fn: str, *tensors):
+    """The tensors' addresses. Refuses what the library cannot see: tensors that are not contiguous, or not all on
+    the current CUDA device."""
+    dev, out = None, []
     for t in tensors:
         if t is None or t.__class__ is int:
+            out.append(t)
             continue
-        if dev == -2:
-            dev = t.get_device()
-            if dev < 0 or dev != torch.cuda.current_device():
+        d = t.get_device()
+        if d != dev:
+            if dev is not None or d < 0 or d != torch.cuda.current_device():
                 raise MoEError(fn, ERR_INVALID_ARG)
-        elif t.get_device() != dev:
-            raise MoEError(fn, ERR_INVALID_ARG)
+            dev = d
         if not t.is_contiguous():
             raise MoEError(fn, ERR_INVALID_ARG)
+        out.append(t.data_ptr())
+    return out
 
 
 def _stream(stream) -> Optional[int]:
@@ -317,7 +320,7 @@ def moe_layer_forward_fp8_codes(cfg, x, x_codes, x_scales, w_router, bias, wq, o
                                 topk_idx_out=None, topk_w_out=None, counts_out=None, lis_out=None, h_out=None,
                                 h_shared_out=None, perm_out=None, stream=None):
     """moe_layer_forward_fp8 for tokens that come with E4M3 codes [T, d] and scales [T] (moe_add_rmsnorm's)."""
-    _operands("moe_layer_forward_fp8_codes", x, x_codes, x_scales, w_router, bias, out, ws)
+    _pointers("moe_layer_forward_fp8_codes", x, x_codes, x_scales, w_router, bias, out, ws)
     st = MoEFp8Experts(**{k: _p(wq.get(k)) for k, _ in MoEFp8Experts._fields_})
     _check("moe_layer_forward_fp8_codes", lib().moe_layer_forward_fp8_codes(
         ctypes.byref(cfg), _p(x), _p(x_codes), _p(x_scales), _p(w_router), _p(bias), ctypes.byref(st), _p(out),
@@ -328,12 +331,10 @@ def moe_layer_forward_fp8_codes(cfg, x, x_codes, x_scales, w_router, bias, wq, o
 def moe_add_rmsnorm(x, residual, weight, eps, y, sum_out=None, codes=None, scales=None, stream=None):
     """y [rows, d] = RMS norm of x + residual (residual may be None) times weight; sum_out: the sum; codes
     (uint8, like x) and scales [rows] (fp32): E4M3 codes of y, one scale a row. x is fp32 or bf16, contiguous."""
-    _operands("moe_add_rmsnorm", x, residual, weight, sum_out, y, codes, scales)
+    ptrs = _pointers("moe_add_rmsnorm", x, residual, weight, sum_out, y, codes, scales)
     d = x.shape[-1]
-    rc = lib().moe_add_rmsnorm(x.numel() // d if d else 0, d, _DTYPES.get(x.dtype, -1), eps, _p(x), _p(residual),
-                               _p(weight), _p(sum_out), _p(y), _p(codes), _p(scales), _stream(stream))
-    if rc:
-        _check("moe_add_rmsnorm", rc)
+    _check("moe_add_rmsnorm", lib().moe_add_rmsnorm(x.numel() // d if d else 0, d, _DTYPES.get(x.dtype, -1), eps,
+                                                    *ptrs, _stream(stream)))
 
 
 def _w4_shape(t, cols):
@@ -345,20 +346,18 @@ def _w4_shape(t, cols):
 def moe_quantize_w4(src, group, codes, scales, stream=None):
     """4-bit codes [n, rows, cols / 2] (uint8) and bf16 scales [n, ceil(cols / group), rows] of bf16 matrices
     src [n, rows, cols] (or one matrix [rows, cols])."""
-    _operands("moe_quantize_w4", src, codes, scales)
+    ptrs = _pointers("moe_quantize_w4", src, codes, scales)
     cols = int(src.shape[-1])
     n, rows = _w4_shape(src, cols)
-    _check("moe_quantize_w4", lib().moe_quantize_w4(n, rows, cols, int(group), _p(src), _p(codes), _p(scales),
-                                                    _stream(stream)))
+    _check("moe_quantize_w4", lib().moe_quantize_w4(n, rows, cols, int(group), *ptrs, _stream(stream)))
 
 
 def moe_dequantize_w4(codes, scales, group, dst, stream=None):
     """The bf16 matrices dst [n, rows, cols] that codes and scales (as moe_quantize_w4 writes them) stand for."""
-    _operands("moe_dequantize_w4", codes, scales, dst)
+    ptrs = _pointers("moe_dequantize_w4", codes, scales, dst)
     cols = int(dst.shape[-1])
     n, rows = _w4_shape(dst, cols)
-    _check("moe_dequantize_w4", lib().moe_dequantize_w4(n, rows, cols, int(group), _p(codes), _p(scales), _p(dst),
-                                                        _stream(stream)))
+    _check("moe_dequantize_w4", lib().moe_dequantize_w4(n, rows, cols, int(group), *ptrs, _stream(stream)))
 
 
 def moe_w4_workspace_size(cfg) -> int:
@@ -380,7 +379,7 @@ def _w4_experts(wq) -> MoEW4Experts:
 
 def moe_grouped_ffn_w4(cfg, x_perm, offsets, wq, task_w, perm, y_perm, ws, stream=None):
     """wq: a dict of device tensors as quantize_experts_w4 returns (kept alive by the caller)."""
-    _operands("moe_grouped_ffn_w4", x_perm, offsets, task_w, perm, y_perm, ws, *_w4_tensors(wq))
+    _pointers("moe_grouped_ffn_w4", x_perm, offsets, task_w, perm, y_perm, ws, *_w4_tensors(wq))
     st = _w4_experts(wq)
     _check("moe_grouped_ffn_w4", lib().moe_grouped_ffn_w4(ctypes.byref(cfg), _p(x_perm), _p(offsets),
                                                           ctypes.byref(st), _p(task_w), _p(perm), _p(y_perm), _p(ws),
@@ -390,7 +389,7 @@ def moe_grouped_ffn_w4(cfg, x_perm, offsets, wq, task_w, perm, y_perm, ws, strea
 def moe_layer_forward_w4(cfg, x, w_router, bias, wq, out, ws, logits_out=None, topk_idx_out=None, topk_w_out=None,
                          counts_out=None, lis_out=None, stream=None):
     """wq: a dict of device tensors as quantize_experts_w4 returns (kept alive by the caller)."""
-    _operands("moe_layer_forward_w4", x, w_router, bias, out, ws, logits_out, topk_idx_out, topk_w_out, counts_out,
+    _pointers("moe_layer_forward_w4", x, w_router, bias, out, ws, logits_out, topk_idx_out, topk_w_out, counts_out,
               lis_out, *_w4_tensors(wq))
     st = _w4_experts(wq)
     _check("moe_layer_forward_w4", lib().moe_layer_forward_w4(
