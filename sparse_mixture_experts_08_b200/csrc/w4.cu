@@ -140,11 +140,14 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 // bits 0x4180 and the code at mantissa bit 3 is 16 + code, and (16 + code) s - 24 s is
 // rounded once. This needs 24 s to be a bf16 number: w4_scale_is_short says that s has at
 // most 6 significant bits (the quantizer's have 5) and is not so large that 24 s overflows.
+// (The lowest pair needs no shift the other way: two products on the FMA pipe for a shift
+// on the ALU pipe, which the unpacking loads more.)
 __device__ __forceinline__ uint32_t w4_pair_scaled(uint32_t w, int e, uint32_t ss, uint32_t ms) {
+  if (e == 0) return mul_bf16x2(w4_pair(w), ss);
   uint32_t r;
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;"
       : "=r"(r)
-      : "r"(e == 0 ? w << 3 : w >> (4 * e - 3)), "r"(0x00780078u), "r"(0x41804180u));  // (w & a) | b
+      : "r"(w >> (4 * e - 3)), "r"(0x00780078u), "r"(0x41804180u));  // (w & a) | b
   uint32_t d;
   asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(r), "r"(ss), "r"(ms));
   return d;
@@ -231,9 +234,8 @@ __global__ void __launch_bounds__(QW_WARPS * 32)
 // commit 46, and some hundred a turn of a long loop), so it commits once a chunk.
 // Barriers of a stage of the ring: codes (local) -> expanders; input rows (PAIR: of both
 // CTAs, at the leader) -> issuer; expanded (PAIR: at the leader) -> issuer; free: the
-// issuer's commit. A slot in tensor memory is free once an earlier chunk is done, which
-// that chunk's stage barrier tells (no more than STAGES chunks earlier: the barrier cannot
-// be a phase further yet). Every wait is bounded in time as in tc_gemm.cu.
+// issuer's commit. A slot in tensor memory is free once the chunk A_SLOTS before is done,
+// which that chunk's stage barrier tells. Every wait is bounded in time as in tc_gemm.cu.
 constexpr int WT_EXPAND_WARP = 4;
 constexpr int WT_MAX_GROUPS = 1040;
 constexpr unsigned long long WT_DRAIN_LIMIT_NS = 200ull * 1000 * 1000;
@@ -244,7 +246,7 @@ struct WtShape {
   static constexpr int PHASES = PAIR ? 1 : 2;          // both products in one launch (short segments)
   static constexpr int SMEM_BUDGET = (PHASES == 2 ? 180 : 196) * 1024;
   static constexpr int BK = PAIR ? 128 : 256;          // columns of K a stage
-  static constexpr int TEAMS = BN > 128 ? 2 : 3;    // teams of four expanding warps
+  static constexpr int TEAMS = BN > 128 || BN == 32 ? 2 : 3;    // teams of four expanding warps
   static constexpr int EW = BN > 128 ? 8 : 4;              // epilogue warps
   static constexpr int EPI_WARP = WT_EXPAND_WARP + 4 * TEAMS;
   static constexpr int THREADS = 32 * (EPI_WARP + EW);
@@ -268,7 +270,16 @@ struct WtShape {
   static constexpr int A_SLOTS = A_SLOTS_RAW > 6 ? 6 : A_SLOTS_RAW;
   static constexpr int DYN_SMEM = STAGES * STAGE_BYTES + 1024;
   static_assert(BN % 16 == 0 && BN >= 16 && BN <= 256 && HALF % 8 == 0, "tile");
-  static_assert(STAGE_BYTES % 1024 == 0 && A_SLOTS >= 2 && STAGES >= A_SLOTS, "ring");
+  static_assert(STAGE_BYTES % 1024 == 0 && A_SLOTS >= 2, "ring");
+  // A wait tells a barrier's phases apart by parity alone, so whoever waits for chunk n in
+  // a stage must know that chunk n - STAGES, the stage's last, has passed there. What is
+  // known: an issuer is done with its chunks in order, and a chunk was expanded when the
+  // chunk A_SLOTS before it was done. So a team at chunk n knows from its turn before that
+  // chunk m = n - TEAMS - A_SLOTS is done, with it m - A_SLOTS, and of one issuer all, of
+  // two every second chunk before those: any but m - 1. An issuer at chunk n knows its own
+  // earlier ones, and from its last that chunk n - ISSUERS - A_SLOTS is done.
+  static_assert(STAGES >= TEAMS + A_SLOTS && (ISSUERS == 1 || STAGES != TEAMS + A_SLOTS + 1), "expanders' phases");
+  static_assert(ISSUERS == 1 || (A_SLOTS == 3 && (STAGES % 2 == 0 || STAGES == 5)), "issuers' phases");
 };
 
 template <int PHASES>
@@ -930,6 +941,10 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
           for (int i = 0; i < BK / 32; ++i) {
             const int gi = (i * 32) >> gl2;
             if (EARLY) cw[i] = lds128(base + code_off + ((i ^ sw) << 4));
+            if (i > 0 && ((i * 32) & (p.group - 1))) {  // the same group as the granule before
+              sc[i] = sc[i > 0 ? i - 1 : 0];
+              continue;
+            }
             sc[i] = lds16(base + scale_off + gi * scale_pitch);
             if (ch * (BK >> gl2) + gi >= ng) sc[i] = 0u;  // behind K: x is zero there, the scale not this row's
             few = few && w4_scale_is_short(sc[i]);
