@@ -820,7 +820,11 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
     }
     // every issued copy lands before the CTA may exit (PAIR: the leader's barriers count
     // both CTAs' rows; the peer waits for the leader at the last cluster barrier): the
-    // last use of stage i was its fill number (used - 1 - i) / STAGES
+    // last use of stage i was its fill number (used - 1 - i) / STAGES. (Rows that the peer
+    // fetched for a stage which a leader that gave up never armed are on no barrier: the
+    // peer leaves them 5 ms.)
+    if (PAIR && !ok && !codes && !leader)
+      for (int i = 0; i < 50; ++i) __nanosleep(100000);
     if (lane == 0 && (codes || leader))
       for (int i = 0; i < STAGES && i < used; ++i) {
         const volatile int never = 0;

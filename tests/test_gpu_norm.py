@@ -198,3 +198,41 @@ def test_block_norm_then_8_bit_and_4_bit_layers():
     moe.moe_add_rmsnorm(out["w4"], stream, weight, 1e-5, nxt, sum_out=stream)
     s = (x.float() + res.float()).to(torch.bfloat16)
     assert torch.equal(stream, (out["w4"].float() + s.float()).to(torch.bfloat16))
+
+
+def test_codes_of_tiny_rows():
+    """Rows whose scale has no fp32 reciprocal: weights near the smallest normal number, and below it."""
+    d = 512
+    gen = torch.Generator().manual_seed(4)
+    x = torch.randn(5, d, generator=gen).cuda()
+    for size in (1e-30, 1e-36, 3e-38, 1e-39):
+        w = torch.full((d,), size, device="cuda")
+        y, codes, scales = torch.empty_like(x), torch.empty(5, d, dtype=torch.uint8, device="cuda"), torch.empty(5, device="cuda")
+        moe.moe_add_rmsnorm(x, None, w, 1e-6, y, codes=codes, scales=scales)
+        ref = norm64(x, None, w, 1e-6)
+        # below 2^-126 a number is off by up to 2^-150: y by one such rounding, and so the
+        # scale, which then is off by that much of its own size
+        step = 2.0 ** -150
+        assert ((y.to(F64) - ref).abs() <= (2.0 ** -24 + fp32_part(d)) * ref.abs() + 2 * step).all()
+        want = ref.abs().amax(1) / 448
+        rel = fp32_part(d) + 2.0 ** -22
+        assert ((scales.to(F64) - want).abs() <= rel * want + 2 * step).all()
+        val = codes.view(torch.float8_e4m3fn).to(F64) * scales.to(F64)[:, None]
+        off = 2 * step / want[:, None]  # the scale's own relative error
+        half = torch.maximum(2.0 ** -4 * ref.abs(), 2.0 ** -10 * want[:, None]) * (1 + 2.0 ** -10)
+        assert ((val - ref).abs() <= half + (rel + 2 * off) * ref.abs() + 2 * step).all()
+
+
+def test_no_rows():
+    x = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    moe.moe_add_rmsnorm(x, None, w, 1e-6, torch.empty_like(x))
+
+
+def test_binding_refuses_strided_and_host_tensors():
+    x = torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    wide = torch.zeros(4, 128, dtype=torch.bfloat16, device="cuda")
+    for a in ((wide[:, ::2], None, w, x), (x, wide[:, :64], w, x), (x, None, w.cpu(), x), (x.cpu(), None, w, x)):
+        with pytest.raises(moe.MoEError):
+            moe.moe_add_rmsnorm(a[0], a[1], a[2], 1e-6, a[3])

@@ -170,6 +170,21 @@ GROUPED = [
     ([0, 0, 19], 96, 2080, 128, moe.RELU),
     ([300, 1, 0, 513], 224, 352, 64, moe.RELU),
     ([129, 128, 127, 256], 1056, 544, 128, moe.SWIGLU),
+    # segments around 12 rows (tiles of 32), K that ends inside 64 and inside 256 columns
+    ([13, 30, 0, 9, 17, 3, 1, 24], 352, 1120, 32, moe.SWIGLU),
+    ([32, 31, 33, 1], 1056, 96, 64, moe.RELU),
+    # few long tiles, each cut between many blocks; both products in one launch
+    ([3], 4096, 6176, 128, moe.SWIGLU),
+    ([1, 1], 14336, 64, 64, moe.RELU),
+    # around 50, 80 and 400 rows (tiles of 64, 128 and 192 over two blocks), rows of weights
+    # that end inside a pair's tile, one tile of the second block empty
+    ([50, 49, 64, 0, 20], 640, 1376, 32, moe.SWIGLU),
+    ([81, 64, 192, 0, 1], 1376, 544, 64, moe.RELU),
+    ([400, 17, 385, 193], 288, 1312, 32, moe.SWIGLU),
+    ([577], 2080, 160, 128, moe.SWIGLU),
+    # more groups than a warp has lanes
+    ([(7 * i) % 5 for i in range(150)], 64, 96, 32, moe.SWIGLU),
+    ([(11 * i) % 190 for i in range(40)], 96, 160, 64, moe.RELU),
 ]
 
 
@@ -318,6 +333,10 @@ LAYERS = [
     (2048, 128, 160, 16, 4, 0, 0, 64, moe.SWIGLU, False),
     (8300, 64, 96, 8, 2, 1, 64, 32, moe.SWIGLU, True),
     (33, 128, 128, 700, 8, 0, 0, 128, moe.SWIGLU, False),
+    # 512 tasks and 513: the last batch whose dispatch is one launch, the first with three
+    (64, 96, 64, 24, 8, 0, 0, 32, moe.SWIGLU, True),
+    (57, 96, 64, 24, 9, 1, 32, 32, moe.RELU, False),
+    (3, 2080, 1376, 6, 2, 1, 1376, 64, moe.SWIGLU, True),
 ]
 
 
@@ -415,3 +434,103 @@ def test_fp8_refuses_and_w4_accepts_the_same_widths():
     assert moe.moe_w4_workspace_size(ok) > 0
     with pytest.raises(moe.MoEError):
         moe.moe_w4_workspace_size(moe.make_config(4, 48, 160, 3, 1))
+
+
+def _outputs(case, ws, seed=0):
+    c, wq, _, x, wr, bias, _ = _layer_case(case, seed)
+    return lambda: run_layer(c, x, wr, bias, wq, ws=ws)["out"]
+
+
+def test_one_workspace_for_batches_of_all_sizes():
+    """A server allocates for its largest batch: batches that take both products in one launch, in two, cut tiles
+    and whole ones, in turn on the same memory, give what each gives on a workspace of its own."""
+    cases = [(T, 288, 2080, 8, 2, 1, 160, 32, moe.SWIGLU, True) for T in (1, 700, 16, 90, 33, 2, 1500, 5)]
+    big = max((_layer_case(case)[0] for case in cases), key=moe.moe_w4_workspace_size)
+    shared = moe.w4_workspace(big)
+    calls = [(_outputs(case, shared), _outputs(case, None)()) for case in cases]
+    for _ in range(3):
+        for call, want in calls:
+            assert torch.equal(call(), want)
+    assert moe.moe_read_device_status(shared) == moe.OK
+
+
+@pytest.mark.parametrize("T", [2, 28, 60, 200, 640])
+def test_many_calls_give_the_same_bits(T):
+    """Sums that are cut between blocks are joined by whichever block is last: the order of the additions is fixed."""
+    c, wq, _, x, wr, bias, _ = _layer_case((T, 512, 4128, 4, 2, 0, 0, 64, moe.SWIGLU, False))
+    ws, want, out = moe.w4_workspace(c), torch.empty_like(x), torch.empty_like(x)
+    moe.moe_layer_forward_w4(c, x, wr, bias, wq, want, ws)
+    for _ in range(100):
+        moe.moe_layer_forward_w4(c, x, wr, bias, wq, out, ws)
+        assert torch.equal(out, want)
+    assert moe.moe_read_device_status(ws) == moe.OK
+
+
+@pytest.mark.parametrize("T", [4, 30, 70, 300, 900])
+def test_waits_that_run_out_are_reported_and_the_next_call_is_right(T):
+    """With a time limit of 1 ns the kernels give up at a wait that outlasts one poll of its barrier and return; the
+    workspace works again afterwards (the counters of cut tiles do not keep what the broken call left). A poll blocks
+    for a while by itself, so a call whose waits are all shorter than that completes, and must be right then."""
+    case = (T, 256, 1120, 4, 2, 1, 96, 64, moe.SWIGLU, True)
+    c, wq, _, x, wr, bias, _ = _layer_case(case)
+    ws = moe.w4_workspace(c)
+    want = run_layer(c, x, wr, bias, wq, ws=ws)["out"]
+    try:
+        moe.moe_debug_set_wait_limit_ns(1)
+        got = run_layer(c, x, wr, bias, wq, ws=ws)["out"]
+        status = moe.moe_read_device_status(ws)  # synchronises: the kernels returned
+    finally:
+        moe.moe_debug_set_wait_limit_ns(0)
+    assert status == moe.ERR_TIMEOUT or (status == moe.OK and torch.equal(got, want))
+    for _ in range(3):
+        assert torch.equal(run_layer(c, x, wr, bias, wq, ws=ws)["out"], want)
+    assert moe.moe_read_device_status(ws) == moe.OK
+
+
+def test_two_graphs_in_turn_on_one_workspace():
+    """A prompt's graph and a decode step's graph replayed in turn, as a server does, with one workspace."""
+    cases = [(T, 256, 1408, 8, 2, 1, 352, 64, moe.SWIGLU, True) for T in (300, 8)]
+    parts = [_layer_case(case) for case in cases]
+    ws = moe.w4_workspace(parts[0][0])
+    graphs = []
+    for c, wq, _, x, wr, bias, _ in parts:
+        want = run_layer(c, x, wr, bias, wq)["out"]
+        out, graph = torch.empty_like(x), torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            moe.moe_layer_forward_w4(c, x, wr, bias, wq, out, ws)
+        graphs.append((graph, out, want))
+    for i in (0, 1, 1, 0, 1, 0, 0):
+        graph, out, want = graphs[i]
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
+def test_all_tokens_on_one_expert():
+    """Routing that leaves all experts but one empty."""
+    c, wq, val, x, wr, _, act = _layer_case((48, 160, 224, 6, 1, 0, 0, 32, moe.SWIGLU, True))
+    bias = torch.tensor([0.0, 0, 1e4, 0, 0, 0], device="cuda")
+    r = run_layer(c, x, wr, bias, wq)
+    assert (r["idx"] == 2).all() and r["counts"].tolist() == [0, 0, 48, 0, 0, 0]
+    ref, bound = layer_ref(x, r["idx"], r["w"], val, c, act)
+    check(r["out"], ref, bound)
+
+
+def test_binding_refuses_strided_and_host_tensors():
+    c, wq, _, x, wr, bias, _ = _layer_case(LAYERS[0])
+    ws, out = moe.w4_workspace(c), torch.empty_like(x)
+    wide = torch.empty(c.T, 2 * c.d, dtype=torch.bfloat16, device="cuda")
+    for bad in (dict(x=wide[:, ::2]), dict(x=x.cpu()), dict(out=wide[:, ::2]), dict(wr=wr.cpu()),
+                dict(wq=dict(wq, up=wq["up"].cpu())), dict(wq=dict(wq, gate=wq["gate"].transpose(1, 2)))):
+        a = dict(dict(x=x, wr=wr, wq=wq, out=out), **bad)
+        with pytest.raises(moe.MoEError):
+            moe.moe_layer_forward_w4(c, a["x"], a["wr"], bias, a["wq"], a["out"], ws)
+    v = torch.zeros(8, 64, dtype=torch.bfloat16, device="cuda")
+    codes = torch.empty(8, 32, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(2, 8, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(moe.MoEError):
+        moe.moe_quantize_w4(v.t(), 32, codes, scales)
+    with pytest.raises(moe.MoEError):
+        moe.moe_dequantize_w4(codes, scales.cpu(), 32, v)
