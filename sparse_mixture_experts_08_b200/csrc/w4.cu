@@ -244,9 +244,9 @@ template <int BN>
 struct WtShape {
   static constexpr bool PAIR = BN >= 64;
   static constexpr int PHASES = PAIR ? 1 : 2;          // both products in one launch (short segments)
-  static constexpr int SMEM_BUDGET = (PHASES == 2 ? 180 : 196) * 1024;
-  static constexpr int BK = PAIR ? 128 : 256;          // columns of K a stage
-  static constexpr int TEAMS = BN > 128 || BN == 32 ? 2 : 3;    // teams of four expanding warps
+  static constexpr int SMEM_BUDGET = (PHASES == 2 ? 180 : BN == 64 ? 190 : 196) * 1024;
+  static constexpr int BK = BN > 64 ? 128 : 256;       // columns of K a stage
+  static constexpr int TEAMS = BN > 128 || BN == 32 || BN == 64 ? 2 : 3;    // teams of four expanding warps
   static constexpr int EW = BN > 128 ? 8 : 4;              // epilogue warps
   static constexpr int EPI_WARP = WT_EXPAND_WARP + 4 * TEAMS;
   static constexpr int THREADS = 32 * (EPI_WARP + EW);
@@ -262,12 +262,14 @@ struct WtShape {
   // Issuers: short segments have two (in warps 1 and 3) that take alternate chunks, each
   // with a sum of its own, since one's instruction stream would set the pace.
   static constexpr int ISSUERS = PAIR ? 1 : 2;
-  static constexpr int NUM_ACC = 2, ACC_COLS = ISSUERS * BN;
+  // Two sums in tensor memory, so that a tile's epilogue runs beside the next tile's
+  // products; one for the tallest tiles, whose long K hides it (w4_deep).
+  static constexpr int NUM_ACC = BN > 192 ? 1 : 2, ACC_COLS = ISSUERS * BN;
   // Expanded weights in tensor memory: a ring of slots of a chunk (two bf16 a column). A
   // slot is free once the chunk A_SLOTS before is done.
   static constexpr int A_COLS = BK / 2;
   static constexpr int A_SLOTS_RAW = (512 - NUM_ACC * ACC_COLS) / A_COLS;
-  static constexpr int A_SLOTS = A_SLOTS_RAW > 6 ? 6 : A_SLOTS_RAW;
+  static constexpr int A_SLOTS = A_SLOTS_RAW > STAGES - TEAMS ? STAGES - TEAMS : A_SLOTS_RAW;
   static constexpr int DYN_SMEM = STAGES * STAGE_BYTES + 1024;
   static_assert(BN % 16 == 0 && BN >= 16 && BN <= 256 && HALF % 8 == 0, "tile");
   static_assert(STAGE_BYTES % 1024 == 0 && A_SLOTS >= 2, "ring");
@@ -1304,9 +1306,19 @@ int w4_pick_bn(long long T, double avg_rows) {
 
 bool w4_both_products(int bn) { return bn <= 32; }
 
-size_t w4_partial_bytes(int bn) { return w4_partial_floats(bn) * sizeof(float) * (w4_both_products(bn) ? 2 : 1); }
+// Long segments' tiles: 224 rows with one sum in tensor memory where every tile runs over
+// at least 32 chunks of K, 192 rows with two otherwise (8 experts of 4096 x 14336, 4096
+// tokens: up 1350 -> 1279 us, down 697 -> 671; at K = 1408 down 103 -> 126, so not there).
+static bool w4_deep(const W4Params& p) {
+  for (int i = 0; i < p.n_classes; ++i)
+    if (p.cls[i].K < 4096) return false;
+  return true;
+}
+
+size_t w4_partial_bytes(int bn) { return w4_partial_floats(bn == 192 ? 224 : bn) * sizeof(float) * (w4_both_products(bn) ? 2 : 1); }
 
 cudaError_t launch_w4_gemm(int epi, int bn, const W4Params& p, cudaStream_t s) {
+  if (bn == 192 && w4_deep(p)) bn = 224;
 #define MOE_W4_CASE(BN_)                                                  \
   if (bn == BN_) {                                                        \
     static_assert(WtShape<BN_>::PHASES == (BN_ <= 32 ? 2 : 1), "phases"); \
@@ -1318,10 +1330,12 @@ cudaError_t launch_w4_gemm(int epi, int bn, const W4Params& p, cudaStream_t s) {
   MOE_W4_CASE(64)
   MOE_W4_CASE(128)
   MOE_W4_CASE(192)
+  MOE_W4_CASE(224)
 #undef MOE_W4_CASE
   if (epi == EPI_DOWN && bn == 64) return launch_impl<64, EPI_DOWN>(p, s);
   if (epi == EPI_DOWN && bn == 128) return launch_impl<128, EPI_DOWN>(p, s);
   if (epi == EPI_DOWN && bn == 192) return launch_impl<192, EPI_DOWN>(p, s);
+  if (epi == EPI_DOWN && bn == 224) return launch_impl<224, EPI_DOWN>(p, s);
   return cudaErrorInvalidValue;
 }
 

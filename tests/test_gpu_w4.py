@@ -182,6 +182,10 @@ GROUPED = [
     ([81, 64, 192, 0, 1], 1376, 544, 64, moe.RELU),
     ([400, 17, 385, 193], 288, 1312, 32, moe.SWIGLU),
     ([577], 2080, 160, 128, moe.SWIGLU),
+    # tiles of 224 rows, for the first product, the second and both
+    ([450, 0, 224, 225, 1, 700], 4096, 160, 128, moe.SWIGLU),
+    ([230, 449], 96, 4128, 32, moe.RELU),
+    ([800], 4160, 4096, 64, moe.SWIGLU),
     # more groups than a warp has lanes
     ([(7 * i) % 5 for i in range(150)], 64, 96, 32, moe.SWIGLU),
     ([(11 * i) % 190 for i in range(40)], 96, 160, 64, moe.RELU),
