@@ -861,13 +861,13 @@ cudaError_t launch_permute_rows(int dtype, int Tk, int k, int d, const void* x, 
 }
 
 // ------------------------------------------------ the whole dispatch of a small batch
-// route_index, rank and permute_rows in one launch, for batches whose tables are a few
-// hundred entries: what those launches cost there is their latency (three of them 15 us,
+// route_index, rank and permute_rows in one launch, for batches of at most a thousand
+// tasks: what those launches cost there is their latency (three of them 15 us,
 // this one 5, at 16 tokens). Every block builds the tables for itself from the ids and
 // copies its share of the rows; block 0 writes the tables. The order is the stable
 // counting sort's: task q goes to offsets[e] + the number of earlier tasks of expert e.
 // Any id outside [0, m) sets MOE_ERR_DEVICE_INDEX and nothing else is written.
-constexpr int SD_THREADS = 256, SD_MAX_TASKS = 512;
+constexpr int SD_THREADS = 256, SD_MAX_TASKS = 1024;
 __global__ void __launch_bounds__(SD_THREADS)
     small_dispatch_kernel(int T, int k, int m, int chunks, int parts, const int32_t* __restrict__ idx,
                           const float* __restrict__ task_w, const uint4* __restrict__ x, int32_t* __restrict__ counts,

@@ -337,9 +337,12 @@ LAYERS = [
     (2048, 128, 160, 16, 4, 0, 0, 64, moe.SWIGLU, False),
     (8300, 64, 96, 8, 2, 1, 64, 32, moe.SWIGLU, True),
     (33, 128, 128, 700, 8, 0, 0, 128, moe.SWIGLU, False),
-    # 512 tasks and 513: the last batch whose dispatch is one launch, the first with three
     (64, 96, 64, 24, 8, 0, 0, 32, moe.SWIGLU, True),
     (57, 96, 64, 24, 9, 1, 32, 32, moe.RELU, False),
+    # 1024 tasks and 1026: the last batch whose dispatch is one launch, the first with three
+    (128, 96, 64, 24, 8, 0, 0, 32, moe.SWIGLU, True),
+    (114, 96, 64, 24, 9, 1, 32, 32, moe.RELU, False),
+    (1, 64, 64, 1024, 32, 0, 0, 32, moe.SWIGLU, True),
     (3, 2080, 1376, 6, 2, 1, 1376, 64, moe.SWIGLU, True),
 ]
 
