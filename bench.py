@@ -81,6 +81,9 @@ def parse():
     ap.add_argument("--fp8", action="store_true",
                     help="8-bit experts: E4M3 weights with per-channel scales (quantized once, untimed), "
                          "moe_layer_forward_fp8")
+    ap.add_argument("--w4", type=int, nargs="?", const=128, default=None, metavar="GROUP",
+                    help="4-bit experts: codes with one bf16 scale a group of GROUP (128) weights (quantized once, "
+                         "untimed), moe_layer_forward_w4")
     ap.add_argument("--global-lis", action="store_true",
                     help="every step also sums the per-expert counts over all ranks (NCCL all-reduce of m int32) "
                          "and takes the Load Imbalance Score of the whole job's batch (moe_lis_from_counts); "
@@ -511,6 +514,9 @@ def layer_run(cfg, args, dev, rank: int, world: int, dist, steps, warmup: int, w
     fp8 = args.fp8
     if rep and cfg.dtype != W.BF16:
         raise SystemExit("--replicate runs bf16 layers only")
+    w4 = args.w4
+    if w4 is not None and (rep or floe is not None or fp8 or cfg.dtype != W.BF16):
+        raise SystemExit("--w4 runs plain bf16 layers (no --replicate / --floe / --fp8)")
     if fp8 and (rep or floe is not None or cfg.dtype != W.BF16):
         raise SystemExit("--fp8 runs plain bf16 layers (no --replicate / --floe)")
     if floe is not None and (cfg.dtype != W.BF16 or cfg.act != W.SWIGLU or cfg.n_shared):
@@ -519,11 +525,13 @@ def layer_run(cfg, args, dev, rank: int, world: int, dist, steps, warmup: int, w
         ws = moe.replica_workspace(c, device=dev)
     elif floe is not None:
         ws = moe.floe_workspace(c, device=dev)
-    elif fp8:
-        ws = moe.fp8_workspace(c, device=dev)
-        # one-time E4M3 weights (untimed), then the bf16 copies are dropped
-        wq = moe.quantize_experts(d_in["w_gate"], d_in.get("w_up"), d_in["w_down"], d_in.get("ws_gate"),
-                                  d_in.get("ws_up"), d_in.get("ws_down"))
+    elif fp8 or w4 is not None:
+        ws = moe.fp8_workspace(c, device=dev) if fp8 else moe.w4_workspace(c, device=dev)
+        # one-time E4M3 or 4-bit weights (untimed), then the bf16 copies are dropped
+        bf16_weights = (d_in["w_gate"], d_in.get("w_up"), d_in["w_down"], d_in.get("ws_gate"), d_in.get("ws_up"),
+                        d_in.get("ws_down"))
+        wq = moe.quantize_experts(*bf16_weights) if fp8 else moe.quantize_experts_w4(*bf16_weights, group=w4)
+        del bf16_weights
         for key in ("w_gate", "w_up", "w_down", "ws_gate", "ws_up", "ws_down"):
             d_in.pop(key, None)
         torch.cuda.synchronize(dev)
@@ -549,7 +557,7 @@ def layer_run(cfg, args, dev, rank: int, world: int, dist, steps, warmup: int, w
     lis = moe.lis_buffer(dev)
     lis0 = moe.lis_buffer(dev)
     glob = args.global_lis
-    if glob and (rep or floe is not None or fp8):
+    if glob and (rep or floe is not None or fp8 or w4 is not None):
         raise SystemExit("--global-lis runs the plain layer")
     gcounts = torch.empty(cfg.m, dtype=torch.int32, device=dev)
     glis = moe.lis_buffer(dev)
@@ -560,6 +568,10 @@ def layer_run(cfg, args, dev, rank: int, world: int, dist, steps, warmup: int, w
         if fp8:
             moe.moe_layer_forward_fp8(c, d_in["x"] if x is None else x, d_in["w_router"], d_in["bias"], wq,
                                       out if o is None else o, ws, counts_out=counts, lis_out=lis, stream=s)
+            return
+        if w4 is not None:
+            moe.moe_layer_forward_w4(c, d_in["x"] if x is None else x, d_in["w_router"], d_in["bias"], wq,
+                                     out if o is None else o, ws, counts_out=counts, lis_out=lis, stream=s)
             return
         args_ = (c, d_in["x"] if x is None else x, d_in["w_router"], d_in["bias"], d_in["w_gate"], d_in.get("w_up"),
                  d_in["w_down"], d_in.get("ws_gate"), d_in.get("ws_up"), d_in.get("ws_down"),
@@ -690,9 +702,14 @@ def layer_run(cfg, args, dev, rank: int, world: int, dist, steps, warmup: int, w
                "d2h": out_hosts[0].numel() * out_hosts[0].element_size()}
 
     cfg_groups = dataclasses.replace(cfg, m=cfg.m + 1) if rep else cfg  # the replica is one more routed group
-    plan_ksplit = _down_ksplit(cfg, cfg_groups, fp8)
-    costs, layer_flops, layer_bytes = stage_costs(cfg_groups, active, plan_ksplit, weight_bytes=1 if fp8 else None)
+    plan_ksplit = 1 if w4 is not None else _down_ksplit(cfg, cfg_groups, fp8)
+    costs, layer_flops, layer_bytes = stage_costs(
+        cfg_groups, active, plan_ksplit, weight_bytes=1 if fp8 else 0.5 + 2.0 / w4 if w4 is not None else None)
     extra = {}
+    if w4 is not None and min(cfg.T, 2.0 * cfg.T * cfg.k / cfg.m) <= 32:
+        # short segments: one launch does both products, timed as the up stage
+        costs["expert_up"] = tuple(a + b for a, b in zip(costs["expert_up"], costs["expert_down"]))
+        extra["stages_joined"] = "expert_up covers both products (one launch)"
     if floe is not None:
         # dense up projection: W_up only, u written in fp32; sparse part: the gate and
         # down rows of the kept channels, u and the compact h
@@ -755,7 +772,8 @@ def ours(args):
 
     cfg = W.CONFIGS[args.config]
     rep, floe, fp8 = args.replicate, args.floe, args.fp8
-    variant = rep or floe is not None or fp8
+    w4 = args.w4
+    variant = rep or floe is not None or fp8 or w4 is not None
     r = layer_run(cfg, args, dev, rank, world, dist, args.steps, args.warmup, with_e2e=True,
                   sustained_ms=SUSTAINED_MS if (world == 1 and not variant and not args.no_extra) else 0.0)
     # ---- max over ranks
@@ -766,7 +784,7 @@ def ours(args):
     fl, by = r["costs"][r["dom"]]
     roof = roofline_for(cfg, r["dom"], fl, by, r["dom_ms"], pk, pk_src, long_step, fp8,
                         cfg.name + ("_fp8" if fp8 else "") + ("_floe" if floe is not None else "")
-                        + ("_replicated" if rep else ""))
+                        + ("_replicated" if rep else "") + ("_w4" if w4 is not None else ""))
     tensor_peak = (pk["bf16_tflops_sustained"] if long_step else pk["bf16_tflops"]) * (2.0 if fp8 else 1.0)
     t_layer = max(r["layer_flops"] / (tensor_peak * 1e12), r["layer_bytes"] / (pk["hbm_gbs"] * 1e9))
     variant_note = {}
@@ -779,6 +797,9 @@ def ours(args):
                                    "once, outside the timing); x and h rows quantized per row inside each step; router "
                                    "in bf16",
                         "dtype_note": "expert GEMMs e4m3 x e4m3 with fp32 accumulation; router bf16"}
+    elif w4 is not None:
+        variant_note = {"variant": f"4-bit experts: codes with one bf16 scale a group of {w4} weights (quantized once, "
+                                   "outside the timing); activations, their products and the router in bf16"}
     elif rep:
         variant_note = {"variant": "R&Q replica dispatch: the heavy-hitter's tasks alternate between it and a replica "
                                    "expert m that computes with its bf16 weights; routing.lis is over the m + 1 experts"}
@@ -787,7 +808,8 @@ def ours(args):
             "vs_baseline": None, "dtype": "e4m3" if fp8 else "bf16" if cfg.dtype == W.BF16 else "f32",
             "data": "synthetic (seeded generator; x ~ N(0,1), weights ~ N(0, 1/sqrt(fan_in)), Zipf router bias)",
             "config": dict(run_config(cfg, world),
-                           **({"expert_weights": "e4m3, per-channel fp32 scales"} if fp8 else {})),
+                           **({"expert_weights": "e4m3, per-channel fp32 scales"} if fp8 else
+                              {"expert_weights": f"4-bit, bf16 scale a group of {w4}"} if w4 is not None else {})),
             "roofline": roof,
             "layer_roofline": {"time_us": t_layer * 1e6, "frac": t_layer / (ms * 1e-3),
                                "flops": r["layer_flops"], "bytes": r["layer_bytes"]},
