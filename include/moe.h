@@ -348,7 +348,8 @@ MOE_API moe_status_t moe_layer_forward_fp8_codes(const moe_config_t* cfg, const 
  *   sum_out (nullable) = r, y (nullable) = y, both rounded to `dtype`;
  *   codes, scales (nullable, both or neither) = E4M3 codes [rows, d] and fp32 scales
  *   [rows] of y in moe_quantize_e4m3's format, taken from the fp32 y (not from its
- *   rounding to bf16). r and y are fp32 in between.
+ *   rounding to bf16; y / scale is y times the scale's fp32 reciprocal). r and y are fp32
+ *   in between.
  * x, residual, sum_out, y [rows, d] and weight [d] are `dtype` (moe_dtype_t), contiguous
  * and 16-byte aligned; scales 4-byte aligned. sum_out and y may be x or residual
  * themselves (not each other, and no partial overlap). At least one of y and codes is
@@ -406,13 +407,18 @@ typedef struct {
   const void* sh_down_scale;
 } moe_w4_experts_t;
 
-/* Workspace of moe_grouped_ffn_w4 and moe_layer_forward_w4 (host out-parameter). bf16
- * layers with d, f and f_shared multiples of 32 only (MOE_ERR_UNSUPPORTED otherwise). */
+/* Workspace of moe_grouped_ffn_w4 and moe_layer_forward_w4 (host out-parameter), zeroed
+ * once before its first use like every workspace. One workspace serves calls of all
+ * batch sizes it is large enough for, one after the other; calls that overlap on the GPU
+ * need one each. bf16 layers with d, f and f_shared multiples of 32 up to 2^23 and fewer
+ * than 2^31 rows in a stack of matrices only (MOE_ERR_UNSUPPORTED otherwise). */
 MOE_API moe_status_t moe_w4_workspace_size(const moe_config_t* cfg, size_t* bytes);
 
 /* moe_grouped_ffn with 4-bit experts: same segments, task weights and fp32 y_perm; only
  * the routed matrices of wq are read. Activations stay bf16 (the hidden activation h is
- * rounded to bf16 between the two products), sums are fp32. */
+ * rounded to bf16 between the two products), sums are fp32 in an order that depends on
+ * the sizes alone, so the same call gives the same bits. A weight is code * scale rounded
+ * to bf16 (no rounding for moe_quantize_w4's scales). */
 MOE_API moe_status_t moe_grouped_ffn_w4(const moe_config_t* cfg, const void* x_perm, const int32_t* offsets,
                                         const moe_w4_experts_t* wq, const float* task_w, const int32_t* perm,
                                         float* y_perm, void* ws, size_t ws_bytes, moe_stream_t stream);
@@ -420,7 +426,9 @@ MOE_API moe_status_t moe_grouped_ffn_w4(const moe_config_t* cfg, const void* x_p
 /* moe_layer_forward with 4-bit experts, routed and shared. The router is the bf16
  * layer's (same logits, top-k and gate weights, same histogram, LIS and permutation).
  * Optional outputs as in moe_layer_forward. ws: moe_w4_workspace_size() bytes, 256-byte
- * aligned. Stage events (moe_set_stage_events) as in moe_layer_forward. */
+ * aligned. Stage events (moe_set_stage_events) as in moe_layer_forward; stages that one
+ * launch does coincide (up to 1024 tasks: histogram, ranks and permutation; short
+ * segments: both products, timed as the first). */
 MOE_API moe_status_t moe_layer_forward_w4(const moe_config_t* cfg, const void* x, const void* w_router,
                                           const float* bias, const moe_w4_experts_t* wq, void* out,
                                           float* logits_out, int32_t* topk_idx_out, float* topk_w_out,
