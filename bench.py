@@ -706,7 +706,7 @@ def layer_run(cfg, args, dev, rank: int, world: int, dist, steps, warmup: int, w
     costs, layer_flops, layer_bytes = stage_costs(
         cfg_groups, active, plan_ksplit, weight_bytes=1 if fp8 else 0.5 + 2.0 / w4 if w4 is not None else None)
     extra = {}
-    if w4 is not None and min(cfg.T, 2.0 * cfg.T * cfg.k / cfg.m) <= 32:
+    if w4 is not None and min(cfg.T, 2.0 * cfg.T * cfg.k / cfg.m) <= 64:
         # short segments: one launch does both products, timed as the up stage
         costs["expert_up"] = tuple(a + b for a, b in zip(costs["expert_up"], costs["expert_down"]))
         extra["stages_joined"] = "expert_up covers both products (one launch)"

@@ -116,7 +116,7 @@ static Layout make_layout(const moe_config_t& c, const Plan& p) {
   };
   const size_t Tk = (size_t)c.T * c.k;
   const size_t T = (size_t)c.T;
-  // the status word, then (in every layer's workspace alike) the grid count (offset 128)
+  // the status word, then (in every layer's workspace alike) the grid counts (offset 128)
   // and the counters (offset 256) of the 4-bit products
   L.status = take(256 + W4_COUNTER_WORDS * sizeof(unsigned));
   L.logits = take(T * c.m * 4);
@@ -325,10 +325,11 @@ static moe_status_t run_ffn_w4(const moe_config_t& c, const FfnIo& io, int* stat
   p.status = status;
   p.wait_limit_ns = g_wait_limit_ns;
   p.partial = io.w4_partial;
-  p.grid_count = reinterpret_cast<unsigned long long*>(status + 32);
   unsigned* const counters = reinterpret_cast<unsigned*>(status + 64);
   const int bn = w4_bn(c);
   const bool both = w4_both_products(bn);
+  const int kind = w4_grid_kind(bn);
+  p.grid_count = reinterpret_cast<unsigned long long*>(status + 32) + kind;
   for (int down = 0; down < 2; ++down) {
     W4Class* const cls = p.cls + (both && down ? 2 : 0);
     int n = 0;
@@ -367,7 +368,7 @@ static moe_status_t run_ffn_w4(const moe_config_t& c, const FfnIo& io, int* stat
     const int epi = down && !both ? EPI_DOWN : swiglu ? EPI_SWIGLU : EPI_RELU;
     if (both) {  // one launch (its stages coincide)
       if (down) {
-        p.counters = counters + 2 * W4_COUNTERS;
+        p.counters = counters + 2 * W4_COUNTERS + kind * 4 * W4_COUNTERS2;
         MOE_CUDA(launch_w4_gemm(epi, bn, p, s));
         if (stage_marks) MOE_TRY(mark_stage(5, s));
       }

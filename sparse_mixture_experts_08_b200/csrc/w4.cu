@@ -243,8 +243,8 @@ constexpr unsigned long long WT_DRAIN_LIMIT_NS = 200ull * 1000 * 1000;
 template <int BN>
 struct WtShape {
   static constexpr bool PAIR = BN >= 64;
-  static constexpr int PHASES = PAIR ? 1 : 2;          // both products in one launch (short segments)
-  static constexpr int SMEM_BUDGET = (PHASES == 2 ? 180 : BN == 64 ? 190 : 196) * 1024;
+  static constexpr int PHASES = BN <= 64 ? 2 : 1;      // both products in one launch
+  static constexpr int SMEM_BUDGET = (PHASES == 2 ? 180 : 196) * 1024;
   static constexpr int BK = BN > 64 ? 128 : 256;       // columns of K a stage
   static constexpr int TEAMS = BN > 128 || BN == 32 || BN == 64 ? 2 : 3;    // teams of four expanding warps
   static constexpr int EW = BN > 128 ? 8 : 4;              // epilogue warps
@@ -1256,17 +1256,21 @@ cudaError_t launch_impl(const W4Params& p, cudaStream_t s) {
   cfg.blockDim = dim3(S::THREADS);
   cfg.dynamicSmemBytes = S::DYN_SMEM;
   cfg.stream = s;
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[3];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  int attrs = 1;
   if (S::PAIR) {
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-  } else {
-    attr[1].id = cudaLaunchAttributeCooperative;
-    attr[1].val.cooperative = 1;
+    attr[attrs].id = cudaLaunchAttributeClusterDimension;
+    attr[attrs].val.clusterDim.x = 2;
+    attr[attrs].val.clusterDim.y = 1;
+    attr[attrs].val.clusterDim.z = 1;
+    ++attrs;
+  }
+  if (S::PHASES == 2) {
+    attr[attrs].id = cudaLaunchAttributeCooperative;
+    attr[attrs].val.cooperative = 1;
+    ++attrs;
   }
   static int walkers[64] = {0};  // a device: CTAs or pairs that can be resident at once
   int dev = 0;
@@ -1288,7 +1292,7 @@ cudaError_t launch_impl(const W4Params& p, cudaStream_t s) {
   }
   cfg.gridDim = dim3(walkers[dev] * (S::PAIR ? 2 : 1));
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = attrs;
   e = cudaLaunchKernelEx(&cfg, kern, maps, p);
   count_launch();
   return e;
@@ -1304,7 +1308,11 @@ int w4_pick_bn(long long T, double avg_rows) {
   return want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : std::min((double)T, avg_rows) <= 160 ? 128 : 192;
 }
 
-bool w4_both_products(int bn) { return bn <= 32; }
+// (at 64 rows 96 tokens on 8 experts of 4096 x 4096 ran 107 us in two launches, 102 in one;
+// at 128 rows 506 tokens on 8 of 4096 x 14336 ran 372 and 380.)
+bool w4_both_products(int bn) { return bn <= 64; }
+
+int w4_grid_kind(int bn) { return bn <= 32 ? 0 : 1; }
 
 // Long segments' tiles: 224 rows with one sum in tensor memory where every tile runs over
 // at least 32 chunks of K, 192 rows with two otherwise (8 experts of 4096 x 14336, 4096
@@ -1321,7 +1329,7 @@ cudaError_t launch_w4_gemm(int epi, int bn, const W4Params& p, cudaStream_t s) {
   if (bn == 192 && w4_deep(p)) bn = 224;
 #define MOE_W4_CASE(BN_)                                                  \
   if (bn == BN_) {                                                        \
-    static_assert(WtShape<BN_>::PHASES == (BN_ <= 32 ? 2 : 1), "phases"); \
+    static_assert(WtShape<BN_>::PHASES == (BN_ <= 64 ? 2 : 1), "phases"); \
     if (epi == EPI_SWIGLU) return launch_impl<BN_, EPI_SWIGLU>(p, s);     \
     if (epi == EPI_RELU) return launch_impl<BN_, EPI_RELU>(p, s);         \
   }
@@ -1332,7 +1340,6 @@ cudaError_t launch_w4_gemm(int epi, int bn, const W4Params& p, cudaStream_t s) {
   MOE_W4_CASE(192)
   MOE_W4_CASE(224)
 #undef MOE_W4_CASE
-  if (epi == EPI_DOWN && bn == 64) return launch_impl<64, EPI_DOWN>(p, s);
   if (epi == EPI_DOWN && bn == 128) return launch_impl<128, EPI_DOWN>(p, s);
   if (epi == EPI_DOWN && bn == 192) return launch_impl<192, EPI_DOWN>(p, s);
   if (epi == EPI_DOWN && bn == 224) return launch_impl<224, EPI_DOWN>(p, s);

@@ -40,8 +40,10 @@ constexpr int W4_MAX_CTAS = 160;              // CTAs of a launch
 constexpr int W4_COUNTERS = W4_MAX_CTAS * 8;  // one an epilogue warp: a product's cut tiles
 constexpr int W4_COUNTERS2 = W4_MAX_CTAS * 4; // the same where one launch does both products
 // Counter words of a workspace: two sets that the launches of the two products use in
-// turn, four for launches that do both (even and odd launches, first and second product).
-constexpr int W4_COUNTER_WORDS = 2 * W4_COUNTERS + 4 * W4_COUNTERS2;
+// turn; for launches that do both, four of each kind of grid (even and odd launches, first
+// and second product), as each kind counts its own launches.
+constexpr int W4_GRID_KINDS = 2;
+constexpr int W4_COUNTER_WORDS = 2 * W4_COUNTERS + W4_GRID_KINDS * 4 * W4_COUNTERS2;
 
 struct W4Params {
   W4Class cls[4];  // [product][routed, shared]; launches of one product use the first two
@@ -49,7 +51,7 @@ struct W4Params {
   int group;    // 32, 64 or 128
   float* partial;           // w4_partial_bytes(): sums of tiles that CTAs share
   // warps that have left their sums of a tile, zero before the launch
-  unsigned* counters;       // [W4_COUNTERS], or all four sets of W4_COUNTERS2
+  unsigned* counters;       // [W4_COUNTERS], or the four sets of W4_COUNTERS2 of this kind
   unsigned* counters_next;  // [W4_COUNTERS]: zeroed here, used by the next product
   unsigned long long* grid_count;  // both products: epilogue warps that have left the first
   int* status;
@@ -63,6 +65,7 @@ size_t w4_partial_bytes(int bn);
 // Whether tiles of bn rows take both products in one launch (epi: the first one's, cls all
 // four); otherwise a launch each.
 bool w4_both_products(int bn);
+int w4_grid_kind(int bn);  // and of which kind its grid is: one size on a device
 cudaError_t launch_w4_gemm(int epi, int bn, const W4Params& p, cudaStream_t s);
 cudaError_t launch_quantize_w4(long long n, int rows, int cols, int group, const void* src, uint8_t* codes,
                                void* scales, cudaStream_t s);

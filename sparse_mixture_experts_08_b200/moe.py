@@ -339,7 +339,7 @@ def moe_add_rmsnorm(x, residual, weight, eps, y, sum_out=None, codes=None, scale
     (uint8, like x) and scales [rows] (fp32): E4M3 codes of y, one scale a row. x is fp32 or bf16, contiguous."""
     ptrs = _pointers("moe_add_rmsnorm", x, residual, weight, sum_out, y, codes, scales)
     d = x.shape[-1]
-    _check("moe_add_rmsnorm", lib().moe_add_rmsnorm(x.numel() // d if d else 0, d, _DTYPES.get(x.dtype, -1), eps,
+    _check("moe_add_rmsnorm", lib().moe_add_rmsnorm(x.numel() // d if d else 0, d, _DTYPES.get(x.dtype, -1), float(eps),
                                                     *ptrs, _stream(stream)))
 
 

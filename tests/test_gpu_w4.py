@@ -186,6 +186,9 @@ GROUPED = [
     ([450, 0, 224, 225, 1, 700], 4096, 160, 128, moe.SWIGLU),
     ([230, 449], 96, 4128, 32, moe.RELU),
     ([800], 4160, 4096, 64, moe.SWIGLU),
+    # more than a hundred pieces of work a block or pair (those past the listed ones are worked out on the way)
+    ([12288], 64, 32768, 32, moe.RELU),
+    ([1] * 600, 32, 4096, 32, moe.RELU),
     # more groups than a warp has lanes
     ([(7 * i) % 5 for i in range(150)], 64, 96, 32, moe.SWIGLU),
     ([(11 * i) % 190 for i in range(40)], 96, 160, 64, moe.RELU),
