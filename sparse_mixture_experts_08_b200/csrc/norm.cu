@@ -161,7 +161,8 @@ __global__ void __launch_bounds__(MAX_THREADS)
     }
   if (codes) {
     amax = row_reduce<WIDE, true>(amax, red[1]);
-    float sc = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+    float sc = __fdiv_rn(amax, 448.f);
+    if (sc == 0.f) sc = 1.f;  // a row of zeros, or one whose scale would be below 2^-150: its codes are zeros
     if (t == 0) scales[row] = sc;
     if (sc < 0x1p-100f) {  // the reciprocal of a tiny scale would overflow
       sc *= 0x1p64f;

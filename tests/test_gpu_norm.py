@@ -223,6 +223,18 @@ def test_codes_of_tiny_rows():
         assert ((val - ref).abs() <= half + (rel + 2 * off) * ref.abs() + 2 * step).all()
 
 
+def test_codes_of_rows_too_small_for_a_scale():
+    """amax / 448 rounds to zero in fp32: scale 1 and codes of zero (of either sign), no NaN code."""
+    d = 512
+    gen = torch.Generator().manual_seed(5)
+    x = torch.randn(5, d, generator=gen).cuda()
+    x[:, :9] = 0
+    w = torch.full((d,), 1e-44, device="cuda")
+    codes, scales = torch.empty(5, d, dtype=torch.uint8, device="cuda"), torch.empty(5, device="cuda")
+    moe.moe_add_rmsnorm(x, None, w, 1e-6, None, codes=codes, scales=scales)
+    assert (scales == 1).all() and (codes & 0x7F == 0).all()
+
+
 def test_no_rows():
     x = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
     w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
