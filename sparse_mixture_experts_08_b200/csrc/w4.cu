@@ -38,7 +38,8 @@ __device__ __forceinline__ float scale_5bits(float amax) {
 // 2^-12 first (the addition of 1.5 2^11) gives the half-way number exactly or stays on its
 // side; the second addition rounds to whole numbers as the division would have.
 __device__ __forceinline__ uint32_t code_bits(float v, float r) {
-  return __float_as_uint(__fadd_rn(__fmaf_rn(v, r, 3072.f), 12582920.f - 3072.f));
+  constexpr float to_12 = 0x1.8p11f, to_0 = 0x1.8p23f + 8.f - to_12;
+  return __float_as_uint(__fadd_rn(__fmaf_rn(v, r, to_12), to_0));
 }
 
 __device__ __forceinline__ uint32_t abs_max_bf16x2(uint32_t a, uint32_t b) {
