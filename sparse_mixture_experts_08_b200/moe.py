@@ -142,11 +142,12 @@ def _p(t) -> Optional[int]:
 _DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
 
 
-def _pointers(fn: str, *tensors):
-    """The tensors' addresses. Refuses what the library cannot see: tensors that are not contiguous, or not all on
-    the current CUDA device."""
+def _pointers(fn: str, specs):
+    """The addresses of specs' tensors: (tensor, dtype, elements) each. Refuses what the library cannot see: tensors
+    that are not contiguous, not all on the current CUDA device, of another type, or with fewer elements than the call
+    reads or writes. None and addresses pass as they are; dtype None: any type."""
     dev, out = None, []
-    for t in tensors:
+    for t, dtype, n in specs:
         if t is None or t.__class__ is int:
             out.append(t)
             continue
@@ -155,7 +156,7 @@ def _pointers(fn: str, *tensors):
             if dev is not None or d < 0 or d != torch.cuda.current_device():
                 raise MoEError(fn, ERR_INVALID_ARG)
             dev = d
-        if not t.is_contiguous():
+        if (t.dtype is not dtype and dtype is not None) or t.numel() < n or not t.is_contiguous():
             raise MoEError(fn, ERR_INVALID_ARG)
         out.append(t.data_ptr())
     return out
@@ -326,7 +327,10 @@ def moe_layer_forward_fp8_codes(cfg, x, x_codes, x_scales, w_router, bias, wq, o
                                 topk_idx_out=None, topk_w_out=None, counts_out=None, lis_out=None, h_out=None,
                                 h_shared_out=None, perm_out=None, stream=None):
     """moe_layer_forward_fp8 for tokens that come with E4M3 codes [T, d] and scales [T] (moe_add_rmsnorm's)."""
-    _pointers("moe_layer_forward_fp8_codes", x, x_codes, x_scales, w_router, bias, out, ws)
+    n, bf16, f32 = cfg.T * cfg.d, torch.bfloat16, torch.float32
+    _pointers("moe_layer_forward_fp8_codes", (
+        (x, bf16, n), (x_codes, torch.uint8, n), (x_scales, f32, cfg.T), (w_router, bf16, cfg.m * cfg.d),
+        (bias, f32, cfg.m), (out, bf16, n), (ws, None, 0)))
     st = MoEFp8Experts(**{k: _p(wq.get(k)) for k, _ in MoEFp8Experts._fields_})
     _check("moe_layer_forward_fp8_codes", lib().moe_layer_forward_fp8_codes(
         ctypes.byref(cfg), _p(x), _p(x_codes), _p(x_scales), _p(w_router), _p(bias), ctypes.byref(st), _p(out),
@@ -337,10 +341,13 @@ def moe_layer_forward_fp8_codes(cfg, x, x_codes, x_scales, w_router, bias, wq, o
 def moe_add_rmsnorm(x, residual, weight, eps, y, sum_out=None, codes=None, scales=None, stream=None):
     """y [rows, d] = RMS norm of x + residual (residual may be None) times weight; sum_out: the sum; codes
     (uint8, like x) and scales [rows] (fp32): E4M3 codes of y, one scale a row. x is fp32 or bf16, contiguous."""
-    ptrs = _pointers("moe_add_rmsnorm", x, residual, weight, sum_out, y, codes, scales)
-    d = x.shape[-1]
-    _check("moe_add_rmsnorm", lib().moe_add_rmsnorm(x.numel() // d if d else 0, d, _DTYPES.get(x.dtype, -1), float(eps),
-                                                    *ptrs, _stream(stream)))
+    d, n, dtype = x.shape[-1], x.numel(), x.dtype
+    rows = n // d if d else 0
+    ptrs = _pointers("moe_add_rmsnorm", (
+        (x, dtype, n), (residual, dtype, n), (weight, dtype, d), (sum_out, dtype, n), (y, dtype, n),
+        (codes, torch.uint8, n), (scales, torch.float32, rows)))
+    _check("moe_add_rmsnorm", lib().moe_add_rmsnorm(rows, d, _DTYPES.get(dtype, -1), float(eps), *ptrs,
+                                                    _stream(stream)))
 
 
 def _w4_shape(t, cols):
@@ -349,20 +356,29 @@ def _w4_shape(t, cols):
     return (t.numel() // (rows * cols) if rows and cols else 0), rows
 
 
+def _w4_scales(n, rows, cols, group):
+    """Elements of a stack of matrices' scales (0 for a group that the library refuses)."""
+    return n * -(-cols // group) * rows if group > 0 else 0
+
+
 def moe_quantize_w4(src, group, codes, scales, stream=None):
     """4-bit codes [n, rows, cols / 2] (uint8) and bf16 scales [n, ceil(cols / group), rows] of bf16 matrices
     src [n, rows, cols] (or one matrix [rows, cols])."""
-    ptrs = _pointers("moe_quantize_w4", src, codes, scales)
     cols = int(src.shape[-1])
     n, rows = _w4_shape(src, cols)
+    ptrs = _pointers("moe_quantize_w4", (
+        (src, torch.bfloat16, src.numel()), (codes, torch.uint8, src.numel() // 2),
+        (scales, torch.bfloat16, _w4_scales(n, rows, cols, int(group)))))
     _check("moe_quantize_w4", lib().moe_quantize_w4(n, rows, cols, int(group), *ptrs, _stream(stream)))
 
 
 def moe_dequantize_w4(codes, scales, group, dst, stream=None):
     """The bf16 matrices dst [n, rows, cols] that codes and scales (as moe_quantize_w4 writes them) stand for."""
-    ptrs = _pointers("moe_dequantize_w4", codes, scales, dst)
     cols = int(dst.shape[-1])
     n, rows = _w4_shape(dst, cols)
+    ptrs = _pointers("moe_dequantize_w4", (
+        (codes, torch.uint8, dst.numel() // 2), (scales, torch.bfloat16, _w4_scales(n, rows, cols, int(group))),
+        (dst, torch.bfloat16, dst.numel())))
     _check("moe_dequantize_w4", lib().moe_dequantize_w4(n, rows, cols, int(group), *ptrs, _stream(stream)))
 
 
@@ -372,35 +388,40 @@ def moe_w4_workspace_size(cfg) -> int:
     return n.value
 
 
-_W4_NAMES = tuple(name for name, _ in MoEW4Experts._fields_[1:])
-
-
-def _w4_tensors(wq):
-    return [wq.get(name) for name in _W4_NAMES]
-
-
-def _w4_experts(wq) -> MoEW4Experts:
-    return MoEW4Experts(int(wq["group"]), *[_p(t) for t in _w4_tensors(wq)])
+def _w4_experts(fn, cfg, wq, specs):
+    """moe_w4_experts_t of wq, and the addresses of specs' tensors. Entries that the layer does not use are any."""
+    group, u8, bf16, d = int(wq["group"]), torch.uint8, torch.bfloat16, cfg.d
+    specs = list(specs)
+    for pre, n, f in (("", cfg.m, cfg.f), ("sh_", cfg.n_shared, cfg.f_shared)):
+        codes, of_d, of_f = n * f * d // 2, _w4_scales(n, f, d, group), _w4_scales(n, d, f, group)
+        for key, scales in (("gate", of_d), ("up", of_d), ("down", of_f)):
+            used = n > 0 and (key != "up" or cfg.act == SWIGLU)
+            q, s = wq.get(pre + key), wq.get(pre + key + "_scale")
+            specs += ((q, u8, codes), (s, bf16, scales)) if used else ((q, None, 0), (s, None, 0))
+    ptrs = _pointers(fn, specs)
+    return MoEW4Experts(group, *ptrs[-12:]), ptrs[:-12]
 
 
 def moe_grouped_ffn_w4(cfg, x_perm, offsets, wq, task_w, perm, y_perm, ws, stream=None):
     """wq: a dict of device tensors as quantize_experts_w4 returns (kept alive by the caller)."""
-    _pointers("moe_grouped_ffn_w4", x_perm, offsets, task_w, perm, y_perm, ws, *_w4_tensors(wq))
-    st = _w4_experts(wq)
-    _check("moe_grouped_ffn_w4", lib().moe_grouped_ffn_w4(ctypes.byref(cfg), _p(x_perm), _p(offsets),
-                                                          ctypes.byref(st), _p(task_w), _p(perm), _p(y_perm), _p(ws),
+    tasks, f32, i32 = cfg.T * cfg.k, torch.float32, torch.int32
+    st, (xp, op, twp, pp, yp, wsp) = _w4_experts("moe_grouped_ffn_w4", cfg, wq, (
+        (x_perm, torch.bfloat16, tasks * cfg.d), (offsets, i32, cfg.m + 1), (task_w, f32, tasks), (perm, i32, tasks),
+        (y_perm, f32, tasks * cfg.d), (ws, None, 0)))
+    _check("moe_grouped_ffn_w4", lib().moe_grouped_ffn_w4(ctypes.byref(cfg), xp, op, ctypes.byref(st), twp, pp, yp, wsp,
                                                           ws.numel(), _stream(stream)))
 
 
 def moe_layer_forward_w4(cfg, x, w_router, bias, wq, out, ws, logits_out=None, topk_idx_out=None, topk_w_out=None,
                          counts_out=None, lis_out=None, stream=None):
     """wq: a dict of device tensors as quantize_experts_w4 returns (kept alive by the caller)."""
-    _pointers("moe_layer_forward_w4", x, w_router, bias, out, ws, logits_out, topk_idx_out, topk_w_out, counts_out,
-              lis_out, *_w4_tensors(wq))
-    st = _w4_experts(wq)
-    _check("moe_layer_forward_w4", lib().moe_layer_forward_w4(
-        ctypes.byref(cfg), _p(x), _p(w_router), _p(bias), ctypes.byref(st), _p(out), _p(logits_out),
-        _p(topk_idx_out), _p(topk_w_out), _p(counts_out), _p(lis_out), _p(ws), ws.numel(), _stream(stream)))
+    n, tasks, bf16, f32, i32 = cfg.T * cfg.d, cfg.T * cfg.k, torch.bfloat16, torch.float32, torch.int32
+    st, (xp, rp, bp, *outs, wsp) = _w4_experts("moe_layer_forward_w4", cfg, wq, (
+        (x, bf16, n), (w_router, bf16, cfg.m * cfg.d), (bias, f32, cfg.m), (out, bf16, n),
+        (logits_out, f32, cfg.T * cfg.m), (topk_idx_out, i32, tasks), (topk_w_out, f32, tasks),
+        (counts_out, i32, cfg.m), (lis_out, torch.uint8, LIS_BYTES), (ws, None, 0)))
+    _check("moe_layer_forward_w4", lib().moe_layer_forward_w4(ctypes.byref(cfg), xp, rp, bp, ctypes.byref(st), *outs,
+                                                              wsp, ws.numel(), _stream(stream)))
 
 
 def quantize_experts_w4(w_gate, w_up, w_down, ws_gate=None, ws_up=None, ws_down=None, group=128,
@@ -414,7 +435,7 @@ def quantize_experts_w4(w_gate, w_up, w_down, ws_gate=None, ws_up=None, ws_down=
             continue
         n, rows, cols = w.shape
         codes = torch.empty((n, rows, cols // 2), dtype=torch.uint8, device=w.device)
-        scales = torch.empty((n, -(-cols // group), rows), dtype=torch.bfloat16, device=w.device)
+        scales = torch.empty((n, -(-cols // max(group, 1)), rows), dtype=torch.bfloat16, device=w.device)
         moe_quantize_w4(w, group, codes, scales, stream=stream)
         out[key], out[key + "_scale"] = codes, scales
     return out

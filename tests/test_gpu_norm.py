@@ -248,3 +248,16 @@ def test_binding_refuses_strided_and_host_tensors():
     for a in ((wide[:, ::2], None, w, x), (x, wide[:, :64], w, x), (x, None, w.cpu(), x), (x.cpu(), None, w, x)):
         with pytest.raises(moe.MoEError):
             moe.moe_add_rmsnorm(a[0], a[1], a[2], 1e-6, a[3])
+
+
+def test_binding_refuses_other_types_and_sizes():
+    x = torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    codes, scales = torch.empty(4, 64, dtype=torch.uint8, device="cuda"), torch.empty(4, device="cuda")
+    for bad in (dict(weight=w.float()), dict(weight=w[:56]), dict(residual=x[:3]), dict(y=x.float()), dict(y=x[:2]),
+                dict(sum_out=x[:1]), dict(codes=codes[:3]), dict(codes=x), dict(scales=scales[:3]),
+                dict(scales=scales.half())):
+        a = dict(dict(residual=None, weight=w, y=torch.empty_like(x), sum_out=None, codes=codes, scales=scales), **bad)
+        with pytest.raises(moe.MoEError):
+            moe.moe_add_rmsnorm(x, a["residual"], a["weight"], 1e-6, a["y"], sum_out=a["sum_out"], codes=a["codes"],
+                                scales=a["scales"])

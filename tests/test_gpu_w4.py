@@ -544,3 +544,25 @@ def test_binding_refuses_strided_and_host_tensors():
         moe.moe_quantize_w4(v.t(), 32, codes, scales)
     with pytest.raises(moe.MoEError):
         moe.moe_dequantize_w4(codes, scales.cpu(), 32, v)
+
+
+def test_binding_refuses_other_types_and_sizes():
+    c, wq, _, x, wr, bias, _ = _layer_case(LAYERS[0])
+    ws, out = moe.w4_workspace(c), torch.empty_like(x)
+    for bad in (dict(x=x.float()), dict(out=out.float()), dict(wr=wr[:-1]), dict(wr=wr.float()),
+                dict(bias=bias.to(torch.bfloat16)), dict(counts_out=torch.empty(c.m - 1, dtype=torch.int32, device="cuda")),
+                dict(wq=dict(wq, up=wq["up"][:-1])), dict(wq=dict(wq, group=32)),
+                dict(wq=dict(wq, down_scale=wq["down_scale"].float()))):
+        a = dict(dict(x=x, wr=wr, bias=bias, wq=wq, out=out, counts_out=None), **bad)
+        with pytest.raises(moe.MoEError):
+            moe.moe_layer_forward_w4(c, a["x"], a["wr"], a["bias"], a["wq"], a["out"], ws, counts_out=a["counts_out"])
+    v = torch.zeros(8, 64, dtype=torch.bfloat16, device="cuda")
+    codes = torch.empty(8, 32, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(2, 8, dtype=torch.bfloat16, device="cuda")
+    for bad in ((v.float(), codes, scales), (v, codes[:7], scales), (v, codes, scales[:1]), (v, codes, scales.half())):
+        with pytest.raises(moe.MoEError):
+            moe.moe_quantize_w4(bad[0], 32, bad[1], bad[2])
+        with pytest.raises(moe.MoEError):
+            moe.moe_dequantize_w4(bad[1], bad[2], 32, bad[0])
+    with pytest.raises(moe.MoEError):
+        moe.moe_quantize_w4(v, 0, codes, scales)

@@ -163,3 +163,45 @@ def test_binding_refuses_other_types():
     x = torch.zeros(2, 16, dtype=torch.float16)
     with pytest.raises(moe.MoEError):
         moe.moe_add_rmsnorm(x, None, x, 1e-5, x, stream=0)
+
+
+def test_binding_checks_types_and_sizes(monkeypatch):
+    import torch
+    from sparse_mixture_experts_08_b200 import moe as binding
+
+    class Fake:  # a tensor that says it is on the device
+        def __init__(self, *shape, dtype):
+            self.t, self.dtype = torch.zeros(shape, dtype=dtype), dtype
+            self.numel, self.is_contiguous, self.data_ptr = self.t.numel, self.t.is_contiguous, self.t.data_ptr
+
+        def get_device(self):
+            return 0
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    t = Fake(4, 8, dtype=torch.bfloat16)
+    got = binding._pointers("f", ((t, torch.bfloat16, 32), (None, torch.float32, 9), (1 << 20, torch.float32, 9),
+                                  (t, None, 1)))
+    assert got == [t.data_ptr(), None, 1 << 20, t.data_ptr()]
+    for spec in ((t, torch.float32, 32), (t, torch.bfloat16, 33), (torch.zeros(4), torch.float32, 4)):
+        with pytest.raises(moe.MoEError):
+            binding._pointers("f", ((t, torch.bfloat16, 32), spec))
+
+    def experts(act, **kw):
+        m, d, f, g = 3, 96, 160, 64
+        wq = {"group": g}
+        for key, rows, cols in (("gate", f, d), ("up", f, d), ("down", d, f)):
+            wq[key] = Fake(m, rows, cols // 2, dtype=torch.uint8)
+            wq[key + "_scale"] = Fake(m, -(-cols // g), rows, dtype=torch.bfloat16)
+        wq.update(kw)
+        st, ptrs = binding._w4_experts("f", moe.make_config(4, d, f, m, 1, act=act), wq, ((t, torch.bfloat16, 32),))
+        assert ptrs == [t.data_ptr()] and (st.gate, st.down_scale) == (wq["gate"].data_ptr(), wq["down_scale"].data_ptr())
+        assert st.sh_gate is None and st.group == wq["group"]
+
+    experts(moe.SWIGLU)
+    experts(moe.RELU, up=Fake(1, dtype=torch.float32), up_scale=None)  # not used
+    experts(moe.SWIGLU, group=0)  # the library refuses it
+    for kw in (dict(up=Fake(3, 160, 47, dtype=torch.uint8)), dict(down=Fake(3, 96, 80, dtype=torch.float32)),
+               dict(gate_scale=Fake(3, 1, 160, dtype=torch.bfloat16)),
+               dict(down_scale=Fake(3, 3, 96, dtype=torch.float16)), dict(group=32)):
+        with pytest.raises(moe.MoEError):
+            experts(moe.SWIGLU, **kw)
