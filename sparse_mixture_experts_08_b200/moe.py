@@ -145,7 +145,8 @@ _DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
 def _pointers(fn: str, specs):
     """The addresses of specs' tensors: (tensor, dtype, elements) each. Refuses what the library cannot see: tensors
     that are not contiguous, not all on the current CUDA device, of another type, or with fewer elements than the call
-    reads or writes. None and addresses pass as they are; dtype None: any type."""
+    reads or writes. None and addresses pass as they are; dtype None: any type. Integers of a type's size pass for it,
+    and it for them (bf16 as its bits, E4M3 for its codes)."""
     dev, out = None, []
     for t, dtype, n in specs:
         if t is None or t.__class__ is int:
@@ -156,7 +157,10 @@ def _pointers(fn: str, specs):
             if dev is not None or d < 0 or d != torch.cuda.current_device():
                 raise MoEError(fn, ERR_INVALID_ARG)
             dev = d
-        if (t.dtype is not dtype and dtype is not None) or t.numel() < n or not t.is_contiguous():
+        if t.dtype is not dtype and dtype is not None and (
+                t.dtype.itemsize != dtype.itemsize or t.dtype.is_floating_point and dtype.is_floating_point):
+            raise MoEError(fn, ERR_INVALID_ARG)
+        if t.numel() < n or not t.is_contiguous():
             raise MoEError(fn, ERR_INVALID_ARG)
         out.append(t.data_ptr())
     return out

@@ -566,3 +566,8 @@ def test_binding_refuses_other_types_and_sizes():
             moe.moe_dequantize_w4(bad[1], bad[2], 32, bad[0])
     with pytest.raises(moe.MoEError):
         moe.moe_quantize_w4(v, 0, codes, scales)
+    # bf16 as its bits is no other type
+    a, b = torch.empty_like(x), torch.empty_like(x)
+    moe.moe_layer_forward_w4(c, x, wr, bias, wq, a, ws)
+    moe.moe_layer_forward_w4(c, x.view(torch.int16), wr.view(torch.int16), bias, wq, b.view(torch.int16), ws)
+    assert torch.equal(a, b)

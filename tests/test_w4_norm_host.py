@@ -182,7 +182,10 @@ def test_binding_checks_types_and_sizes(monkeypatch):
     got = binding._pointers("f", ((t, torch.bfloat16, 32), (None, torch.float32, 9), (1 << 20, torch.float32, 9),
                                   (t, None, 1)))
     assert got == [t.data_ptr(), None, 1 << 20, t.data_ptr()]
-    for spec in ((t, torch.float32, 32), (t, torch.bfloat16, 33), (torch.zeros(4), torch.float32, 4)):
+    bits, e4m3 = Fake(32, dtype=torch.int16), Fake(32, dtype=torch.float8_e4m3fn)
+    binding._pointers("f", ((bits, torch.bfloat16, 32), (e4m3, torch.uint8, 32)))
+    for spec in ((bits, torch.float32, 16), (Fake(32, dtype=torch.float16), torch.bfloat16, 32), (bits, torch.uint8, 32),
+                 (t, torch.float32, 32), (t, torch.bfloat16, 33), (torch.zeros(4), torch.float32, 4)):
         with pytest.raises(moe.MoEError):
             binding._pointers("f", ((t, torch.bfloat16, 32), spec))
 
