@@ -420,7 +420,8 @@ MOE_API moe_status_t moe_w4_workspace_size(const moe_config_t* cfg, size_t* byte
  * the routed matrices of wq are read. Activations stay bf16 (the hidden activation h is
  * rounded to bf16 between the two products), sums are fp32 in an order that depends on
  * the sizes alone, so the same call gives the same bits. A weight is code * scale rounded
- * to bf16 (no rounding for moe_quantize_w4's scales). */
+ * to bf16 (no rounding for moe_quantize_w4's scales). Offsets that decrease or leave
+ * [0, T k] set MOE_ERR_DEVICE_INDEX in the status word, and nothing is written to y_perm. */
 MOE_API moe_status_t moe_grouped_ffn_w4(const moe_config_t* cfg, const void* x_perm, const int32_t* offsets,
                                         const moe_w4_experts_t* wq, const float* task_w, const int32_t* perm,
                                         float* y_perm, void* ws, size_t ws_bytes, moe_stream_t stream);

@@ -316,6 +316,7 @@ struct WtSched {
   int rows[WT_MAX_GROUPS], brow[WT_MAX_GROUPS];  // by group; first row in its segment order
   short height[WT_MAX_GROUPS];
   int hist[32];
+  int none;  // no work: an error that was there before the launch, or bad offsets
   WtItem items[WT_ITEMS];
 };
 
@@ -391,11 +392,18 @@ __device__ __forceinline__ WtItem wt_item(const W4Params& p, const WtSched<WtSha
 // The schedule, by one warp: groups ordered by tile height, tallest first (a counting
 // sort over the heights, stable in group order), tiles and costs added up in that order,
 // and this walker's first pieces of work. First the order, then a warp for each phase.
+//
+// The CTAs of a launch share tiles, so all of them must lay out the same schedule. Each
+// checks every offset for itself, and any bad one leaves it without work: were that left to
+// the status word (`prior`, read before), only CTAs that read it after another's check
+// would stop.
 template <int BN>
-__device__ __forceinline__ void wt_order(const W4Params& p, WtSched<WtShape<BN>::PHASES>& s, int G, int lane) {
+__device__ __forceinline__ void wt_order(const W4Params& p, WtSched<WtShape<BN>::PHASES>& s, int G, int lane,
+                                         int prior) {
   constexpr int NB = BN / 16 + 1;  // bucket = tile height / 16 (0: a group without rows)
   static_assert(NB <= 32, "a bucket a lane");
   const int G0 = p.cls[0].n_groups;
+  bool bad = prior != 0;
   s.hist[lane] = 0;
   __syncwarp();
   for (int g0 = 0; g0 < G; g0 += 32) {
@@ -411,6 +419,7 @@ __device__ __forceinline__ void wt_order(const W4Params& p, WtSched<WtShape<BN>:
         brow = a;
         if (a < 0 || b < a || b > c.max_row) {
           set_status(p.status, MOE_ERR_DEVICE_INDEX);
+          bad = true;
           rows = brow = 0;
         }
       } else {
@@ -446,12 +455,14 @@ __device__ __forceinline__ void wt_order(const W4Params& p, WtSched<WtShape<BN>:
     __syncwarp();
   }
   for (int gi = lane; gi < G; gi += 32) s.gid[s.hist[s.height[gi] >> 4] + s.ph[0].cost[gi]] = gi;
+  bad = __any_sync(0xffffffffu, bad);
+  if (lane == 0) s.none = bad;
   __syncwarp();
 }
 
 template <int BN, int EPI>
 __device__ __forceinline__ void wt_phase(const W4Params& p, WtSched<WtShape<BN>::PHASES>& s, int G, int walker,
-                                         int walkers, int lane, int phase, bool none) {
+                                         int walkers, int lane, int phase) {
   using S = WtShape<BN>;
   WtPhase& f = s.ph[phase];
   const int G0 = p.cls[0].n_groups;
@@ -476,7 +487,7 @@ __device__ __forceinline__ void wt_phase(const W4Params& p, WtSched<WtShape<BN>:
   int total = __shfl_sync(0xffffffffu, inc, 31);
   if (lane == 0) f.tile_start[G] = total;
   __syncwarp();
-  if (none) total = 0;
+  if (s.none) total = 0;
   // whole rounds, and the tiles that are cut
   int rounds = 0;
   if (total >= walkers) {
@@ -701,11 +712,10 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
   if (warp == 0 || (TWO && warp == 2)) {
     pdl_wait();
     // an earlier kernel of the call that flagged a device error leaves tables that are not used
-    const int prior = p.status ? *reinterpret_cast<volatile int*>(p.status) : 0;
-    if (warp == 0) wt_order<BN>(p, sched, G, lane);
+    if (warp == 0) wt_order<BN>(p, sched, G, lane, p.status ? *reinterpret_cast<volatile int*>(p.status) : 0);
     __syncwarp();
     if (TWO) schedule_bar();
-    wt_phase<BN, EPI>(p, sched, G, walker, walkers, lane, warp >> 1, __any_sync(0xffffffffu, prior != 0));
+    wt_phase<BN, EPI>(p, sched, G, walker, walkers, lane, warp >> 1);
     if (TWO) {
       schedule_bar();
       const int n0 = sched.ph[0].n, n = n0 + sched.ph[S::PHASES - 1].n;

@@ -1,0 +1,69 @@
+"""4-bit expert products when something goes wrong: bad offsets, waits that run out, calls cut short.
+
+No GPU is faulted: bad offsets are checked in the kernel, and every wait has a time limit.
+"""
+import time
+
+import pytest
+import torch
+
+import sparse_mixture_experts_08_b200 as moe
+from gpu_helpers import require_gpu
+from test_gpu_w4 import _segments, make_experts
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _gpu():
+    require_gpu()
+
+
+# rows of 3 segments, d, f: tiles of 16, 32, 64, 128, 192 rows, and of 224 in the first, the second and both products
+HEIGHTS = [(12, 64, 96), (45, 352, 544), (90, 352, 1120), (300, 352, 544), (600, 352, 544), (600, 4096, 96),
+           (600, 96, 4128), (600, 4128, 4096)]
+
+
+def _grouped(rows, d, f, m=3, act=moe.SWIGLU):
+    """A configuration, weights, input rows and good offsets of m segments that share `rows` rows."""
+    gen = torch.Generator().manual_seed(rows + d + f)
+    wq, _ = make_experts(gen, m, d, f, 32, act)
+    x = torch.randn(rows, d, generator=gen).to(torch.bfloat16).cuda()
+    lengths = [rows // m] * (m - 1)
+    return moe.make_config(rows, d, f, m, 1, act=act), wq, x, _segments(lengths + [rows - sum(lengths)])
+
+
+@pytest.mark.parametrize("rows,d,f", HEIGHTS)
+def test_bad_offsets_leave_everything_unwritten_in_every_tile_height(rows, d, f):
+    """All blocks of a launch come to the same verdict: no row is written, and none of them waits for another that
+    dropped its work (the wait limit is 2 s)."""
+    c, wq, x, good = _grouped(rows, d, f)
+    ws = moe.w4_workspace(c)
+    want = torch.empty(rows, d, device="cuda")
+    moe.moe_grouped_ffn_w4(c, x, good, wq, None, None, want, ws)
+    assert moe.moe_read_device_status(ws) == moe.OK
+    a, b = good.tolist()[1:3]
+    for offsets in ([0, a, b, rows + 1], [0, a, a - 1, rows], [-1, a, b, rows], [0, a, b, -5], [0, rows + 7, b, rows]):
+        bad = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+        y = torch.full((rows, d), -7.0, device="cuda")
+        torch.cuda.synchronize()
+        start = time.perf_counter()
+        moe.moe_grouped_ffn_w4(c, x, bad, wq, None, None, y, ws)
+        assert moe.moe_read_device_status(ws) == moe.ERR_DEVICE_INDEX
+        assert time.perf_counter() - start < 1.0
+        assert (y == -7.0).all()
+    y = torch.empty_like(want)
+    moe.moe_grouped_ffn_w4(c, x, good, wq, None, None, y, ws)
+    assert moe.moe_read_device_status(ws) == moe.OK and torch.equal(y, want)
+
+
+@pytest.mark.parametrize("rows", [100, 2200])
+def test_one_bad_offset_among_many_groups(rows):
+    c, wq, x, good = _grouped(rows, 96, 64, m=70)
+    ws = moe.w4_workspace(c)
+    for at, value in ((70, rows + 1), (64, 0), (1, rows)):
+        bad = good.clone()
+        bad[at] = value
+        y = torch.full((rows, 96), -7.0, device="cuda")
+        moe.moe_grouped_ffn_w4(c, x, bad, wq, None, None, y, ws)
+        assert moe.moe_read_device_status(ws) == moe.ERR_DEVICE_INDEX and (y == -7.0).all()
