@@ -661,7 +661,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
   __shared__ __align__(16) __nv_bfloat16 stg[EPI == EPI_DOWN ? 1 : EW][16][32];  // epilogue warp: 16 output rows
   __shared__ uint32_t tmem_base_s;
   __shared__ int abort_s;
-  __shared__ unsigned long long launch_s;  // TWO: the launch's number on this workspace
+  __shared__ unsigned long long launch_s;  // the launch's number on this workspace
   extern __shared__ uint8_t dyn_smem[];
 
   // (the shuffle tells the compiler that the role is the whole warp's: loop state and
@@ -726,22 +726,20 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
   } else if (warp == 3) {
     // TWO: the second product's input rows are the first one's output, so they wait for a
     // grid-wide count of the epilogue warps that have left the first product (all CTAs are
-    // resident: a cooperative launch). The count only grows, by the same number a launch
-    // whatever happens in it, so launches are numbered by it. (The weights do not wait: the
-    // ring holds the second product's first chunks before the last CTA leaves the first.)
-    // The counters of cut tiles: this launch zeroes the set that the next one uses,
-    // whatever it, or one that was cut short, leaves in its own.
+    // resident: a cooperative launch). (The weights do not wait: the ring holds the second
+    // product's first chunks before the last CTA leaves the first.) Otherwise every CTA
+    // counts when it ends. Either count only grows, by the same number a launch whatever
+    // happens in it and not fully before every CTA has read it here, so launches are
+    // numbered by it. The counters of cut tiles: this launch zeroes the set that the next
+    // one uses, whatever it, or one that was cut short, leaves in its own.
     pdl_wait();
-    if (TWO) {
-      unsigned long long v;
-      asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p.grid_count) : "memory");
-      const unsigned long long number = v / (gridDim.x * EW);
-      if (lane == 0) launch_s = number;
-      if (blockIdx.x == 0)
-        for (int i = lane; i < 2 * W4_COUNTERS2; i += 32)
-          p.counters[(number & 1 ? 0 : 2 * W4_COUNTERS2) + i] = 0u;
-    } else if (blockIdx.x == 0) {
-      for (int i = lane; i < W4_COUNTERS; i += 32) p.counters_next[i] = 0u;
+    unsigned long long v;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p.grid_count) : "memory");
+    const unsigned long long number = v / (TWO ? gridDim.x * EW : W4_MAX_CTAS);
+    if (lane == 0) launch_s = number;
+    if (blockIdx.x == 0) {
+      constexpr int SET = TWO ? 2 * W4_COUNTERS2 : W4_COUNTERS;
+      for (int i = lane; i < SET; i += 32) p.counters[(number & 1 ? 0 : SET) + i] = 0u;
     }
   }
   if (warp < WT_EXPAND_WARP || warp >= S::EPI_WARP) __syncthreads();  // the schedule is there
@@ -1177,8 +1175,8 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
         // the last of the tile's walkers to get here adds the parts, in the order of K
         __threadfence();
         __syncwarp();
-        unsigned* const counters =
-            p.counters + (TWO ? (2 * (int)(launch_s & 1) + phase) * W4_COUNTERS2 : 0);
+        const int set = (int)(launch_s & 1);
+        unsigned* const counters = p.counters + (TWO ? (2 * set + phase) * W4_COUNTERS2 : set * W4_COUNTERS);
         unsigned n = 0;
         if (lane == 0) n = atomicAdd(&counters[(it.wa * CTAS + (int)rank) * EW + ew], 1u);
         n = __shfl_sync(0xffffffffu, n, 0);
@@ -1210,6 +1208,8 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   if (PAIR) cluster_sync_all();  // neither CTA leaves while the other may signal it or read its memory
+  if (!TWO && threadIdx.x == 0)  // W4_MAX_CTAS a launch, however many CTAs it has
+    atomicAdd(p.grid_count, blockIdx.x ? 1ull : (unsigned long long)(W4_MAX_CTAS - (gridDim.x - 1)));
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_g<PAIR>(tmem, 512);

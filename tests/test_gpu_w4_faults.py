@@ -2,6 +2,7 @@
 
 No GPU is faulted: bad offsets are checked in the kernel, and every wait has a time limit.
 """
+import ctypes
 import time
 
 import pytest
@@ -67,3 +68,57 @@ def test_one_bad_offset_among_many_groups(rows):
         y = torch.full((rows, 96), -7.0, device="cuda")
         moe.moe_grouped_ffn_w4(c, x, bad, wq, None, None, y, ws)
         assert moe.moe_read_device_status(ws) == moe.ERR_DEVICE_INDEX and (y == -7.0).all()
+
+
+class _Cudart:
+    """The runtime calls that take a node out of a graph."""
+
+    def __init__(self):
+        self.lib = ctypes.CDLL("libcudart.so.12")
+
+    def call(self, name, *args):
+        assert getattr(self.lib, name)(*args) == 0, name
+
+    def nodes(self, graph):
+        n = ctypes.c_size_t(0)
+        self.call("cudaGraphGetNodes", graph, None, ctypes.byref(n))
+        nodes = (ctypes.c_void_p * n.value)()
+        self.call("cudaGraphGetNodes", graph, nodes, ctypes.byref(n))
+        return [ctypes.c_void_p(v) for v in nodes]
+
+    def last_node(self, graph):
+        """The node that no other depends on."""
+        def dependents(node):
+            n = ctypes.c_size_t(0)
+            self.call("cudaGraphNodeGetDependentNodes", node, None, ctypes.byref(n))
+            return n.value
+        last = [node for node in self.nodes(graph) if dependents(node) == 0]
+        assert len(last) == 1
+        return last[0]
+
+
+@pytest.mark.parametrize("rows,d,f", [(300, 352, 4128), (600, 352, 4128), (600, 4128, 4096)])
+def test_a_call_cut_short_after_its_first_product_leaves_no_counters(rows, d, f):
+    """The first product is launched, the second is not (what a call leaves that returns an error between them): the
+    next calls on the workspace find their counters of cut tiles at zero."""
+    c, wq, x, good = _grouped(rows, d, f)
+    ws, y = moe.w4_workspace(c), torch.empty(rows, d, device="cuda")
+    inputs = [torch.roll(x, i, 1) for i in range(4)]  # other rows each time: what the workspace holds of h is stale
+    want = []
+    for xi in inputs:
+        want.append(torch.empty(rows, d, device="cuda"))
+        moe.moe_grouped_ffn_w4(c, xi, good, wq, None, None, want[-1], moe.w4_workspace(c))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(graph):
+        moe.moe_grouped_ffn_w4(c, x, good, wq, None, None, y, ws)
+    rt, handle = _Cudart(), ctypes.c_void_p(graph.raw_cuda_graph())
+    assert len(rt.nodes(handle)) == 2  # a launch for each product
+    rt.call("cudaGraphDestroyNode", rt.last_node(handle))
+    graph.instantiate()
+    for cut_short in (1, 2, 3):
+        for _ in range(cut_short):
+            graph.replay()
+        y.fill_(float("nan"))
+        moe.moe_grouped_ffn_w4(c, inputs[cut_short], good, wq, None, None, y, ws)
+        assert moe.moe_read_device_status(ws) == moe.OK and torch.equal(y, want[cut_short])
