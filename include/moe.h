@@ -494,8 +494,12 @@ MOE_API moe_status_t moe_debug_set_wait_limit_ns(uint64_t ns);
  * (moe_atomic_experts / moe_atomic_forward with T K < 16384) waits for n arrivals
  * more than its grid has, so with n > 0 it can only end at the bounded wait's
  * time limit: the kernel then records MOE_ERR_TIMEOUT and its blocks return
- * without the assembly phase. 0 (the default) restores the normal barrier. Not
- * thread-safe; meant for fault-injection tests. */
+ * without the assembly phase. In the 4-bit expert products n = 1 makes every
+ * product wait for one arrival more than the expanded weights have, and n = 2 (3)
+ * stops the input rows of a block (of the second block of a pair) after its first
+ * piece of work: the waits run out, the kernel records MOE_ERR_TIMEOUT and returns.
+ * 0 (the default) restores the normal barriers. Not thread-safe; meant for
+ * fault-injection tests. */
 MOE_API moe_status_t moe_debug_set_barrier_extra(uint32_t n);
 
 /* Profiling hook: when n > 0, every later moe_layer_forward records the n

@@ -28,6 +28,7 @@ int num_sms() {
 }
 
 static unsigned long long g_wait_limit_ns = 2000ull * 1000 * 1000;
+static unsigned g_stall = 0;
 static cudaEvent_t g_stage_events[8];
 static int g_n_stage_events = 0;
 
@@ -324,6 +325,7 @@ static moe_status_t run_ffn_w4(const moe_config_t& c, const FfnIo& io, int* stat
   p.group = w.group;
   p.status = status;
   p.wait_limit_ns = g_wait_limit_ns;
+  p.stall = g_stall;
   p.partial = io.w4_partial;
   unsigned* const counters = reinterpret_cast<unsigned*>(status + 64);
   const int bn = w4_bn(c);
@@ -1545,6 +1547,7 @@ moe_status_t moe_debug_set_wait_limit_ns(uint64_t ns) {
 
 moe_status_t moe_debug_set_barrier_extra(uint32_t n) {
   set_grid_barrier_extra(n);
+  g_stall = n;
   return MOE_OK;
 }
 

@@ -544,8 +544,11 @@ struct WtWalk {
   __device__ __forceinline__ WtWalk(const W4Params& p_, const WtSched<WtShape<BN>::PHASES>& s_, int G_, int w, int ws)
       : p(p_), s(s_), G(G_), walker(w), walkers(ws), i(0), n(-1) {}
 
+  __device__ __forceinline__ int all() const {
+    return s.ph[0].n + (WtShape<BN>::PHASES == 2 ? s.ph[WtShape<BN>::PHASES - 1].n : 0);
+  }
   __device__ __forceinline__ bool next(WtItem& it) {
-    if (n < 0) n = s.ph[0].n + (WtShape<BN>::PHASES == 2 ? s.ph[WtShape<BN>::PHASES - 1].n : 0);
+    if (n < 0) n = all();
     while (i < n) {
       it = i < WT_ITEMS ? s.items[i] : wt_item<BN>(p, s, G, walker, walkers, i);
       ++i;
@@ -631,6 +634,21 @@ __device__ __forceinline__ uint32_t lds16(uint32_t a) {
 // Barrier of the two warps that lay out the schedule of two products (named barrier 1).
 __device__ __forceinline__ void schedule_bar() { asm volatile("barrier.sync 1, 64;" ::: "memory"); }
 
+// Bytes that a barrier expects and no copy will bring, counted as if one had.
+__device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes)
+               : "memory");
+}
+// A word of a CTA of the pair, read from or written to it (a shared::cluster address).
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_cluster(uint32_t a, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
 // Tile copy over three dimensions; PAIR: counted on a barrier of the leader CTA.
 template <bool PAIR>
 __device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint32_t bar, void* dst, int x, int y, int z) {
@@ -661,6 +679,9 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
   __shared__ __align__(16) __nv_bfloat16 stg[EPI == EPI_DOWN ? 1 : EW][16][32];  // epilogue warp: 16 output rows
   __shared__ uint32_t tmem_base_s;
   __shared__ int abort_s;
+  // PAIR: chunks whose input rows this CTA fetched, the stages whose last such copy was the
+  // short one, and whether the other CTA gave up
+  __shared__ int x_used_s, x_half_s, peer_abort_s;
   __shared__ unsigned long long launch_s;  // the launch's number on this workspace
   extern __shared__ uint8_t dyn_smem[];
 
@@ -680,7 +701,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(&code_full[i], 1);
       mbar_init(&x_full[i], 1);
-      mbar_init(&a_full[i], 4 * CTAS);  // a team of each CTA
+      mbar_init(&a_full[i], 4 * CTAS + (p.stall == 1));  // a team of each CTA
       mbar_init(&stage_free[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -689,6 +710,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
     }
     mbar_init(&drain_bar, S::ISSUERS);
     abort_s = 0;
+    x_used_s = x_half_s = peer_abort_s = 0;
     fence_mbar_init();
   }
   if (warp == 2 && lane < (int)(sizeof(maps) / sizeof(CUtensorMap)))
@@ -754,9 +776,10 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
     // would bound the short tiles). As in the issuer, the whole warp walks and waits and
     // one lane issues.
     const bool codes = warp == 0;
+    if (!codes && p.stall == 2 + rank) walk.n = min(walk.all(), 1);
     bool second = false;
     int st = 0, used = 0;
-    uint32_t ph = 0;
+    uint32_t ph = 0, halves = 0;
     const int gpc = BK / p.group;
     while (ok && walk.next(it)) {
       const W4Class& c = p.cls[it.cls];
@@ -819,6 +842,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
         }
         __syncwarp();
         ++used;
+        if (PAIR) halves = (halves & ~(1u << st)) | ((uint32_t)half << st);
         if (++st == STAGES) {
           st = 0;
           ph ^= 1u;
@@ -829,19 +853,22 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
       set_status(p.status, MOE_ERR_TIMEOUT);
       abort_s = 1;
     }
-    // every issued copy lands before the CTA may exit (PAIR: the leader's barriers count
-    // both CTAs' rows; the peer waits for the leader at the last cluster barrier): the
-    // last use of stage i was its fill number (used - 1 - i) / STAGES. (Rows that the peer
-    // fetched for a stage which a leader that gave up never armed are on no barrier: the
-    // peer leaves them 5 ms.)
-    if (PAIR && !ok && !codes && !leader)
-      for (int i = 0; i < 50; ++i) __nanosleep(100000);
+    // every issued copy lands before the CTA may exit: the last use of stage i was its fill
+    // number (used - 1 - i) / STAGES. (PAIR: the leader's barriers count both CTAs' rows,
+    // and the peer waits for the leader at the last cluster barrier. Where either CTA gave
+    // up, the copies are settled there, with what both have fetched.)
+    if (PAIR && !codes && lane == 0) {
+      x_used_s = used;
+      x_half_s = (int)halves;
+    }
     if (lane == 0 && (codes || leader))
       for (int i = 0; i < STAGES && i < used; ++i) {
         const volatile int never = 0;
         if (!mbar_wait(codes ? &code_full[i] : &x_full[i], (uint32_t)((used - 1 - i) / STAGES) & 1u,
-                       WT_DRAIN_LIMIT_NS, &never))
+                       WT_DRAIN_LIMIT_NS, PAIR && !codes ? abort_flag : &never)) {
           set_status(p.status, MOE_ERR_TIMEOUT);
+          abort_s = 1;
+        }
       }
   } else if (warp == 1 || warp == 3) {
     // ---------------------------------------------------------------- matrix issuers
@@ -1207,7 +1234,35 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (PAIR) cluster_sync_all();  // neither CTA leaves while the other may signal it or read its memory
+  if (PAIR) {
+    if (threadIdx.x == 0 && abort_s) st_cluster(mapa_shared(smem_u32(&peer_abort_s), rank ^ 1u), 1u);
+    __syncwarp();
+    cluster_sync_all();  // neither CTA leaves while the other may signal it or read its memory
+    if (abort_s | peer_abort_s) {  // (alike in both CTAs)
+      // Rows that one CTA fetched and the other did not: stage by stage the barrier gets the
+      // expectation, or the bytes, that it lacks. A stage is fetched again only after a
+      // product has read it, so it lacks at most its last fill.
+      if (leader && warp == 2 && lane == 0) {
+        const int own = x_used_s, peer = (int)ld_cluster(mapa_shared(smem_u32(&x_used_s), 1u));
+        const uint32_t halves = own > peer ? (uint32_t)x_half_s : ld_cluster(mapa_shared(smem_u32(&x_half_s), 1u));
+        const int used = max(own, peer);
+        for (int n = min(own, peer); n < used; ++n) {
+          const int i = n % STAGES;
+          const uint32_t bytes = (halves >> i & 1u ? S::HALF : S::B_ROWS) * BK * 2;
+          if (own > peer)
+            mbar_complete_tx(&x_full[i], bytes);
+          else
+            mbar_arrive_expect_tx(&x_full[i], bytes);
+        }
+        for (int i = 0; i < STAGES && i < used; ++i) {
+          const volatile int never = 0;
+          mbar_wait(&x_full[i], (uint32_t)((used - 1 - i) / STAGES) & 1u, WT_DRAIN_LIMIT_NS, &never);
+        }
+      }
+      __syncwarp();
+      cluster_sync_all();  // both CTAs' rows have landed
+    }
+  }
   if (!TWO && threadIdx.x == 0)  // W4_MAX_CTAS a launch, however many CTAs it has
     atomicAdd(p.grid_count, blockIdx.x ? 1ull : (unsigned long long)(W4_MAX_CTAS - (gridDim.x - 1)));
   if (warp == 1) {

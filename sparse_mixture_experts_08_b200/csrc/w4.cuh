@@ -58,6 +58,7 @@ struct W4Params {
   unsigned long long* grid_count;
   int* status;
   unsigned long long wait_limit_ns;
+  unsigned stall;  // test hook, 0 but for tests of the time limits (moe_debug_set_barrier_extra)
 };
 
 // Input rows of a tile (16 .. 192) for segments of at most T and on average avg_rows rows.

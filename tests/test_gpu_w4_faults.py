@@ -122,3 +122,39 @@ def test_a_call_cut_short_after_its_first_product_leaves_no_counters(rows, d, f)
         y.fill_(float("nan"))
         moe.moe_grouped_ffn_w4(c, inputs[cut_short], good, wq, None, None, y, ws)
         assert moe.moe_read_device_status(ws) == moe.OK and torch.equal(y, want[cut_short])
+
+
+# rows of 3 segments, d, f: several tiles a block in every tile height (16, 32, 64, 128, 192, 224), a few chunks each
+STALLED = [(12, 288, 30720), (45, 288, 30720), (90, 288, 30720), (300, 288, 10240), (700, 288, 10240),
+           (700, 4128, 2080)]
+
+
+@pytest.mark.parametrize("stall", [1, 2, 3])
+@pytest.mark.parametrize("rows,d,f", STALLED)
+def test_stalled_products_time_out_and_the_next_calls_are_right(rows, d, f, stall):
+    """The hook keeps a barrier from ever completing (1), or stops the input rows of a block, of either block of a
+    pair, whose copies the other block's barrier counts (2, 3): the call can only end at its time limit, 1 ms, with
+    every copy settled, and the workspace works again."""
+    c, wq, x, good = _grouped(rows, d, f, act=moe.RELU)
+    ws = moe.w4_workspace(c)
+    want, y = torch.empty(rows, d, device="cuda"), torch.empty(rows, d, device="cuda")
+    moe.moe_grouped_ffn_w4(c, x, good, wq, None, None, want, ws)
+    assert moe.moe_read_device_status(ws) == moe.OK
+    start = time.perf_counter()
+    try:
+        moe.moe_debug_set_wait_limit_ns(1_000_000)
+        moe.moe_debug_set_barrier_extra(stall)
+        for _ in range(2):
+            moe.moe_grouped_ffn_w4(c, x, good, wq, None, None, y, ws)
+            status = moe.moe_read_device_status(ws)
+            # (blocks without a pair have no second block to stop)
+            assert status == (moe.OK if stall == 3 and rows < 90 else moe.ERR_TIMEOUT)
+    finally:
+        moe.moe_debug_set_barrier_extra(0)
+        moe.moe_debug_set_wait_limit_ns(0)
+    # every copy is settled: a barrier that lacks one is waited for 200 ms in each of the two calls
+    assert time.perf_counter() - start < 0.4
+    for _ in range(3):
+        y.fill_(float("nan"))
+        moe.moe_grouped_ffn_w4(c, x, good, wq, None, None, y, ws)
+        assert moe.moe_read_device_status(ws) == moe.OK and torch.equal(y, want)
