@@ -963,7 +963,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
     bool dry = true;  // the first turn, before there is work
     it.c0 = 0;
     it.c1 = 1;
-    int ng = 0;
+    int kdim = 0;
     do {
 #pragma unroll 1
       for (int ch = it.c0; ch < it.c1; ++ch) {
@@ -978,6 +978,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
           constexpr bool EARLY = BK == 128;
           uint4 cw[BK / 32];
           uint32_t sc[BK / 32];
+          const int kleft = kdim - ch * BK;
           bool few = true;
 #pragma unroll
           for (int i = 0; i < BK / 32; ++i) {
@@ -988,9 +989,16 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
               continue;
             }
             sc[i] = lds16(base + scale_off + gi * scale_pitch);
-            if (ch * (BK >> gl2) + gi >= ng) sc[i] = 0u;  // behind K: x is zero there, the scale not this row's
+            if (32 * i >= kleft) sc[i] = 0u;
             few = few && w4_scale_is_short(sc[i]);
           }
+          // Behind K x is zero, but the codes there read as -8 and the scale is another row's
+          // or, in a short last group, this row's, which times -8 may be infinite: zero too.
+          // (K is a multiple of the 32 columns that a granule holds.)
+          if (kleft < BK)
+#pragma unroll
+            for (int i = 0; i < BK / 32; ++i)
+              if (32 * i >= kleft) sc[i] = 0u;
           few = __all_sync(0xffffffffu, few);
           if (!dry && !slot_free()) {
             ok = false;
@@ -1042,7 +1050,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
       }
       if (!ok || !walk.next(it)) break;
       if (TWO) layout(wt_cta_f<BN, EPI>(it.cls >> 1) == 64);
-      ng = (p.cls[it.cls].K + p.group - 1) >> gl2;
+      kdim = p.cls[it.cls].K;
     } while (true);
     if (!ok) {
       set_status(p.status, MOE_ERR_TIMEOUT);

@@ -571,3 +571,33 @@ def test_binding_refuses_other_types_and_sizes():
     moe.moe_layer_forward_w4(c, x, wr, bias, wq, a, ws)
     moe.moe_layer_forward_w4(c, x.view(torch.int16), wr.view(torch.int16), bias, wq, b.view(torch.int16), ws)
     assert torch.equal(a, b)
+
+
+def _huge_last_group(gen, m, rows, cols, group):
+    """Weights whose last group, shorter than the others, reaches 3.3e38: eight times its scale is no bf16 number."""
+    v = torch.randn(m, rows, cols, generator=gen) * cols ** -0.5
+    last = v[:, :, cols // group * group:]
+    last /= last.abs().amax(2, keepdim=True)
+    last *= 3.3e38
+    q, s = pack_ref(v.to(torch.bfloat16).cuda(), group)
+    assert cols % group and torch.isfinite(values64(q, s, group).to(torch.bfloat16)).all() and torch.isinf(s * 8).any()
+    return encode(q), s, values64(q, s, group)
+
+
+@pytest.mark.parametrize("rows", [3, 24, 50, 100, 400])
+@pytest.mark.parametrize("key", ["gate", "down"])
+def test_scales_near_the_top_of_the_range_in_a_short_last_group(key, rows):
+    """Codes behind K stand for no weight: rows of zeros give zeros, rows of tiny inputs what the formula gives."""
+    gen = torch.Generator().manual_seed(rows)
+    d, f, group = 96, 352, 64
+    wq, val = make_experts(gen, 2, d, f, group, moe.RELU)
+    wq[key], wq[key + "_scale"], val[key] = _huge_last_group(gen, 2, *((f, d) if key == "gate" else (d, f)), group)
+    x = (torch.randn(2 * rows, d, generator=gen) * 2.0 ** -110).to(torch.bfloat16).cuda()
+    x[0] = x[rows] = 0
+    c = moe.make_config(2 * rows, d, f, 2, 1, act=moe.RELU)
+    ws, y = moe.w4_workspace(c), torch.empty(2 * rows, d, dtype=torch.float32, device="cuda")
+    moe.moe_grouped_ffn_w4(c, x, _segments([rows, rows]), wq, None, None, y, ws)
+    assert (y[0] == 0).all() and (y[rows] == 0).all()
+    for e in range(2):
+        ref, bound = ffn64(x[e * rows:(e + 1) * rows].to(F64), val, "", e, moe.RELU)
+        check(y[e * rows:(e + 1) * rows], ref, bound)
