@@ -331,7 +331,7 @@ static moe_status_t run_ffn_w4(const moe_config_t& c, const FfnIo& io, int* stat
   const int bn = w4_bn(c);
   const bool both = w4_both_products(bn);
   const int kind = w4_grid_kind(bn);
-  p.grid_count = reinterpret_cast<unsigned long long*>(status + 32) + (both ? kind : W4_GRID_KINDS);
+  p.grid_count = reinterpret_cast<unsigned long long*>(status + 32) + kind;
   for (int down = 0; down < 2; ++down) {
     W4Class* const cls = p.cls + (both && down ? 2 : 0);
     int n = 0;
@@ -375,7 +375,8 @@ static moe_status_t run_ffn_w4(const moe_config_t& c, const FfnIo& io, int* stat
         if (stage_marks) MOE_TRY(mark_stage(5, s));
       }
     } else {
-      p.counters = counters;
+      p.counters = counters + down * W4_COUNTERS;
+      p.counters_next = counters + (1 - down) * W4_COUNTERS;
       MOE_CUDA(launch_w4_gemm(epi, bn, p, s));
       if (!down && stage_marks) MOE_TRY(mark_stage(5, s));
     }

@@ -649,6 +649,41 @@ __device__ __forceinline__ void st_cluster(uint32_t a, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 
+// What a role does whose wait ran out, or that another role's tells to stop (PAIR: both
+// CTAs' settle words are set). Not inlined, like wt_settle: a launch of microseconds starts
+// with a cold instruction cache.
+template <bool PAIR>
+__device__ __noinline__ void wt_give_up(int* status, volatile int* abort_flag, uint32_t settle) {
+  set_status(status, MOE_ERR_TIMEOUT);
+  *abort_flag = 1;
+  if (PAIR)
+    for (uint32_t r = 0; r < 2; ++r) st_cluster(mapa_shared(settle, r), 1u);
+}
+
+// The leader CTA of a pair in which a role gave up waits for both CTAs' input rows. Rows
+// that one CTA fetched (chunks used[0], the stages whose last copy was the short one
+// used[1]) and the other did not: stage by stage the barrier gets the expectation, or the
+// bytes, that it lacks. A stage is fetched again only after a product has read it, so it
+// lacks at most its last fill.
+template <int STAGES>
+__device__ __noinline__ void wt_settle(uint64_t* x_full, const int* used, uint32_t bytes_half, uint32_t bytes_full) {
+  const uint32_t peer_used = mapa_shared(smem_u32(used), 1u);
+  const int own = used[0], peer = (int)ld_cluster(peer_used), last = max(own, peer);
+  const uint32_t halves = own > peer ? (uint32_t)used[1] : ld_cluster(peer_used + 4);
+  for (int n = min(own, peer); n < last; ++n) {
+    const int i = n % STAGES;
+    const uint32_t bytes = (halves >> i & 1u) ? bytes_half : bytes_full;
+    if (own > peer)
+      mbar_complete_tx(&x_full[i], bytes);
+    else
+      mbar_arrive_expect_tx(&x_full[i], bytes);
+  }
+  for (int i = 0; i < STAGES && i < last; ++i) {
+    const volatile int never = 0;
+    mbar_wait(&x_full[i], (uint32_t)((last - 1 - i) / STAGES) & 1u, WT_DRAIN_LIMIT_NS, &never);
+  }
+}
+
 // Tile copy over three dimensions; PAIR: counted on a barrier of the leader CTA.
 template <bool PAIR>
 __device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint32_t bar, void* dst, int x, int y, int z) {
@@ -679,10 +714,10 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
   __shared__ __align__(16) __nv_bfloat16 stg[EPI == EPI_DOWN ? 1 : EW][16][32];  // epilogue warp: 16 output rows
   __shared__ uint32_t tmem_base_s;
   __shared__ int abort_s;
-  // PAIR: chunks whose input rows this CTA fetched, the stages whose last such copy was the
-  // short one, and whether the other CTA gave up
-  __shared__ int x_used_s, x_half_s, peer_abort_s;
-  __shared__ unsigned long long launch_s;  // the launch's number on this workspace
+  // PAIR: chunks whose input rows this CTA fetched and the stages whose last such copy was
+  // the short one; whether a role of either CTA gave up
+  __shared__ int x_used_s[2], settle_s;
+  __shared__ unsigned long long launch_s;  // TWO: the launch's number on this workspace
   extern __shared__ uint8_t dyn_smem[];
 
   // (the shuffle tells the compiler that the role is the whole warp's: loop state and
@@ -696,6 +731,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
   uint8_t* smem_gen = dyn_smem + (smem_base - smem_u32(dyn_smem));
   const int G0 = p.cls[0].n_groups, G = G0 + (p.n_classes > 1 ? p.cls[1].n_groups : 0);
   volatile int* abort_flag = &abort_s;
+  const auto give_up = [&]() { wt_give_up<PAIR>(p.status, abort_flag, smem_u32(&settle_s)); };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
@@ -710,7 +746,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
     }
     mbar_init(&drain_bar, S::ISSUERS);
     abort_s = 0;
-    x_used_s = x_half_s = peer_abort_s = 0;
+    settle_s = 0;
     fence_mbar_init();
   }
   if (warp == 2 && lane < (int)(sizeof(maps) / sizeof(CUtensorMap)))
@@ -748,20 +784,23 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
   } else if (warp == 3) {
     // TWO: the second product's input rows are the first one's output, so they wait for a
     // grid-wide count of the epilogue warps that have left the first product (all CTAs are
-    // resident: a cooperative launch). (The weights do not wait: the ring holds the second
-    // product's first chunks before the last CTA leaves the first.) Otherwise every CTA
-    // counts when it ends. Either count only grows, by the same number a launch whatever
-    // happens in it and not fully before every CTA has read it here, so launches are
-    // numbered by it. The counters of cut tiles: this launch zeroes the set that the next
-    // one uses, whatever it, or one that was cut short, leaves in its own.
+    // resident: a cooperative launch). The count only grows, by W4_COUNT a launch whatever
+    // happens in it (its first warp adds what the others' ones leave of that), so launches
+    // are numbered by it. (The weights do not wait: the ring holds the second product's
+    // first chunks before the last CTA leaves the first.)
+    // The counters of cut tiles: this launch zeroes the set that the next one uses,
+    // whatever a launch that was cut short has left there.
     pdl_wait();
-    unsigned long long v;
-    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p.grid_count) : "memory");
-    const unsigned long long number = v / (TWO ? gridDim.x * EW : W4_MAX_CTAS);
-    if (lane == 0) launch_s = number;
-    if (blockIdx.x == 0) {
-      constexpr int SET = TWO ? 2 * W4_COUNTERS2 : W4_COUNTERS;
-      for (int i = lane; i < SET; i += 32) p.counters[(number & 1 ? 0 : SET) + i] = 0u;
+    if (TWO) {
+      unsigned long long v;
+      asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p.grid_count) : "memory");
+      const unsigned long long number = v / W4_COUNT;
+      if (lane == 0) launch_s = number;
+      if (blockIdx.x == 0)
+        for (int i = lane; i < 2 * W4_COUNTERS2; i += 32)
+          p.counters[(number & 1 ? 0 : 2 * W4_COUNTERS2) + i] = 0u;
+    } else if (blockIdx.x == 0) {
+      for (int i = lane; i < W4_COUNTERS; i += 32) p.counters_next[i] = 0u;
     }
   }
   if (warp < WT_EXPAND_WARP || warp >= S::EPI_WARP) __syncthreads();  // the schedule is there
@@ -792,7 +831,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
       const bool half = cta_rows <= S::HALF;
       if (TWO && !codes && it.cls >= 2 && !second) {
         second = true;
-        if (!w4_grid_wait(p.grid_count, (launch_s + 1) * (gridDim.x * EW), lim, abort_flag)) {
+        if (!w4_grid_wait(p.grid_count, (launch_s + 1) * W4_COUNT, lim, abort_flag)) {
           ok = false;
           break;
         }
@@ -850,24 +889,22 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
       }
     }
     if (!ok) {
-      set_status(p.status, MOE_ERR_TIMEOUT);
-      abort_s = 1;
+      give_up();
     }
     // every issued copy lands before the CTA may exit: the last use of stage i was its fill
     // number (used - 1 - i) / STAGES. (PAIR: the leader's barriers count both CTAs' rows,
     // and the peer waits for the leader at the last cluster barrier. Where either CTA gave
     // up, the copies are settled there, with what both have fetched.)
     if (PAIR && !codes && lane == 0) {
-      x_used_s = used;
-      x_half_s = (int)halves;
+      x_used_s[0] = used;
+      x_used_s[1] = (int)halves;
     }
     if (lane == 0 && (codes || leader))
       for (int i = 0; i < STAGES && i < used; ++i) {
         const volatile int never = 0;
         if (!mbar_wait(codes ? &code_full[i] : &x_full[i], (uint32_t)((used - 1 - i) / STAGES) & 1u,
                        WT_DRAIN_LIMIT_NS, PAIR && !codes ? abort_flag : &never)) {
-          set_status(p.status, MOE_ERR_TIMEOUT);
-          abort_s = 1;
+          give_up();
         }
       }
   } else if (warp == 1 || warp == 3) {
@@ -923,8 +960,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
         }
       }
       if (!ok) {
-        set_status(p.status, MOE_ERR_TIMEOUT);
-        abort_s = 1;
+        give_up();
       }
       if (elect_one()) {
         if (PAIR)
@@ -961,9 +997,10 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
                             abort_flag);
     };
     bool dry = true;  // the first turn, before there is work
+    it.cls = 0;
     it.c0 = 0;
     it.c1 = 1;
-    int kdim = 0;
+    int ng = 0;
     do {
 #pragma unroll 1
       for (int ch = it.c0; ch < it.c1; ++ch) {
@@ -978,7 +1015,6 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
           constexpr bool EARLY = BK == 128;
           uint4 cw[BK / 32];
           uint32_t sc[BK / 32];
-          const int kleft = kdim - ch * BK;
           bool few = true;
 #pragma unroll
           for (int i = 0; i < BK / 32; ++i) {
@@ -989,16 +1025,9 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
               continue;
             }
             sc[i] = lds16(base + scale_off + gi * scale_pitch);
-            if (32 * i >= kleft) sc[i] = 0u;
+            if (ch * (BK >> gl2) + gi >= ng) sc[i] = 0u;  // behind K: x is zero there, the scale not this row's
             few = few && w4_scale_is_short(sc[i]);
           }
-          // Behind K x is zero, but the codes there read as -8 and the scale is another row's
-          // or, in a short last group, this row's, which times -8 may be infinite: zero too.
-          // (K is a multiple of the 32 columns that a granule holds.)
-          if (kleft < BK)
-#pragma unroll
-            for (int i = 0; i < BK / 32; ++i)
-              if (32 * i >= kleft) sc[i] = 0u;
           few = __all_sync(0xffffffffu, few);
           if (!dry && !slot_free()) {
             ok = false;
@@ -1019,9 +1048,15 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[i * 16 + j * 4 + e] = w4_pair_scaled(w[j], e, ss, ms);
             }
-            if (!few)  // a scale of another origin: code - 8 (exact) came out above
+            if (!few) {
+              // A scale of another origin, or a large one: code - 8 (exact) came out above.
+              // Codes behind K, in a short last group, read as -8, which such a scale may
+              // take to infinity: zero. (K is a multiple of the 32 columns of a granule.)
+              const int left = p.cls[it.cls].K - ch * BK - 64 * h;
 #pragma unroll
-              for (int k = 0; k < 32; ++k) v[k] = mul_bf16x2(v[k], sc[2 * h + (k >> 4)] * 0x10001u);
+              for (int k = 0; k < 32; ++k)
+                v[k] = mul_bf16x2(v[k], 32 * (k >> 4) < left ? sc[2 * h + (k >> 4)] * 0x10001u : 0u);
+            }
             tmem_st_x32(t_slot + h * 32, v);
           }
           tmem_st_wait();
@@ -1050,11 +1085,10 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
       }
       if (!ok || !walk.next(it)) break;
       if (TWO) layout(wt_cta_f<BN, EPI>(it.cls >> 1) == 64);
-      kdim = p.cls[it.cls].K;
+      ng = (p.cls[it.cls].K + p.group - 1) >> gl2;
     } while (true);
     if (!ok) {
-      set_status(p.status, MOE_ERR_TIMEOUT);
-      abort_s = 1;
+      give_up();
     }
   } else if (warp >= S::EPI_WARP) {
     // ---------------------------------------------------------------- epilogue
@@ -1070,7 +1104,7 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
       __threadfence();
       asm volatile("fence.proxy.async.global;" ::: "memory");
       __syncwarp();
-      if (lane == 0) atomicAdd(p.grid_count, 1ull);
+      if (lane == 0) atomicAdd(p.grid_count, blockIdx.x || ew ? 1ull : W4_COUNT - (gridDim.x * EW - 1));
     };
     while (ok && walk.next(it)) {
       const W4Class& c = p.cls[it.cls];
@@ -1210,12 +1244,13 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
         // the last of the tile's walkers to get here adds the parts, in the order of K
         __threadfence();
         __syncwarp();
-        const int set = (int)(launch_s & 1);
-        unsigned* const counters = p.counters + (TWO ? (2 * set + phase) * W4_COUNTERS2 : set * W4_COUNTERS);
+        unsigned* const counter = p.counters + (TWO ? (2 * (int)(launch_s & 1) + phase) * W4_COUNTERS2 : 0) +
+                                  (it.wa * CTAS + (int)rank) * EW + ew;
         unsigned n = 0;
-        if (lane == 0) n = atomicAdd(&counters[(it.wa * CTAS + (int)rank) * EW + ew], 1u);
+        if (lane == 0) n = atomicAdd(counter, 1u);
         n = __shfl_sync(0xffffffffu, n, 0);
         if (n == (unsigned)(it.wb - it.wa)) {
+          if (!TWO && lane == 0) *counter = 0u;  // whether a launch of the other product follows or not
           __threadfence();
 #pragma unroll 1
           for (int c0 = cfirst; c0 < rows; c0 += CSTEP) {
@@ -1235,44 +1270,21 @@ __global__ void __launch_bounds__(WtShape<BN>::THREADS, 1)
     }
     if (!left_first) leave_first();
     if (!ok) {
-      set_status(p.status, MOE_ERR_TIMEOUT);
-      abort_s = 1;
+      give_up();
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (PAIR) {
-    if (threadIdx.x == 0 && abort_s) st_cluster(mapa_shared(smem_u32(&peer_abort_s), rank ^ 1u), 1u);
-    __syncwarp();
     cluster_sync_all();  // neither CTA leaves while the other may signal it or read its memory
-    if (abort_s | peer_abort_s) {  // (alike in both CTAs)
-      // Rows that one CTA fetched and the other did not: stage by stage the barrier gets the
-      // expectation, or the bytes, that it lacks. A stage is fetched again only after a
-      // product has read it, so it lacks at most its last fill.
-      if (leader && warp == 2 && lane == 0) {
-        const int own = x_used_s, peer = (int)ld_cluster(mapa_shared(smem_u32(&x_used_s), 1u));
-        const uint32_t halves = own > peer ? (uint32_t)x_half_s : ld_cluster(mapa_shared(smem_u32(&x_half_s), 1u));
-        const int used = max(own, peer);
-        for (int n = min(own, peer); n < used; ++n) {
-          const int i = n % STAGES;
-          const uint32_t bytes = (halves >> i & 1u ? S::HALF : S::B_ROWS) * BK * 2;
-          if (own > peer)
-            mbar_complete_tx(&x_full[i], bytes);
-          else
-            mbar_arrive_expect_tx(&x_full[i], bytes);
-        }
-        for (int i = 0; i < STAGES && i < used; ++i) {
-          const volatile int never = 0;
-          mbar_wait(&x_full[i], (uint32_t)((used - 1 - i) / STAGES) & 1u, WT_DRAIN_LIMIT_NS, &never);
-        }
-      }
+    if (__builtin_expect(settle_s, 0)) {  // (alike in both CTAs)
+      if (leader && warp == 2 && lane == 0)
+        wt_settle<STAGES>(x_full, x_used_s, S::HALF * BK * 2, S::B_ROWS * BK * 2);
       __syncwarp();
       cluster_sync_all();  // both CTAs' rows have landed
     }
   }
-  if (!TWO && threadIdx.x == 0)  // W4_MAX_CTAS a launch, however many CTAs it has
-    atomicAdd(p.grid_count, blockIdx.x ? 1ull : (unsigned long long)(W4_MAX_CTAS - (gridDim.x - 1)));
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_g<PAIR>(tmem, 512);

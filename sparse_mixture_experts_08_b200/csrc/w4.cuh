@@ -39,9 +39,10 @@ struct W4Class {
 constexpr int W4_MAX_CTAS = 160;              // CTAs of a launch
 constexpr int W4_COUNTERS = W4_MAX_CTAS * 8;  // one an epilogue warp: a product's cut tiles
 constexpr int W4_COUNTERS2 = W4_MAX_CTAS * 4; // the same where one launch does both products
-// Counter words of a workspace: two sets that even and odd launches of one product use; for
-// launches that do both, four of each kind of grid (even and odd launches, first and second
-// product). Each kind counts its own launches, and launches of one product count theirs.
+constexpr unsigned long long W4_COUNT = 1024; // what a launch of both products counts: more than its epilogue warps
+// Counter words of a workspace: two sets that the launches of the two products use in
+// turn; for launches that do both, four of each kind of grid (even and odd launches, first
+// and second product), as each kind counts its own launches.
 constexpr int W4_GRID_KINDS = 2;
 constexpr int W4_COUNTER_WORDS = 2 * W4_COUNTERS + W4_GRID_KINDS * 4 * W4_COUNTERS2;
 
@@ -50,12 +51,12 @@ struct W4Params {
   int n_classes;
   int group;    // 32, 64 or 128
   float* partial;           // w4_partial_bytes(): sums of tiles that CTAs share
-  // warps that have left their sums of a tile: two sets of W4_COUNTERS, or the four sets of
-  // W4_COUNTERS2 of this kind; a launch finds its own zero and zeroes the next one's
-  unsigned* counters;
-  // both products: epilogue warps that have left the first, of all launches of this kind;
-  // otherwise W4_MAX_CTAS for each launch that ended
-  unsigned long long* grid_count;
+  // warps that have left their sums of a tile, zero before the launch
+  unsigned* counters;       // [W4_COUNTERS], or the four sets of W4_COUNTERS2 of this kind
+  // [W4_COUNTERS]: zeroed here, used by the next product (a tile's last warp zeroes its own
+  // counter; this is for what a launch leaves whose waits ran out)
+  unsigned* counters_next;
+  unsigned long long* grid_count;  // both products: epilogue warps that have left the first
   int* status;
   unsigned long long wait_limit_ns;
   unsigned stall;  // test hook, 0 but for tests of the time limits (moe_debug_set_barrier_extra)
