@@ -27,8 +27,11 @@
  *    config structs and scalar out-parameters (bytes, moe_status_t*) are HOST
  *    pointers. The library allocates no device memory; scratch comes from the
  *    caller's workspace `ws` of `ws_bytes` bytes (size it with
- *    moe_workspace_size / moe_atomic_workspace_size, zero it once before first
- *    use: its first 4 bytes hold the device status word).
+ *    moe_workspace_size / moe_atomic_workspace_size and the like, zero it once before
+ *    first use: its first 4 bytes hold the device status word, the rest of its first
+ *    32 KiB counters that one call leaves to the next). One zeroed buffer may serve
+ *    calls of every kind and size that it is large enough for, one after the other;
+ *    calls that overlap on the GPU need one each.
  *  - Layouts are row-major with nn.Linear [out, in] weights:
  *      x [T, d]; w_router [m, d]; bias [m] fp32;
  *      w_gate, w_up [m, f, d]; w_down [m, d, f];   (ReLU experts: w_gate = W1, w_up = NULL, w_down = W2)

@@ -107,6 +107,11 @@ struct Layout {
   size_t lrank, tile_cnt, idx2, gmap, lis2, total;
 };
 
+// What one call leaves to the next, at the start of every workspace alike (so one buffer
+// may serve calls of all kinds): the status word, then the grid counts (offset 128) and the
+// counters (offset 256) of the 4-bit products.
+constexpr size_t STATE_BYTES = 256 + W4_COUNTER_WORDS * sizeof(unsigned);
+
 static Layout make_layout(const moe_config_t& c, const Plan& p) {
   Layout L;
   size_t off = 0;
@@ -117,9 +122,7 @@ static Layout make_layout(const moe_config_t& c, const Plan& p) {
   };
   const size_t Tk = (size_t)c.T * c.k;
   const size_t T = (size_t)c.T;
-  // the status word, then (in every layer's workspace alike) the grid counts (offset 128)
-  // and the counters (offset 256) of the 4-bit products
-  L.status = take(256 + W4_COUNTER_WORDS * sizeof(unsigned));
+  L.status = take(STATE_BYTES);
   L.logits = take(T * c.m * 4);
   L.idx = take(Tk * 4);
   L.w = take(Tk * 4);
@@ -1125,7 +1128,7 @@ static AtomicPlan make_atomic_plan(const moe_atomic_config_t& c) {
     off += align256(bytes);
     return o;
   };
-  p.status = take(256);
+  p.status = take(STATE_BYTES);
   p.zr = take((size_t)p.ksplit * c.T * c.Nr * 4);
   p.zc = take((size_t)p.ksplit * c.T * c.Nc * 4);
   p.idx = take((size_t)c.T * c.K * 4);

@@ -158,3 +158,23 @@ def test_stalled_products_time_out_and_the_next_calls_are_right(rows, d, f, stal
         y.fill_(float("nan"))
         moe.moe_grouped_ffn_w4(c, x, good, wq, None, None, y, ws)
         assert moe.moe_read_device_status(ws) == moe.OK and torch.equal(y, want)
+
+
+def test_one_buffer_for_atomic_and_4_bit_calls():
+    """What an atomic-expert call writes into a workspace leaves the 4-bit products' counters alone."""
+    ac = moe.make_atomic_config(8, 256, 64, 64, 16, moe.ATOMIC_SILU)
+    gen = torch.Generator().manual_seed(2)
+    ax, wr, wc, wi, wo = ((torch.randn(n, 256, generator=gen) / 16).to(torch.bfloat16).cuda()
+                          for n in (8, 64, 64, 4096, 4096))
+    out, first = torch.empty_like(ax), torch.empty_like(ax)
+    for rows, d, f in HEIGHTS[:6]:
+        c, wq, x, good = _grouped(rows, d, f)
+        want, y = torch.empty(rows, d, device="cuda"), torch.full((rows, d), float("nan"), device="cuda")
+        moe.moe_grouped_ffn_w4(c, x, good, wq, None, None, want, moe.w4_workspace(c))
+        size = max(moe.moe_w4_workspace_size(c), moe.moe_atomic_workspace_size(ac))
+        ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+        moe.moe_atomic_forward(ac, ax, wr, wc, wi, wo, first, ws)
+        moe.moe_grouped_ffn_w4(c, x, good, wq, None, None, y, ws)
+        moe.moe_atomic_forward(ac, ax, wr, wc, wi, wo, out, ws)
+        assert moe.moe_read_device_status(ws) == moe.OK
+        assert torch.equal(y, want) and torch.equal(out, first)
