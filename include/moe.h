@@ -351,8 +351,7 @@ MOE_API moe_status_t moe_layer_forward_fp8_codes(const moe_config_t* cfg, const 
  *   sum_out (nullable) = r, y (nullable) = y, both rounded to `dtype`;
  *   codes, scales (nullable, both or neither) = E4M3 codes [rows, d] and fp32 scales
  *   [rows] of y in moe_quantize_e4m3's format, taken from the fp32 y (not from its
- *   rounding to bf16; y / scale is y times the scale's fp32 reciprocal). r and y are fp32
- *   in between.
+ *   rounding to bf16). r and y are fp32 in between.
  * x, residual, sum_out, y [rows, d] and weight [d] are `dtype` (moe_dtype_t), contiguous
  * and 16-byte aligned; scales 4-byte aligned. sum_out and y may be x or residual
  * themselves (not each other, and no partial overlap). At least one of y and codes is

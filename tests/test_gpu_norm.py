@@ -261,3 +261,51 @@ def test_binding_refuses_other_types_and_sizes():
         with pytest.raises(moe.MoEError):
             moe.moe_add_rmsnorm(x, a["residual"], a["weight"], 1e-6, a["y"], sum_out=a["sum_out"], codes=a["codes"],
                                 scales=a["scales"])
+
+
+def _e4m3_ties():
+    """The numbers halfway between two neighbouring E4M3 numbers."""
+    v = torch.arange(0x7F, dtype=torch.uint8).view(torch.float8_e4m3fn).double()
+    return (v[1:] + v[:-1]) / 2
+
+
+@pytest.mark.parametrize("size", [1.0, 1e4, 3e-5, 1e30, 1e-35])
+def test_codes_are_those_of_the_rounded_quotient(size):
+    """Rows of one and minus one have a root mean square of exactly 1, so y is the weight, bit for bit: values around
+    every tie between two codes, whose quotients by the scale decide which of them it is."""
+    gen = torch.Generator().manual_seed(8)
+    ties = _e4m3_ties()
+    steps = torch.arange(-2, 3)
+    d = len(ties) * len(steps) + 10
+    assert d % 16 == 0
+    sign = torch.where(torch.rand(2, d, generator=gen) < 0.5, -1.0, 1.0).cuda()
+    for _ in range(200):
+        top = (1 + torch.rand(1, generator=gen)) * size
+        scale = top / 448
+        v = (ties * scale.double()).float()
+        w = (v[:, None].view(torch.int32) + steps).to(torch.int32).view(torch.float32).reshape(-1)
+        w = torch.cat([w, top.expand(10)]).minimum(top).cuda()
+        y, codes, scales = torch.empty_like(sign), torch.empty(2, d, dtype=torch.uint8, device="cuda"), torch.empty(2, device="cuda")
+        moe.moe_add_rmsnorm(sign, None, w, 0.0, y, codes=codes, scales=scales)
+        assert torch.equal(y, sign * w) and (scales.cpu() == scale).all()
+        want = (y.cpu() / scale).to(torch.float8_e4m3fn)
+        assert torch.equal(codes.cpu(), want.view(torch.uint8))
+
+
+@pytest.mark.parametrize("d", [256, 512, 4096, 16384])
+def test_codes_of_bf16_rows_are_the_quantizers(d):
+    """The same bf16 rows through the norm and through moe_quantize_e4m3: one format."""
+    gen = torch.Generator().manual_seed(d)
+    x = torch.where(torch.rand(3, d, generator=gen) < 0.5, -1.0, 1.0).to(torch.bfloat16).cuda()
+    codes, want = (torch.empty(3, d, dtype=torch.uint8, device="cuda") for _ in range(2))
+    scales, want_scales = (torch.empty(3, device="cuda") for _ in range(2))
+    y = torch.empty_like(x)
+    for i in range(50):
+        w = (torch.randn(d, generator=gen) * 2.0 ** torch.randint(-60, 60, (1,), generator=gen)).to(torch.bfloat16).cuda()
+        w[7] = (-0.0, 1.0, float("inf"), float("nan"))[i % 4]
+        moe.moe_add_rmsnorm(x, None, w, 0.0, y, codes=codes, scales=scales)
+        moe.moe_quantize_e4m3(y, want, want_scales)
+        nan = torch.isnan(y)  # (which has two codes)
+        assert torch.equal(y[~nan], (x * w)[~nan]) and torch.equal(nan, torch.isnan(w).expand(3, d))
+        assert torch.equal(scales, want_scales) and torch.equal(codes & 0x7F, want & 0x7F)
+        assert torch.equal(codes[~nan], want[~nan])
