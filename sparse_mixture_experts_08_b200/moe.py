@@ -327,19 +327,31 @@ def moe_layer_forward_fp8(cfg, x, w_router, bias, wq, out, ws, logits_out=None, 
         _p(ws), ws.numel(), _stream(stream)))
 
 
+def _fp8_experts(fn, cfg, wq, specs):
+    """moe_fp8_experts_t of wq, and the addresses of specs' tensors. Entries that the layer does not use are any."""
+    u8, f32, d = torch.uint8, torch.float32, cfg.d
+    specs = list(specs)
+    for pre, n, f in (("", cfg.m, cfg.f), ("sh_", cfg.n_shared, cfg.f_shared)):
+        for key, rows in (("gate", f), ("up", f), ("down", d)):
+            used = n > 0 and (key != "up" or cfg.act == SWIGLU)
+            q, s = wq.get(pre + key), wq.get(pre + key + "_scale")
+            specs += ((q, u8, n * f * d), (s, f32, n * rows)) if used else ((q, None, 0), (s, None, 0))
+    ptrs = _pointers(fn, specs)
+    return MoEFp8Experts(*ptrs[-12:]), ptrs[:-12]
+
+
 def moe_layer_forward_fp8_codes(cfg, x, x_codes, x_scales, w_router, bias, wq, out, ws, logits_out=None,
                                 topk_idx_out=None, topk_w_out=None, counts_out=None, lis_out=None, h_out=None,
                                 h_shared_out=None, perm_out=None, stream=None):
     """moe_layer_forward_fp8 for tokens that come with E4M3 codes [T, d] and scales [T] (moe_add_rmsnorm's)."""
-    n, bf16, f32 = cfg.T * cfg.d, torch.bfloat16, torch.float32
-    _pointers("moe_layer_forward_fp8_codes", (
-        (x, bf16, n), (x_codes, torch.uint8, n), (x_scales, f32, cfg.T), (w_router, bf16, cfg.m * cfg.d),
-        (bias, f32, cfg.m), (out, bf16, n), (ws, None, 0)))
-    st = MoEFp8Experts(**{k: _p(wq.get(k)) for k, _ in MoEFp8Experts._fields_})
+    n, tasks, u8, bf16, f32, i32 = cfg.T * cfg.d, cfg.T * cfg.k, torch.uint8, torch.bfloat16, torch.float32, torch.int32
+    st, (xp, xcp, xsp, rp, bp, op, *outs, wsp) = _fp8_experts("moe_layer_forward_fp8_codes", cfg, wq, (
+        (x, bf16, n), (x_codes, u8, n), (x_scales, f32, cfg.T), (w_router, bf16, cfg.m * cfg.d), (bias, f32, cfg.m),
+        (out, bf16, n), (logits_out, f32, cfg.T * cfg.m), (topk_idx_out, i32, tasks), (topk_w_out, f32, tasks),
+        (counts_out, i32, cfg.m), (lis_out, u8, LIS_BYTES), (h_out, bf16, tasks * cfg.f),
+        (h_shared_out, bf16, cfg.n_shared * cfg.T * cfg.f_shared), (perm_out, i32, tasks), (ws, None, 0)))
     _check("moe_layer_forward_fp8_codes", lib().moe_layer_forward_fp8_codes(
-        ctypes.byref(cfg), _p(x), _p(x_codes), _p(x_scales), _p(w_router), _p(bias), ctypes.byref(st), _p(out),
-        _p(logits_out), _p(topk_idx_out), _p(topk_w_out), _p(counts_out), _p(lis_out), _p(h_out), _p(h_shared_out),
-        _p(perm_out), _p(ws), ws.numel(), _stream(stream)))
+        ctypes.byref(cfg), xp, xcp, xsp, rp, bp, ctypes.byref(st), op, *outs, wsp, ws.numel(), _stream(stream)))
 
 
 def moe_add_rmsnorm(x, residual, weight, eps, y, sum_out=None, codes=None, scales=None, stream=None):

@@ -208,3 +208,78 @@ def test_binding_checks_types_and_sizes(monkeypatch):
                dict(down_scale=Fake(3, 3, 96, dtype=torch.float16)), dict(group=32)):
         with pytest.raises(moe.MoEError):
             experts(moe.SWIGLU, **kw)
+
+
+@pytest.mark.parametrize("act,n_shared", [(moe.SWIGLU, 2), (moe.RELU, 0)])
+def test_binding_checks_every_tensor_of_the_8_bit_layer_on_codes(monkeypatch, act, n_shared):
+    """Weights, scales and optional outputs of another type, too small, strided or on the host are refused before the
+    library is called; entries that the layer does not use are not looked at."""
+    import torch
+    from sparse_mixture_experts_08_b200 import moe as binding
+
+    class Fake:  # a tensor that says it is on the device
+        def __init__(self, *shape, dtype):
+            self.t, self.dtype, self.shape, self.is_cuda = torch.zeros(shape, dtype=dtype), dtype, shape, True
+            self.numel, self.is_contiguous, self.data_ptr = self.t.numel, self.t.is_contiguous, self.t.data_ptr
+
+        def get_device(self):
+            return 0
+
+    calls = []
+
+    class Library:
+        @staticmethod
+        def moe_layer_forward_fp8_codes(*args):
+            calls.append(args)
+            return moe.OK
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(binding, "lib", lambda: Library)
+    T, d, f, m, k, fs = 4, 32, 48, 3, 2, 64
+    u8, bf16, f32, i32 = torch.uint8, torch.bfloat16, torch.float32, torch.int32
+    up = act == moe.SWIGLU
+    c = moe.make_config(T, d, f, m, k, n_shared=n_shared, f_shared=fs if n_shared else 0, act=act)
+    shapes = {"gate": (m, f, d), "down": (m, d, f)}
+    if up:
+        shapes["up"] = (m, f, d)
+    if n_shared:
+        shapes.update({"sh_gate": (n_shared, fs, d), "sh_up": (n_shared, fs, d), "sh_down": (n_shared, d, fs)})
+    wq = {}
+    for key, shape in shapes.items():
+        wq[key], wq[key + "_scale"] = Fake(*shape, dtype=u8), Fake(*shape[:2], dtype=f32)
+    good = {"x": Fake(T, d, dtype=bf16), "x_codes": Fake(T, d, dtype=u8), "x_scales": Fake(T, dtype=f32),
+            "w_router": Fake(m, d, dtype=bf16), "bias": Fake(m, dtype=f32), "out": Fake(T, d, dtype=bf16),
+            "logits_out": Fake(T, m, dtype=f32), "topk_idx_out": Fake(T, k, dtype=i32),
+            "topk_w_out": Fake(T, k, dtype=f32), "counts_out": Fake(m, dtype=i32),
+            "lis_out": Fake(binding.LIS_BYTES, dtype=u8), "h_out": Fake(T * k, f, dtype=bf16),
+            "perm_out": Fake(T * k, dtype=i32)}
+    if n_shared:
+        good["h_shared_out"] = Fake(n_shared * T, fs, dtype=bf16)
+
+    def call(wq=wq, **kw):
+        a = dict(good, **kw)
+        binding.moe_layer_forward_fp8_codes(c, wq=wq, ws=Fake(1 << 16, dtype=u8), stream=0, **a)
+
+    call()
+    call(wq=dict(wq, **({} if up else {"up": Fake(1, dtype=f32)}), **({} if n_shared else {"sh_down": Fake(1, dtype=f32)})))
+    assert len(calls) == 2
+    # the library's arguments in its order
+    st = calls[0][6]._obj
+    assert calls[0][1:6] == tuple(good[key].data_ptr() for key in ("x", "x_codes", "x_scales", "w_router", "bias"))
+    assert calls[0][7:15] == tuple(good[key].data_ptr() for key in (
+        "out", "logits_out", "topk_idx_out", "topk_w_out", "counts_out", "lis_out", "h_out")) + (
+        good["h_shared_out"].data_ptr() if n_shared else None,)
+    assert calls[0][15] == good["perm_out"].data_ptr()
+    for name, _ in binding.MoEFp8Experts._fields_:
+        assert getattr(st, name) == (wq[name].data_ptr() if name in wq else None), name
+    double = torch.float64
+    for where in (good, wq):
+        for name, t in where.items():
+            strided = Fake(*t.shape, dtype=t.dtype)
+            strided.is_contiguous = lambda: False
+            for bad in (Fake(t.numel() - 1, dtype=t.dtype), Fake(*t.shape, dtype=double), strided,
+                        torch.zeros(t.shape, dtype=t.dtype)):
+                with pytest.raises(moe.MoEError) as e:
+                    call(**{name: bad}) if where is good else call(wq=dict(wq, **{name: bad}))
+                assert e.value.status == moe.ERR_INVALID_ARG, name
+    assert len(calls) == 2
