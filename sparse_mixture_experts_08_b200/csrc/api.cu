@@ -274,8 +274,8 @@ struct Fp8Io {
   float* sx_sh;    // [T]
   uint8_t* hq_sh;  // [n_shared T, f_shared]
   float* sh_sh;    // [n_shared T]
-  // codes and scales of x that came with the call (nullable: x is quantized here), and
-  // where each task's row goes
+  // codes and scales of x that came with the call (nullable: x is quantized here; xq then
+  // holds the codes in segment order already), and where each task's row goes
   const uint8_t* x_codes;   // [T, d]
   const float* x_scales;    // [T]
   const int32_t* inv_perm;  // [T k]
@@ -394,8 +394,7 @@ static moe_status_t run_ffn(const moe_config_t& c, const Plan& pl, const FfnIo& 
   const bool tc = c.dtype == MOE_BF16;
   const Fp8Io* q8 = io.q8;
   auto kbl = [&](int K) { return q8 ? kblocks8(K) : kblocks(K); };
-  if (q8 && q8->x_codes) {  // codes that came with x: moved to segment order (two codes as one 16-bit element)
-    MOE_CUDA(launch_permute_rows(MOE_BF16, (int)io.routed_rows, c.k, c.d / 2, q8->x_codes, q8->inv_perm, q8->xq, s));
+  if (q8 && q8->x_codes) {  // codes that came with x
     MOE_CUDA(launch_permute_scales((int)io.routed_rows, c.k, q8->x_scales, q8->inv_perm, q8->sx, s));
   } else if (q8) {  // E4M3 rows of the up projection's inputs
     MOE_CUDA(launch_quantize_e4m3(io.routed_rows, c.d, io.x_perm, c.d, q8->xq, c.d, q8->sx, s));
@@ -766,6 +765,11 @@ static moe_status_t layer_forward_impl(const moe_config_t& c, const void* x, con
   const long long Tk = (long long)c.T * c.k;
 
   float* w_perm = at<float>(ws, L.w_perm);
+  // what goes to segment order: x, or the codes that came with it (two as one 16-bit element)
+  const Fp8Layout F = make_fp8_layout(c, L.total);
+  const void* const rows = x_codes ? (const void*)x_codes : x;
+  void* const rows_perm = x_codes ? at<void>(ws, F.xq) : at<void>(ws, L.x_perm);
+  const int rows_d = x_codes ? c.d / 2 : c.d;
   MOE_TRY(mark_stage(0, s));
   if (fused_route_ok(c)) {
     // router + top-k + per-tile counts and ranks in the GEMM epilogue, then one
@@ -776,8 +780,8 @@ static moe_status_t layer_forward_impl(const moe_config_t& c, const void* x, con
     MOE_TRY(mark_stage(1, s));
     MOE_TRY(mark_stage(2, s));
     MOE_TRY(mark_stage(3, s));
-    MOE_CUDA(launch_route_scatter(c.dtype, c.T, c.k, c.m, c.d, tile_cnt, idx, lrank, w, x, counts, offsets, lis, perm,
-                                  inv_perm, w_perm, at<void>(ws, L.x_perm), status, s));
+    MOE_CUDA(launch_route_scatter(c.dtype, c.T, c.k, c.m, rows_d, tile_cnt, idx, lrank, w, rows, counts, offsets, lis,
+                                  perm, inv_perm, w_perm, rows_perm, status, s));
   } else {
     MOE_CUDA(launch_route(c, x, w_router, bias, nullptr, logits_out, logits, idx, w, status, s, true));
     if (w4 && small_dispatch_ok(Tk, c.m)) {  // (bf16 rows; stage 3 has no launch of its own)
@@ -789,8 +793,7 @@ static moe_status_t layer_forward_impl(const moe_config_t& c, const void* x, con
       MOE_CUDA(launch_route_index(1, c.T, c.k, c.m, idx, counts, offsets, lis, start, status, s));
       MOE_CUDA(launch_rank(c.T, c.k, c.m, idx, offsets, start, w, perm, inv_perm, w_perm, status, s));
       MOE_TRY(mark_stage(3, s));
-      if (!x_codes)  // (given codes are moved instead, in run_ffn)
-        MOE_CUDA(launch_permute_rows(c.dtype, (int)Tk, c.k, c.d, x, inv_perm, at<void>(ws, L.x_perm), s));
+      MOE_CUDA(launch_permute_rows(c.dtype, (int)Tk, c.k, rows_d, rows, inv_perm, rows_perm, s));
     }
   }
   MOE_TRY(mark_stage(4, s));
@@ -822,7 +825,6 @@ static moe_status_t layer_forward_impl(const moe_config_t& c, const void* x, con
   int ksplit = w4 ? 1 : pl.ksplit, kbps = pl.kbps;
   Fp8Io q8;
   if (wq) {
-    const Fp8Layout F = make_fp8_layout(c, L.total);
     q8 = {wq,
           at<uint8_t>(ws, F.xq), at<float>(ws, F.sx), at<uint8_t>(ws, F.hq), at<float>(ws, F.sh),
           at<uint8_t>(ws, F.xq_sh), at<float>(ws, F.sx_sh), at<uint8_t>(ws, F.hq_sh), at<float>(ws, F.sh_sh),

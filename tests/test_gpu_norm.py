@@ -309,3 +309,21 @@ def test_codes_of_bf16_rows_are_the_quantizers(d):
         assert torch.equal(y[~nan], (x * w)[~nan]) and torch.equal(nan, torch.isnan(w).expand(3, d))
         assert torch.equal(scales, want_scales) and torch.equal(codes & 0x7F, want & 0x7F)
         assert torch.equal(codes[~nan], want[~nan])
+
+
+@pytest.mark.parametrize("T", [300, 8200])  # three routing launches, and the fused router with its scatter
+def test_given_codes_are_moved_in_place_of_the_rows(T):
+    """The 8-bit layer on given codes writes no bf16 rows in segment order: on a zeroed workspace it leaves as many
+    bytes untouched as those rows have (less what random rows hold in zero bytes)."""
+    gen = torch.Generator().manual_seed(T)
+    d, f, m, k = 64, 64, 8, 2
+    wq = moe.quantize_experts(_bf16(gen, m, f, d), _bf16(gen, m, f, d), _bf16(gen, m, d, f))
+    c = moe.make_config(T, d, f, m, k)
+    x, wr = _bf16(gen, T, d) * 16, _bf16(gen, m, d)
+    codes, scales = torch.empty(T, d, dtype=torch.uint8, device="cuda"), torch.empty(T, device="cuda")
+    moe.moe_quantize_e4m3(x, codes, scales)
+    a, b, wa, wb = torch.empty_like(x), torch.empty_like(x), moe.fp8_workspace(c), moe.fp8_workspace(c)
+    moe.moe_layer_forward_fp8(c, x, wr, None, wq, a, wa)
+    moe.moe_layer_forward_fp8_codes(c, x, codes, scales, wr, None, wq, b, wb)
+    assert torch.equal(a, b)
+    assert int((wa != 0).sum()) - int((wb != 0).sum()) > 0.95 * T * k * d * 2
