@@ -10,6 +10,7 @@ smallest step) on top of the fp32 part.
 import pytest
 import torch
 
+import norm_exact as N
 import sparse_mixture_experts_08_b200 as moe
 from gpu_helpers import require_gpu
 
@@ -327,3 +328,23 @@ def test_given_codes_are_moved_in_place_of_the_rows(T):
     moe.moe_layer_forward_fp8_codes(c, x, codes, scales, wr, None, wq, b, wb)
     assert torch.equal(a, b)
     assert int((wa != 0).sum()) - int((wb != 0).sum()) > 0.95 * T * k * d * 2
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,d", N.SHAPES)
+def test_no_vector_is_left_out_of_the_sum(rows, d, dtype):
+    """Within the roundings that the sum of squares has on its way, not one for each of its terms: y of fp32 rows, and
+    the fp32 scale of the codes of either type."""
+    gen = torch.Generator().manual_seed(rows + d)
+    x, r, w = (t.cuda() for t in N.inputs(gen, rows, d, dtype))
+    for residual in (None, r):
+        y, with_codes = torch.empty_like(x), d % 16 == 0
+        codes = torch.empty(rows, d, dtype=torch.uint8, device="cuda") if with_codes else None
+        scales = torch.empty(rows, device="cuda") if with_codes else None
+        moe.moe_add_rmsnorm(x, residual, w, 1e-5, y, codes=codes, scales=scales)
+        ref = N.norm64(x, residual, w)
+        rel = N.REL + (torch.finfo(dtype).eps / 2 if dtype != torch.float32 else 2.0 ** -24)
+        assert ((y.to(F64) - ref).abs() <= rel * ref.abs()).all()
+        if with_codes:
+            want = ref.abs().amax(1) / 448
+            assert ((scales.to(F64) - want).abs() <= (N.REL + 2 * 2.0 ** -24) * want).all()

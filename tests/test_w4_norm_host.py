@@ -4,6 +4,7 @@ import ctypes
 
 import pytest
 
+import norm_exact as N
 import sparse_mixture_experts_08_b200 as moe
 from sparse_mixture_experts_08_b200.moe import MoEConfig, MoEW4Experts
 
@@ -283,3 +284,21 @@ def test_binding_checks_every_tensor_of_the_8_bit_layer_on_codes(monkeypatch, ac
                     call(**{name: bad}) if where is good else call(wq=dict(wq, **{name: bad}))
                 assert e.value.status == moe.ERR_INVALID_ARG, name
     assert len(calls) == 2
+
+
+@pytest.mark.parametrize("rows,d", N.SHAPES)
+def test_a_vector_left_out_of_the_norm_is_seen(rows, d):
+    """The bound of test_gpu_norm.py's comparison, with the mistake in the reference: any one 16-byte vector of a row
+    missing from the sum of squares moves y, and the codes' scale, by several times that."""
+    import torch
+    gen = torch.Generator().manual_seed(rows + d)
+    for dtype, vec in ((torch.float32, 4), (torch.bfloat16, 8)):
+        x, r, w = N.inputs(gen, rows, d, dtype)
+        for residual in (None, r):
+            ref = N.norm64(x, residual, w)
+            s = x.to(N.F64) + (0 if residual is None else residual.to(N.F64))
+            least = int((s * s).view(rows, d // vec, vec).sum(2).amax(0).argmin())  # the vector that matters least
+            bad = N.norm64(x, residual, w, without=(vec * least, vec * least + vec))
+            assert ((bad - ref).abs() > 3 * N.REL * ref.abs()).all(1).any()
+            top, want = bad.abs().amax(1), ref.abs().amax(1)
+            assert ((top - want).abs() > 3 * (N.REL + 2 * 2.0 ** -24) * want).any()
