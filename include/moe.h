@@ -356,8 +356,9 @@ MOE_API moe_status_t moe_layer_forward_fp8_codes(const moe_config_t* cfg, const 
  * and 16-byte aligned; scales 4-byte aligned. sum_out and y may be x or residual
  * themselves (not each other, and no partial overlap). At least one of y and codes is
  * given. eps >= 0 and finite; a row of zeros with eps = 0 gives NaN, as the formula does. The
- * sum of a row's squares is fp32 too: a row where it overflows gives y = 0. A row whose
- * scale would round to 0 (max |y| below 448 * 2^-150) gets scale 1 and codes of zero.
+ * sum of a row's squares is fp32 too; where it would leave fp32's range, it is taken of the
+ * row times a power of two. A row whose scale would round to 0 (max |y| below
+ * 448 * 2^-150) gets scale 1 and codes of zero.
  * rows >= 0 (0: nothing is launched); d a multiple of 8 (of 16 with codes) up to 32768
  * (MOE_ERR_UNSUPPORTED otherwise). No workspace. Asynchronous on `stream`. */
 MOE_API moe_status_t moe_add_rmsnorm(int64_t rows, int32_t d, int32_t dtype, float eps, const void* x,

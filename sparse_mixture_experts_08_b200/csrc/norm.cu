@@ -79,7 +79,7 @@ __device__ __forceinline__ float row_reduce(float v, float* buf) {
 // method, q + (v - q s) r with the remainder exact in a fused multiply-add, corrects it.
 // (The theorem wants a q within one unit; for every mantissa of s, every tie and the numbers
 // v around it the corrected quotient was compared with the division's: no other one. A
-// division an element took 29.3 us for 4096 x 4096 bf16 rows, v r alone 25.7, this 26.6.)
+// division an element took 29.3 us for 4096 x 4096 bf16 rows, v r alone 25.7, this 26.7.)
 // Quotients far below E4M3's smallest tie, 2^-10, may be off.
 __device__ __forceinline__ float quotient(float v, float s, float r) {
   const float q = v * r;
@@ -91,12 +91,18 @@ __device__ __forceinline__ float quotient(float v, float s, float r) {
 // half of them idle at 2056 fp32 elements, 8191 rows took 32 us, so 27).
 // Vector i of thread t starts at element N (i TPR + t). An element is read and written by the same thread, in that
 // order, so sum_out or y may be x or residual themselves.
-template <typename T, bool WIDE, int VPT, int MAX_THREADS>
-__global__ void __launch_bounds__(MAX_THREADS)
+// MIN_BLOCKS keeps the registers that the rare rows of large and small squares would take
+// from costing the others a block an SM.
+template <typename T, bool WIDE, int VPT, int MAX_THREADS,
+          int MIN_BLOCKS = !WIDE                             ? (VPT == 1 ? 16 : 10)
+                           : VPT == 2                        ? (MAX_THREADS == 256 ? 5 : 3)
+                           : VPT == 1 || MAX_THREADS == 512 ? 2
+                                                             : 1>
+__global__ void __launch_bounds__(MAX_THREADS, MIN_BLOCKS)
     add_rmsnorm_kernel(long long rows, int d, float eps, const T* x, const T* residual,
                        const T* __restrict__ weight, T* sum_out, T* y, uint8_t* __restrict__ codes,
                        float* __restrict__ scales) {
-  __shared__ float red[2][32];
+  __shared__ float red[4][32];
   const int TPR = WIDE ? blockDim.x : 32;
   const int t = WIDE ? threadIdx.x : threadIdx.x & 31;
   const long long row = WIDE ? blockIdx.x : (long long)blockIdx.x * (MAX_THREADS / 32) + (threadIdx.x >> 5);
@@ -153,8 +159,38 @@ __global__ void __launch_bounds__(MAX_THREADS)
       }
   }
   ss = row_reduce<WIDE, false>(ss, red[0]);
-  const float inv = 1.f / sqrtf(ss / (float)d + eps);
+  float inv = 1.f / sqrtf(ss / (float)d + eps);
   float amax = 0.f;
+  // Squares that may have left fp32's range, above or, beside an eps below 2^-60, below
+  // (one verdict a row): the row times a power of two that takes its largest element to
+  // [1, 2), and another sum. Rows with an infinity keep inv = 0, rows of zeros what eps
+  // gives. (What the test costs the other rows: 4096 x 4096 bf16 26.8 -> 27.0 us, 8191 x
+  // 2056 fp32 26.8 -> 27.6, 16 x 4096 within 0.05.)
+  if (__builtin_expect(!(inv >= 0x1p-63f && inv <= 0x1p30f), 0)) {
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+      for (int j = 0; j < N; ++j) top = fmaxf(top, fabsf(r[i][j]));
+    top = row_reduce<WIDE, true>(top, red[2]);
+    if (top > 0.f && top <= 3.4028235e38f) {
+      const int e = ilogbf(top);
+      // 2^-e in two factors: it may be no fp32 number itself
+      const float f0 = __int_as_float((127 - e / 2) << 23), f1 = __int_as_float((127 - (e - e / 2)) << 23);
+      const float eps_e = eps * f0 * f0 * f1 * f1;
+      if (eps_e <= 0x1p100f) {  // (else the squares are nothing beside eps, and inv is right)
+        ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            r[i][j] = r[i][j] * f0 * f1;
+            ss = fmaf(r[i][j], r[i][j], ss);
+          }
+        inv = 1.f / sqrtf(row_reduce<WIDE, false>(ss, red[3]) / (float)d + eps_e);
+      }
+    }
+  }
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
     if (i * TPR + t < nv) {

@@ -348,3 +348,46 @@ def test_no_vector_is_left_out_of_the_sum(rows, d, dtype):
         if with_codes:
             want = ref.abs().amax(1) / 448
             assert ((scales.to(F64) - want).abs() <= (N.REL + 2 * 2.0 ** -24) * want).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("d", [64, 256, 512, 2048, 4096, 16384, 32768])
+def test_rows_whose_squares_leave_the_range(d, dtype):
+    """Rows near the largest and the smallest numbers, whose squares fp32 cannot hold: the formula's values, for every
+    number of threads a row takes; ordinary rows between them are not touched by that."""
+    gen = torch.Generator().manual_seed(d)
+    sizes = [2.0 ** e for e in (125, 100, 64, 0, -40, -62, -64, -75, -100, -120)]
+    x = (0.5 + torch.rand(len(sizes), d, generator=gen)) * torch.tensor(sizes)[:, None]
+    x = (x * (torch.randint(0, 2, x.shape, generator=gen) * 2 - 1)).to(dtype).cuda()
+    w = (0.5 + torch.rand(d, generator=gen)).to(dtype).cuda()
+    half = torch.finfo(dtype).eps / 2
+    for eps in (0.0, 1e-38, 1e-30, 1e-20, 1e-12, 1e-5):
+        y = torch.empty_like(x)
+        codes, scales = torch.empty(x.shape, dtype=torch.uint8, device="cuda"), torch.empty(len(sizes), device="cuda")
+        moe.moe_add_rmsnorm(x, None, w, eps, y, codes=codes, scales=scales)
+        eps32 = torch.tensor(eps, dtype=torch.float32).item()
+        ref = norm64(x, None, w, eps32)
+        # below 2^-126 y is off by up to 2^-150, or half a step of bf16's there, 2^-134
+        tiny = 2.0 ** -149 if dtype == torch.float32 else 2.0 ** -133
+        assert ((y.to(F64) - ref).abs() <= (half + N.REL) * ref.abs() + tiny).all(), eps
+        top = ref.abs().amax(1)
+        ok = top > 2.0 ** -100
+        assert ((scales.to(F64) - top / 448).abs()[ok] <= (N.REL + 2.0 ** -23) * top[ok] / 448).all()
+        assert not torch.isnan(codes.view(torch.float8_e4m3fn).float()).any()
+        lone = torch.empty(1, d, dtype=dtype, device="cuda")
+        moe.moe_add_rmsnorm(x[3:4].contiguous(), None, w, eps, lone)
+        assert torch.equal(lone[0], y[3])
+
+
+def test_infinities_zeros_and_nan_beside_large_and_small_rows():
+    d = 1024
+    x = torch.ones(6, d)
+    x[0, 5], x[1, 7], x[2], x[3], x[4], x[5, 1:] = float("inf"), float("nan"), 0.0, 1e30, 1e-30, 0.0
+    x[4, 3], x[5, 0] = 1e-45, 3e38
+    w = torch.ones(d, device="cuda")
+    y = torch.empty(6, d, device="cuda")
+    moe.moe_add_rmsnorm(x.cuda(), None, w, 0.0, y)
+    assert torch.isnan(y[0, 5]) and (y[0, :5] == 0).all() and (y[0, 6:] == 0).all()  # inf / inf, and 1 / inf
+    assert torch.isnan(y[1]).all() and torch.isnan(y[2]).all()  # 0 / 0
+    ref = norm64(x[3:].cuda(), None, w, 0.0)
+    assert ((y[3:].to(F64) - ref).abs() <= (N.REL + 2.0 ** -24) * ref.abs() + 2.0 ** -149).all()
