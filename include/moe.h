@@ -371,7 +371,7 @@ MOE_API moe_status_t moe_add_rmsnorm(int64_t rows, int32_t d, int32_t dtype, flo
  * significant bits, nearest, ties to even (1 where that is below 2^-126); a code is
  * v / scale rounded to the nearest whole number, ties to even (-7 .. 7; -8 is valid on
  * input); the weight that a code stands for is code * scale, which for these scales is
- * exactly a bf16 number.
+ * exactly a bf16 number. (Symmetric: formats with zero points cannot be expressed.)
  *   codes  [n, rows, cols / 2] uint8: a row is a sequence of little-endian 32-bit words
  *          of 8 columns; column 2i of a word is held as code + 8 in bits 4i .. 4i+3 and
  *          column 2i + 1 in bits 16+4i .. 19+4i (i = 0 .. 3);

@@ -1,8 +1,8 @@
 // 4-bit expert weights: the internal interface of csrc/w4.cu.
 //
 // A matrix [R, K] is held as codes [R, K / 2] bytes and bf16 scales [ceil(K / G), R]
-// (group-major: a tile's rows are contiguous, so a few 16-byte copies fetch them). A row
-// is a sequence of 32-bit words of 8 columns; column 2i of a word sits in bits 4i..4i+3
+// (group-major: the scales of a tile's rows are one run a group, a box of the tensor map
+// that fetches them). A row is a sequence of 32-bit words of 8 columns; column 2i of a word sits in bits 4i..4i+3
 // and column 2i+1 in bits 16+4i..19+4i, so (word >> 4i) & 0x000F000F is the bf16 pair of
 // neighbouring columns that the tensor cores take, up to the exponent.
 #pragma once
@@ -62,7 +62,8 @@ struct W4Params {
   unsigned stall;  // test hook, 0 but for tests of the time limits (moe_debug_set_barrier_extra)
 };
 
-// Input rows of a tile (16 .. 192) for segments of at most T and on average avg_rows rows.
+// Input rows of a tile (16 .. 192; 192 stands for 224 where w4_deep says so) for segments of
+// at most T and on average avg_rows rows.
 int w4_pick_bn(long long T, double avg_rows);
 constexpr size_t w4_partial_floats(int bn) { return (size_t)W4_MAX_CTAS * 2 * bn * 128; }  // of one product
 size_t w4_partial_bytes(int bn);
