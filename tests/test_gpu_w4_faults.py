@@ -125,7 +125,7 @@ def test_a_call_cut_short_after_its_first_product_leaves_no_counters(rows, d, f)
 
 
 # rows of 3 segments, d, f: several tiles a block in every tile height (16, 32, 64, 128, 192, 224), a few chunks each
-STALLED = [(12, 288, 30720), (45, 288, 30720), (90, 288, 30720), (300, 288, 10240), (700, 288, 10240),
+STALLED = [(12, 288, 30752), (45, 288, 30752), (90, 288, 30752), (300, 288, 10240), (700, 288, 10240),
            (700, 4128, 2080)]
 
 
